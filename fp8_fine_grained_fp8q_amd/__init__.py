@@ -18,11 +18,22 @@ Backward pass (same E4M3 format):
     xq, sa, xqt, sat = fp8q_quantize_act_dual(x)        # tiles along K and along the tokens
     dw = fp8q_gemm_rowscaled(dyqt, sat_dy, xqt, sat)    # wgrad dW = dY^T X
 
+Training step of an MoE layer (the forward pass with values beside the codes, and back):
+    xs, offsets, token_row, _ = fp8q_moe_sort(topk_ids, x, e_begin, n_experts)   # values by expert
+    dys, dw = fp8q_moe_combine_backward(dy, expert_out, token_row, topk_w)
+    dgu, h = fp8q_swiglu_backward(gu, dh, want_h=True)
+    xq, sa, xqt, sat = fp8q_quantize_act_grouped(xs, offsets)    # rows, and token tiles per expert
+    dw = fp8q_grouped_gemm_rowscaled(dguqt, sat_dgu, xqt, sat, offsets, m_tot)   # dW[g] = dgu[g]^T xs[g]
+    dx = fp8q_moe_sort_backward(dxs, token_row)
+    plan = fp8q_adamw_plan(params, grads, m, v)                  # states in FP32 or in E4M3
+    fp8q_adamw(plan, lr=2e-4, step=1)
+
 Layouts: xq uint8 [M, K]; sa float32 [K/128, M]; wq uint8 [G, N, K]; sb float32
 [G, N/128, K/128]; C row-major [M, N].
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -36,12 +47,16 @@ FP8Q_OK = 0
 FP8Q_ERR_OFFSETS = -7  # grouped GEMM offsets rejected by the FP8Q_DEBUG check
 FP8Q_OUT_BF16 = 0
 FP8Q_OUT_F32 = 1
-ABI_VERSION = 7
+FP8Q_STATE_F32 = 0
+FP8Q_STATE_E4M3 = 1
+ABI_VERSION = 8
 
 EXPORTED = ("fp8q_quantize_act_1x128", "fp8q_quantize_w_128x128", "fp8q_gemm_blockscaled",
             "fp8q_grouped_gemm_blockscaled", "fp8q_quantize_w_128x128_t", "fp8q_quantize_act_dual",
             "fp8q_gemm_rowscaled", "fp8q_swiglu_quantize_act_1x128", "fp8q_quantize_per_tensor",
-            "fp8q_quantize_act_w", "fp8q_moe_dispatch", "fp8q_moe_combine", "fp8q_status_string",
+            "fp8q_quantize_act_w", "fp8q_moe_dispatch", "fp8q_moe_combine", "fp8q_moe_sort",
+            "fp8q_moe_sort_backward", "fp8q_moe_combine_backward", "fp8q_swiglu_backward",
+            "fp8q_quantize_act_grouped", "fp8q_grouped_gemm_rowscaled", "fp8q_adamw", "fp8q_status_string",
             "fp8q_abi_version")
 
 
@@ -49,6 +64,18 @@ class Fp8qError(RuntimeError):
     def __init__(self, status: int, what: str):
         super().__init__(f"{what}: {status_string(status)} (status {status})")
         self.status = status
+
+
+class _AdamwTensor(ctypes.Structure):
+    """fp8q_adamw_tensor of include/fp8q.h."""
+    _fields_ = [(name, ctypes.c_void_p) for name in ("p", "grad", "m", "v", "m_scale", "v_scale", "p_bf16")] + [
+        ("n", ctypes.c_int64)]
+
+
+class _AdamwHyper(ctypes.Structure):
+    """fp8q_adamw_hyper of include/fp8q.h."""
+    _fields_ = [(name, ctypes.c_double) for name in ("lr", "beta1", "beta2", "eps", "weight_decay", "grad_scale")] + [
+        ("step", ctypes.c_int64), ("scalars", ctypes.c_void_p)]
 
 
 _lib = None
@@ -76,10 +103,14 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.fp8q_quantize_act_w.argtypes = [vp, i64, vp, i64, i64, i64, vp, vp, vp, vp, vp]
     lib.fp8q_moe_dispatch.argtypes = [vp, i64, i64, i64, i64, vp, vp, i64, i64, vp, vp, vp, vp, vp, vp]
     lib.fp8q_moe_combine.argtypes = [vp, i32, i64, i64, vp, vp, i64, i64, vp, i32, vp]
-    for name in ("fp8q_quantize_act_1x128", "fp8q_quantize_w_128x128", "fp8q_gemm_blockscaled",
-                 "fp8q_grouped_gemm_blockscaled", "fp8q_quantize_w_128x128_t", "fp8q_quantize_act_dual",
-                 "fp8q_gemm_rowscaled", "fp8q_swiglu_quantize_act_1x128", "fp8q_quantize_per_tensor",
-                 "fp8q_quantize_act_w", "fp8q_moe_dispatch", "fp8q_moe_combine"):
+    lib.fp8q_moe_sort.argtypes = [vp, i64, i64, i64, i64, vp, i32, i64, i64, vp, vp, vp, vp, vp]
+    lib.fp8q_moe_sort_backward.argtypes = [vp, i32, i64, i64, vp, i64, i64, vp, i32, vp]
+    lib.fp8q_moe_combine_backward.argtypes = [vp, i32, vp, i32, i64, i64, vp, vp, i64, i64, vp, vp, vp]
+    lib.fp8q_swiglu_backward.argtypes = [vp, vp, i32, i64, i64, vp, vp, vp]
+    lib.fp8q_quantize_act_grouped.argtypes = [vp, vp, i64, i64, i64, vp, vp, vp, vp, vp]
+    lib.fp8q_grouped_gemm_rowscaled.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i64, vp, i32, vp]
+    lib.fp8q_adamw.argtypes = [ctypes.POINTER(_AdamwTensor), i64, i32, i32, ctypes.POINTER(_AdamwHyper), vp]
+    for name in EXPORTED:
         getattr(lib, name).restype = i32
     lib.fp8q_status_string.argtypes = [i32]
     lib.fp8q_status_string.restype = ctypes.c_char_p
@@ -117,6 +148,33 @@ def _need(t: torch.Tensor, dtype, name: str, shape=None):
         raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor")
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+@contextlib.contextmanager
+def _on(stream, *tensors):
+    """Checks that the tensors are on the current device, and makes `stream` the current one, so
+    that outputs allocated inside belong to the stream that writes them; yields its handle."""
+    device = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != device:
+            raise ValueError(f"tensors must be on the current device cuda:{device}, got {t.device}")
+    if stream is None:
+        yield torch.cuda.current_stream().cuda_stream
+        return
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(stream):
+        yield stream.cuda_stream
+
+
+def _need_rows(t, name: str, columns: int = 8, rows=None):
+    """A contiguous bf16 or float32 [rows, C] with C a multiple of `columns`."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"{name} must be a bfloat16 or float32 tensor")
+    _need(t, t.dtype, name)
+    if t.dim() != 2 or t.shape[1] % columns or (rows is not None and t.shape[0] != rows):
+        raise ValueError(f"{name} must be [{'rows' if rows is None else rows}, C] with C a multiple of {columns}, "
+                         f"got {tuple(t.shape)}")
 
 
 def fp8q_quantize_act_1x128(x: torch.Tensor, xq: torch.Tensor | None = None,
@@ -390,6 +448,236 @@ def tensor_stats(stats: torch.Tensor):
     return (float(h[0:1].view(torch.float32)), int(h[1]), float(h[2:3].view(torch.float32)))
 
 
+def fp8q_moe_sort(topk_ids: torch.Tensor, x: torch.Tensor, e_begin: int, n_experts: int, capacity: int | None = None,
+                  xs: torch.Tensor | None = None, row_token: torch.Tensor | None = None, stream=None):
+    """Rows of x (bf16 or float32 [T, H]) in expert order for the local experts [e_begin, e_begin
+    + n_experts): topk_ids int32 [T, k] -> (xs [capacity, H], offsets int32 [n_experts + 1],
+    token_row int32 [T, k], row_token int32 [capacity]), the maps as fp8q_moe_dispatch gives
+    them; capacity defaults to xs's rows, or to T*k.  Rows of xs and row_token behind the last
+    routed one are left as they were."""
+    _need(topk_ids, torch.int32, "topk_ids")
+    if topk_ids.dim() != 2:
+        raise ValueError("topk_ids must be 2-D [T, k]")
+    T, k = topk_ids.shape
+    _need_rows(x, "x", rows=T)
+    H = x.shape[1]
+    cap = int(capacity) if capacity is not None else (xs.shape[0] if xs is not None else T * k)
+    if cap < 0 or n_experts < 1:
+        raise ValueError("capacity must not be negative and n_experts must be positive")
+    with _on(stream, topk_ids, x, xs, row_token) as s:
+        xs = torch.empty((cap, H), dtype=x.dtype, device=x.device) if xs is None else xs
+        row_token = torch.empty(cap, dtype=torch.int32, device=x.device) if row_token is None else row_token
+        _need(xs, x.dtype, "xs", (cap, H))
+        _need(row_token, torch.int32, "row_token", (cap,))
+        offsets = torch.empty(n_experts + 1, dtype=torch.int32, device=x.device)
+        token_row = torch.empty((T, k), dtype=torch.int32, device=x.device)
+        _check(load_library().fp8q_moe_sort(_ptr(topk_ids), T, k, e_begin, n_experts, _ptr(x), _out_code(x.dtype), H, cap,
+                                            _ptr(xs), _ptr(offsets), _ptr(token_row), _ptr(row_token), s),
+               "fp8q_moe_sort")
+    return xs, offsets, token_row, row_token
+
+
+def fp8q_moe_sort_backward(dxs: torch.Tensor, token_row: torch.Tensor, dx: torch.Tensor | None = None,
+                           out_dtype=torch.bfloat16, stream=None):
+    """Gradient of the sort: dx[t] = sum over the token's rows of dxs[row] (dxs bf16 or float32
+    [capacity, H], token_row int32 [T, k]) -> dx [T, H] in out_dtype."""
+    _need_rows(dxs, "dxs")
+    _need(token_row, torch.int32, "token_row")
+    if token_row.dim() != 2:
+        raise ValueError("token_row must be 2-D [T, k]")
+    (T, k), (cap, H) = token_row.shape, dxs.shape
+    with _on(stream, dxs, token_row, dx) as s:
+        dx = torch.empty((T, H), dtype=out_dtype, device=dxs.device) if dx is None else dx
+        _need(dx, dx.dtype, "dx", (T, H))
+        _check(load_library().fp8q_moe_sort_backward(_ptr(dxs), _out_code(dxs.dtype), cap, H, _ptr(token_row), T, k,
+                                                     _ptr(dx), _out_code(dx.dtype), s), "fp8q_moe_sort_backward")
+    return dx
+
+
+def fp8q_moe_combine_backward(dy: torch.Tensor, expert_out: torch.Tensor, token_row: torch.Tensor,
+                              topk_w: torch.Tensor, dout: torch.Tensor | None = None, dw: torch.Tensor | None = None,
+                              stream=None):
+    """Gradients of fp8q_moe_combine: dy [T, N] and expert_out [capacity, N] (bf16 or float32
+    each), token_row int32 / topk_w float32 [T, k] -> (dout like expert_out with dout[row] =
+    topk_w[t, s] * dy[t], dw float32 [T, k] with dw[t, s] = <expert_out[row], dy[t]>).  Rows of
+    dout without a slot are left as they were; dw is 0 for slots without a row."""
+    _need(token_row, torch.int32, "token_row")
+    if token_row.dim() != 2:
+        raise ValueError("token_row must be 2-D [T, k]")
+    T, k = token_row.shape
+    _need_rows(dy, "dy", rows=T)
+    N = dy.shape[1]
+    _need_rows(expert_out, "expert_out")
+    if expert_out.shape[1] != N:
+        raise ValueError(f"expert_out must be [capacity, {N}], got {tuple(expert_out.shape)}")
+    _need(topk_w, torch.float32, "topk_w", (T, k))
+    with _on(stream, dy, expert_out, token_row, topk_w, dout, dw) as s:
+        dout = torch.empty_like(expert_out) if dout is None else dout
+        dw = torch.empty_like(topk_w) if dw is None else dw
+        _need(dout, expert_out.dtype, "dout", expert_out.shape)
+        _need(dw, torch.float32, "dw", (T, k))
+        _check(load_library().fp8q_moe_combine_backward(_ptr(dy), _out_code(dy.dtype), _ptr(expert_out),
+                                                        _out_code(expert_out.dtype), expert_out.shape[0], N,
+                                                        _ptr(token_row), _ptr(topk_w), T, k, _ptr(dout), _ptr(dw), s),
+               "fp8q_moe_combine_backward")
+    return dout, dw
+
+
+def fp8q_swiglu_backward(gu: torch.Tensor, dh: torch.Tensor, dgu: torch.Tensor | None = None,
+                         h: torch.Tensor | None = None, want_h: bool = False, stream=None):
+    """Gradient of h = SiLU(g) * u: gu bf16 [M, 2I] (g | u), dh bf16 or float32 [M, I] -> (dgu bf16
+    [M, 2I], h bf16 [M, I] if want_h or a buffer for it is given, else None)."""
+    _need(gu, torch.bfloat16, "gu")
+    if gu.dim() != 2 or gu.shape[1] % 16:
+        raise ValueError(f"gu must be [M, 2I] with I a multiple of 8, got {tuple(gu.shape)}")
+    M, I = gu.shape[0], gu.shape[1] // 2
+    _need_rows(dh, "dh", rows=M)
+    if dh.shape[1] != I:
+        raise ValueError(f"dh must be [{M}, {I}], got {tuple(dh.shape)}")
+    with _on(stream, gu, dh, dgu, h) as s:
+        dgu = torch.empty_like(gu) if dgu is None else dgu
+        h = torch.empty((M, I), dtype=torch.bfloat16, device=gu.device) if h is None and want_h else h
+        _need(dgu, torch.bfloat16, "dgu", (M, 2 * I))
+        if h is not None:
+            _need(h, torch.bfloat16, "h", (M, I))
+        _check(load_library().fp8q_swiglu_backward(_ptr(gu), _ptr(dh), _out_code(dh.dtype), M, I, _ptr(dgu), _ptr(h), s),
+               "fp8q_swiglu_backward")
+    return dgu, h
+
+
+def _grouped_columns(m_tot: int, groups: int) -> int:
+    return 128 * (m_tot // 128 + groups)
+
+
+def fp8q_quantize_act_grouped(x: torch.Tensor, offsets: torch.Tensor, rows: bool = True, xq=None, sa=None, xqt=None,
+                              sat=None, stream=None):
+    """x bf16 [M, K] sorted by expert, offsets int32 [G + 1] -> (xq uint8 [M, K], sa float32
+    [K/128, M], xqt uint8 [K, Mp], sat float32 [Mp/128, K]) with Mp = 128 (M // 128 + G): 1x128
+    tiles along K (None, None with rows=False) and tiles of 128 tokens of one expert."""
+    _need(x, torch.bfloat16, "x")
+    _need(offsets, torch.int32, "offsets")
+    if x.dim() != 2 or x.shape[1] % 128 or offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise ValueError(f"x must be [M, K] with K a multiple of 128 and offsets [G + 1], got {tuple(x.shape)} and "
+                         f"{tuple(offsets.shape)}")
+    (M, K), G = x.shape, offsets.shape[0] - 1
+    mp = _grouped_columns(M, G)
+    if not rows and (xq is not None or sa is not None):
+        raise ValueError("xq and sa are written with rows=True only")
+    with _on(stream, x, offsets, xq, sa, xqt, sat) as s:
+        if rows:
+            xq = torch.empty((M, K), dtype=torch.uint8, device=x.device) if xq is None else xq
+            sa = torch.empty((K // 128, M), dtype=torch.float32, device=x.device) if sa is None else sa
+            _need(xq, torch.uint8, "xq", (M, K))
+            _need(sa, torch.float32, "sa", (K // 128, M))
+        xqt = torch.empty((K, mp), dtype=torch.uint8, device=x.device) if xqt is None else xqt
+        sat = torch.empty((mp // 128, K), dtype=torch.float32, device=x.device) if sat is None else sat
+        _need(xqt, torch.uint8, "xqt", (K, mp))
+        _need(sat, torch.float32, "sat", (mp // 128, K))
+        _check(load_library().fp8q_quantize_act_grouped(_ptr(x), _ptr(offsets), G, M, K, _ptr(xq), _ptr(sa), _ptr(xqt),
+                                                        _ptr(sat), s), "fp8q_quantize_act_grouped")
+    return xq, sa, xqt, sat
+
+
+def fp8q_grouped_gemm_rowscaled(aq, sa, bq, sb, offsets, m_tot: int, out_dtype=torch.bfloat16,
+                                out: torch.Tensor | None = None, stream=None):
+    """The experts' weight gradients C [G, P, Q]: C[g] = dequant(aq, sa) @ dequant(bq, sb)^T over expert
+    g's token tiles; aq [P, Mp], sa [Mp/128, P], bq [Q, Mp], sb [Mp/128, Q] from
+    fp8q_quantize_act_grouped of tensors with m_tot rows and these offsets."""
+    _need(aq, torch.uint8, "aq")
+    _need(bq, torch.uint8, "bq")
+    _need(offsets, torch.int32, "offsets")
+    if aq.dim() != 2 or bq.dim() != 2 or offsets.dim() != 1 or offsets.shape[0] < 2 or m_tot < 0:
+        raise ValueError("aq must be [P, Mp], bq [Q, Mp] and offsets [G + 1]")
+    P, Q, G = aq.shape[0], bq.shape[0], offsets.shape[0] - 1
+    mp = _grouped_columns(int(m_tot), G)
+    _need(aq, torch.uint8, "aq", (P, mp))
+    _need(bq, torch.uint8, "bq", (Q, mp))
+    _need(sa, torch.float32, "sa", (mp // 128, P))
+    _need(sb, torch.float32, "sb", (mp // 128, Q))
+    with _on(stream, aq, sa, bq, sb, offsets, out) as s:
+        out = torch.empty((G, P, Q), dtype=out_dtype, device=aq.device) if out is None else out
+        _need(out, out.dtype, "out", (G, P, Q))
+        _check(load_library().fp8q_grouped_gemm_rowscaled(_ptr(aq), _ptr(sa), _ptr(bq), _ptr(sb), _ptr(offsets), G,
+                                                          int(m_tot), P, Q, _ptr(out), _out_code(out.dtype), s),
+               "fp8q_grouped_gemm_rowscaled")
+    return out
+
+
+class AdamwPlan:
+    """The tensors of an AdamW step, checked once (fp8q_adamw_plan makes it).  It holds them, so
+    their memory stays theirs as long as the plan lives; replacing a tensor's storage
+    (`tensor.data = ...`, `resize_`) needs a new plan."""
+
+    def __init__(self, tensors, descriptors, grad_dtype, state_dtype, device):
+        self.tensors, self.descriptors = tensors, descriptors
+        self.grad_dtype, self.state_dtype, self.device = grad_dtype, state_dtype, device
+
+
+def fp8q_adamw_plan(params, grads, m, v, m_scales=None, v_scales=None, copies=None) -> AdamwPlan:
+    """Lists of tensors, one entry per parameter, any shapes: params float32, grads bf16 or float32
+    (one type for all), states m and v float32, or uint8 with float32 m_scales / v_scales of
+    ceil(n / 128) entries each (E4M3 codes of m and of sqrt(v); zeros start a run); copies
+    bf16, written with the new parameters, or None.  All memory disjoint."""
+    lists = {"params": params, "grads": grads, "m": m, "v": v, "m_scales": m_scales, "v_scales": v_scales,
+             "copies": copies}
+    lists = {k: list(x) for k, x in lists.items() if x is not None}
+    count = len(lists["params"])
+    if any(len(x) != count for x in lists.values()):
+        raise ValueError(f"the lists must have {count} tensors each")
+    e4m3 = "m_scales" in lists
+    if e4m3 != ("v_scales" in lists):
+        raise ValueError("m_scales and v_scales go together")
+    grad = lists["grads"][0].dtype if count else torch.float32
+    if grad not in (torch.bfloat16, torch.float32):
+        raise ValueError("grads must be bfloat16 or float32")
+    state = torch.uint8 if e4m3 else torch.float32
+    types = {"params": torch.float32, "grads": grad, "m": state, "v": state, "m_scales": torch.float32,
+             "v_scales": torch.float32, "copies": torch.bfloat16}
+    table = (_AdamwTensor * max(count, 1))()
+    fields = {"params": "p", "grads": "grad", "m": "m", "v": "v", "m_scales": "m_scale", "v_scales": "v_scale",
+              "copies": "p_bf16"}
+    spans, devices = [], set()
+    for name, tensors in lists.items():
+        for i, t in enumerate(tensors):
+            _need(t, types[name], f"{name}[{i}]")
+            n = lists["params"][i].numel()
+            want = -(-n // 128) if name.endswith("scales") else n
+            if t.numel() != want:
+                raise ValueError(f"{name}[{i}] must have {want} elements, got {t.numel()}")
+            if n and t.data_ptr() % (4 if name.endswith("scales") else 16):
+                raise ValueError(f"{name}[{i}] must be {4 if name.endswith('scales') else 16}-byte aligned")
+            setattr(table[i], fields[name], t.data_ptr() if n else None)
+            table[i].n = n
+            devices.add(t.device)
+            if n:
+                spans.append((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), f"{name}[{i}]"))
+    spans.sort()
+    for a, b in zip(spans, spans[1:]):
+        if b[0] < a[1]:
+            raise ValueError(f"{a[2]} and {b[2]} share memory")
+    if len(devices) > 1:
+        raise ValueError("all tensors must be on one device")
+    return AdamwPlan(lists, table, _out_code(grad), FP8Q_STATE_E4M3 if e4m3 else FP8Q_STATE_F32,
+                     devices.pop() if devices else None)
+
+
+def fp8q_adamw(plan: AdamwPlan, lr: float, betas=(0.9, 0.95), eps: float = 1e-8, weight_decay: float = 0.0, step: int = 1,
+               grad_scale: float = 1.0, scalars: torch.Tensor | None = None, stream=None) -> None:
+    """One AdamW step over the plan's tensors, in place.  `step` counts from 1.  `scalars`: a device
+    float32 [4] holding {lr, 1 - beta1^step, 1 - beta2^step, grad_scale}, read by the kernels in
+    place of those arguments (a captured step is replayed with new values in it)."""
+    if not isinstance(plan, AdamwPlan):
+        raise ValueError("plan must come from fp8q_adamw_plan")
+    if scalars is not None:
+        _need(scalars, torch.float32, "scalars", (4,))
+    if plan.device is None:
+        return
+    hyper = _AdamwHyper(lr, betas[0], betas[1], eps, weight_decay, grad_scale, step, _ptr(scalars) or None)
+    with _on(stream, plan.tensors["params"][0], scalars) as s:
+        _check(load_library().fp8q_adamw(plan.descriptors, len(plan.tensors["params"]), plan.grad_dtype, plan.state_dtype,
+                                         ctypes.byref(hyper), s), "fp8q_adamw")
+
+
 quantize_act_1x128 = fp8q_quantize_act_1x128
 quantize_w_128x128 = fp8q_quantize_w_128x128
 gemm_blockscaled = fp8q_gemm_blockscaled
@@ -399,3 +687,11 @@ quantize_act_dual = fp8q_quantize_act_dual
 gemm_rowscaled = fp8q_gemm_rowscaled
 swiglu_quantize_act_1x128 = fp8q_swiglu_quantize_act_1x128
 quantize_per_tensor = fp8q_quantize_per_tensor
+moe_sort = fp8q_moe_sort
+moe_sort_backward = fp8q_moe_sort_backward
+moe_combine_backward = fp8q_moe_combine_backward
+swiglu_backward = fp8q_swiglu_backward
+quantize_act_grouped = fp8q_quantize_act_grouped
+grouped_gemm_rowscaled = fp8q_grouped_gemm_rowscaled
+adamw_plan = fp8q_adamw_plan
+adamw = fp8q_adamw

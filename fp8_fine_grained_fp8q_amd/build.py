@@ -19,7 +19,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libfp8q.so")
-SOURCES = ["quant.hip", "gemm.hip", "moe.hip", "fp8q_abi.cpp"]
+SOURCES = ["quant.hip", "gemm.hip", "moe.hip", "swiglu.hip", "wgrad.hip", "adamw.hip", "fp8q_abi.cpp"]
 # Streaming-bandwidth and unit-rate probes the kernels are read against (not part of the path).
 PROBE_LIB = os.path.join(HERE, "libfp8q_probe.so")
 PROBE_SOURCES = ["stream_probe.hip", "unit_probe.hip"]

@@ -3,6 +3,7 @@
 #include "fp8q.h"
 
 #include <hip/hip_runtime.h>
+#include <math.h>
 #include <stdlib.h>
 
 #include <mutex>
@@ -34,6 +35,21 @@ hipStream_t as_stream(void *s) { return static_cast<hipStream_t>(s); }
 bool debug_checks() {
   const char *v = getenv("FP8Q_DEBUG");
   return v != nullptr && v[0] != '\0' && !(v[0] == '0' && v[1] == '\0');
+}
+
+bool bad_dtype(int32_t d) { return d != FP8Q_OUT_BF16 && d != FP8Q_OUT_F32; }
+
+// Columns of the grouped token tiles of M rows on G experts; 0 where they exceed what the
+// kernels address (2^22).
+int64_t grouped_columns(int64_t M, int64_t G) {
+  const int64_t mp = 128 * (M / 128 + G);
+  return mp <= kMaxGemmK ? mp : 0;
+}
+
+// Shared checks of the token maps [T][k] and of rows of `width` columns.
+bool bad_rows(int64_t T, int64_t k, int64_t capacity, int64_t width) {
+  return bad_dim(T) || k < 1 || k > 64 || bad_dim(width) || width % 8 != 0 || bad_dim(capacity) || too_many(T, k) ||
+         T * k >= kMaxDim || too_many(capacity, width) || too_many(T, width);
 }
 
 // Shared checks of the two GEMM entry points (everything except the grouped extras).
@@ -224,16 +240,142 @@ fp8q_status fp8q_moe_combine(const void *expert_out, int32_t in_dtype, int64_t c
                                            topk_weights, T, k, y, out_dtype == FP8Q_OUT_F32, as_stream(stream)));
 }
 
+fp8q_status fp8q_moe_sort(const int32_t *topk_ids, int64_t T, int64_t k, int64_t e_begin, int64_t E, const void *x,
+                          int32_t dtype, int64_t H, int64_t capacity, void *xs, int32_t *offsets, int32_t *token_row,
+                          int32_t *row_token, void *stream) {
+  if (bad_dtype(dtype)) return FP8Q_ERR_DTYPE;
+  if (bad_rows(T, k, capacity, H) || E < 1 || E > 1024 || e_begin < 0 || bad_dim(e_begin)) return FP8Q_ERR_SHAPE;
+  if (too_many(T, (H + 1023) / 1024) || T * ((H + 1023) / 1024) >= kMaxDim) return FP8Q_ERR_SHAPE;
+  if (!offsets || (T > 0 && (!topk_ids || !token_row)) || (T > 0 && H > 0 && !x) ||
+      (capacity > 0 && ((H > 0 && !xs) || !row_token)))
+    return FP8Q_ERR_NULL;
+  if (misaligned(topk_ids, 4) || misaligned(offsets, 4) || misaligned(token_row, 4) || misaligned(row_token, 4) ||
+      misaligned(x) || misaligned(xs))
+    return FP8Q_ERR_ALIGN;
+  if (device_ok() != FP8Q_OK) return FP8Q_ERR_DEVICE;
+  return launched(fp8q::launch_moe_sort(topk_ids, T, k, e_begin, E, x, dtype == FP8Q_OUT_F32, H, capacity, xs, offsets,
+                                        token_row, row_token, as_stream(stream)));
+}
+
+fp8q_status fp8q_moe_sort_backward(const void *dxs, int32_t in_dtype, int64_t capacity, int64_t H,
+                                   const int32_t *token_row, int64_t T, int64_t k, void *dx, int32_t out_dtype,
+                                   void *stream) {
+  if (bad_dtype(in_dtype) || bad_dtype(out_dtype)) return FP8Q_ERR_DTYPE;
+  if (bad_rows(T, k, capacity, H)) return FP8Q_ERR_SHAPE;
+  if (too_many(T, (H + 1023) / 1024) || T * ((H + 1023) / 1024) >= kMaxDim) return FP8Q_ERR_SHAPE;
+  if (T == 0 || H == 0) return FP8Q_OK;
+  if (!token_row || !dx || (capacity > 0 && !dxs)) return FP8Q_ERR_NULL;
+  if (misaligned(token_row, 4) || misaligned(dx) || misaligned(dxs)) return FP8Q_ERR_ALIGN;
+  if (device_ok() != FP8Q_OK) return FP8Q_ERR_DEVICE;
+  return launched(fp8q::launch_moe_sort_backward(dxs, in_dtype == FP8Q_OUT_F32, capacity, H, token_row, T, k, dx,
+                                                 out_dtype == FP8Q_OUT_F32, as_stream(stream)));
+}
+
+fp8q_status fp8q_moe_combine_backward(const void *dy, int32_t dy_dtype, const void *expert_out, int32_t dtype,
+                                      int64_t capacity, int64_t N, const int32_t *token_row,
+                                      const float *topk_weights, int64_t T, int64_t k, void *dout, float *dw,
+                                      void *stream) {
+  if (bad_dtype(dy_dtype) || bad_dtype(dtype)) return FP8Q_ERR_DTYPE;
+  if (bad_rows(T, k, capacity, N)) return FP8Q_ERR_SHAPE;
+  if (T == 0) return FP8Q_OK;
+  if (!token_row || !topk_weights || !dw || (N > 0 && (!dy || (capacity > 0 && (!expert_out || !dout)))))
+    return FP8Q_ERR_NULL;
+  if (misaligned(token_row, 4) || misaligned(topk_weights, 4) || misaligned(dw, 4) || misaligned(dy) ||
+      misaligned(expert_out) || misaligned(dout))
+    return FP8Q_ERR_ALIGN;
+  if (device_ok() != FP8Q_OK) return FP8Q_ERR_DEVICE;
+  return launched(fp8q::launch_moe_combine_backward(dy, dy_dtype == FP8Q_OUT_F32, expert_out, dtype == FP8Q_OUT_F32,
+                                                    capacity, N, token_row, topk_weights, T, k, dout, dw,
+                                                    as_stream(stream)));
+}
+
+fp8q_status fp8q_swiglu_backward(const uint16_t *gu_bf16, const void *dh, int32_t dh_dtype, int64_t M, int64_t I,
+                                 uint16_t *dgu_bf16, uint16_t *h_bf16, void *stream) {
+  if (bad_dtype(dh_dtype)) return FP8Q_ERR_DTYPE;
+  if (bad_dim(M) || bad_dim(I) || I % 8 != 0 || too_many(M, 2 * I)) return FP8Q_ERR_SHAPE;
+  if (M * (I / 8) > int64_t(256) * 0x7fffffff) return FP8Q_ERR_SHAPE;  // workgroups of 256 threads
+  if (M == 0 || I == 0) return FP8Q_OK;
+  if (!gu_bf16 || !dh || !dgu_bf16) return FP8Q_ERR_NULL;
+  if (misaligned(gu_bf16) || misaligned(dh) || misaligned(dgu_bf16) || misaligned(h_bf16)) return FP8Q_ERR_ALIGN;
+  if (device_ok() != FP8Q_OK) return FP8Q_ERR_DEVICE;
+  return launched(fp8q::launch_swiglu_backward(gu_bf16, dh, dh_dtype == FP8Q_OUT_F32, M, I, dgu_bf16, h_bf16,
+                                               as_stream(stream)));
+}
+
+fp8q_status fp8q_quantize_act_grouped(const uint16_t *x_bf16, const int32_t *offsets, int64_t G, int64_t M_tot,
+                                      int64_t K, uint8_t *xq, float *sa, uint8_t *xqt, float *sat, void *stream) {
+  if (G < 1 || bad_dim(G) || bad_dim(M_tot) || bad_dim(K) || K % 128 != 0 || too_many(M_tot, K))
+    return FP8Q_ERR_SHAPE;
+  const int64_t Mp = grouped_columns(M_tot, G);
+  if (Mp == 0 || (Mp / 128) * (K / 128) >= kMaxDim) return FP8Q_ERR_SHAPE;
+  if (M_tot == 0 || K == 0) return FP8Q_OK;
+  if (!x_bf16 || !offsets || !xqt || !sat || !xq != !sa) return FP8Q_ERR_NULL;
+  if (misaligned(x_bf16) || misaligned(offsets, 4) || misaligned(xq) || misaligned(sa) || misaligned(xqt) ||
+      misaligned(sat))
+    return FP8Q_ERR_ALIGN;
+  if (device_ok() != FP8Q_OK) return FP8Q_ERR_DEVICE;
+  return launched(fp8q::launch_quant_act_grouped(x_bf16, offsets, G, M_tot, K, Mp, xq, sa, xqt, sat,
+                                                 as_stream(stream)));
+}
+
+fp8q_status fp8q_grouped_gemm_rowscaled(const uint8_t *aq, const float *sa, const uint8_t *bq, const float *sb,
+                                        const int32_t *offsets, int64_t G, int64_t M_tot, int64_t P, int64_t Q,
+                                        void *c, int32_t out_dtype, void *stream) {
+  if (bad_dtype(out_dtype)) return FP8Q_ERR_DTYPE;
+  if (G < 1 || bad_dim(G) || bad_dim(M_tot) || bad_dim(P) || bad_dim(Q) || P % 128 != 0 || Q % 128 != 0)
+    return FP8Q_ERR_SHAPE;
+  if (too_many(G, P) || too_many(G * P, Q)) return FP8Q_ERR_SHAPE;
+  const int64_t Mp = grouped_columns(M_tot, G);
+  if (Mp == 0 || too_many(G * (P / 128), Q / 128) || G * (P / 128) * (Q / 128) >= kMaxDim) return FP8Q_ERR_SHAPE;
+  if (P == 0 || Q == 0) return FP8Q_OK;
+  if (!c || !offsets || (M_tot > 0 && (!aq || !sa || !bq || !sb))) return FP8Q_ERR_NULL;
+  if (misaligned(aq) || misaligned(sa) || misaligned(bq) || misaligned(sb) || misaligned(offsets, 4) || misaligned(c))
+    return FP8Q_ERR_ALIGN;
+  if (device_ok() != FP8Q_OK) return FP8Q_ERR_DEVICE;
+  return launched(fp8q::launch_grouped_gemm_rowscaled(aq, sa, bq, sb, offsets, G, M_tot, Mp, P, Q, c,
+                                                      out_dtype == FP8Q_OUT_F32, as_stream(stream)));
+}
+
+fp8q_status fp8q_adamw(const fp8q_adamw_tensor *tensors, int64_t count, int32_t grad_dtype, int32_t state_dtype,
+                       const fp8q_adamw_hyper *hyper, void *stream) {
+  if (bad_dtype(grad_dtype) || (state_dtype != FP8Q_STATE_F32 && state_dtype != FP8Q_STATE_E4M3))
+    return FP8Q_ERR_DTYPE;
+  if (bad_dim(count)) return FP8Q_ERR_SHAPE;
+  if (!hyper || (count > 0 && !tensors)) return FP8Q_ERR_NULL;
+  const fp8q_adamw_hyper &h = *hyper;
+  const double numbers[] = {h.lr, h.beta1, h.beta2, h.eps, h.weight_decay, h.grad_scale};
+  for (double v : numbers)
+    if (!isfinite(v)) return FP8Q_ERR_VALUE;
+  if (h.beta1 < 0 || h.beta1 >= 1 || h.beta2 < 0 || h.beta2 >= 1 || h.eps < 0 || h.step < 1) return FP8Q_ERR_VALUE;
+  const bool e4m3 = state_dtype == FP8Q_STATE_E4M3;
+  bool work = false;
+  for (int64_t i = 0; i < count; ++i) {
+    const fp8q_adamw_tensor &t = tensors[i];
+    if (t.n < 0 || t.n >= (int64_t(1) << 40)) return FP8Q_ERR_SHAPE;
+    if (t.n == 0) continue;
+    if (!t.p || !t.grad || !t.m || !t.v || (e4m3 && (!t.m_scale || !t.v_scale))) return FP8Q_ERR_NULL;
+    if (misaligned(t.p) || misaligned(t.grad) || misaligned(t.m) || misaligned(t.v) || misaligned(t.p_bf16) ||
+        (e4m3 && (misaligned(t.m_scale, 4) || misaligned(t.v_scale, 4))))
+      return FP8Q_ERR_ALIGN;
+    work = true;
+  }
+  if (misaligned(h.scalars, 4)) return FP8Q_ERR_ALIGN;
+  if (!work) return FP8Q_OK;
+  if (device_ok() != FP8Q_OK) return FP8Q_ERR_DEVICE;
+  return launched(fp8q::launch_adamw(tensors, count, grad_dtype == FP8Q_OUT_F32, e4m3, h, as_stream(stream)));
+}
+
 const char *fp8q_status_string(fp8q_status status) {
   switch (status) {
     case FP8Q_OK: return "ok";
     case FP8Q_ERR_NULL: return "null pointer argument";
     case FP8Q_ERR_SHAPE: return "invalid shape (negative, K/N (or M for the dual quantizer) not a multiple of 128, G < 1, or too large)";
     case FP8Q_ERR_ALIGN: return "misaligned pointer (16-byte alignment required; offsets 4-byte)";
-    case FP8Q_ERR_DTYPE: return "invalid out_dtype";
+    case FP8Q_ERR_DTYPE: return "invalid dtype argument";
     case FP8Q_ERR_DEVICE: return "no usable HIP device";
     case FP8Q_ERR_LAUNCH: return "kernel launch failed";
     case FP8Q_ERR_OFFSETS: return "grouped GEMM offsets invalid (offsets[0] != 0, decreasing, or offsets[G] != M_tot)";
+    case FP8Q_ERR_VALUE: return "hyperparameter out of range (not finite, beta outside [0, 1), eps < 0 or step < 1)";
     default: return "unknown status";
   }
 }

@@ -154,4 +154,44 @@ __device__ __forceinline__ float absmax8(const uint4 v) {
   return m;
 }
 
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+// Two FP32 values as BF16 in a dword (gfx950's conversion: round to nearest even, NaN kept).
+__device__ __forceinline__ uint32_t pack2_bf16(float lo, float hi) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
+}
+
+// Eight FP32 values as BF16 in one 16-byte chunk.
+__device__ __forceinline__ uint4 pack8_bf16(const float (&v)[8]) {
+  return make_uint4(pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3]), pack2_bf16(v[4], v[5]), pack2_bf16(v[6], v[7]));
+}
+
+// Eight FP32 values from element `off` of an FP32 or BF16 array (16-byte aligned chunks).
+template <bool kF32>
+__device__ __forceinline__ void load8(const void *p, int64_t off, float (&v)[8]) {
+  if (kF32) {
+    const float4 a = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + off);
+    const float4 b = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + off + 4);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  } else {
+    const uint4 u = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + off);
+    v[0] = bf16_lo(u.x); v[1] = bf16_hi(u.x); v[2] = bf16_lo(u.y); v[3] = bf16_hi(u.y);
+    v[4] = bf16_lo(u.z); v[5] = bf16_hi(u.z); v[6] = bf16_lo(u.w); v[7] = bf16_hi(u.w);
+  }
+}
+
+// Eight FP32 values to element `off` of an FP32 or BF16 array.
+template <bool kF32>
+__device__ __forceinline__ void store8(void *p, int64_t off, const float (&v)[8]) {
+  if (kF32) {
+    float *o = static_cast<float *>(p) + off;
+    *reinterpret_cast<float4 *>(o) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4 *>(o + 4) = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + off) = pack8_bf16(v);
+  }
+}
+
 }  // namespace fp8q

@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "fp8q.h"
+
 namespace fp8q {
 
 // Compute units of the current device (cached per device; 256 if the query fails).
@@ -61,5 +63,39 @@ hipError_t launch_moe_dispatch(const int32_t *ids, int64_t T, int64_t k, int64_t
 // y[t] = sum over slots s with 0 <= token_row[t][s] < cap of w[t][s] * out[token_row[t][s]].
 hipError_t launch_moe_combine(const void *out, bool in_f32, int64_t cap, int64_t N, const int32_t *token_row,
                               const float *w, int64_t T, int64_t k, void *y, bool out_f32, hipStream_t stream);
+
+// The dispatch's routing with values in place of codes: xs[token_row[t][s]] = x[t], rows of H
+// BF16 or FP32 values.
+hipError_t launch_moe_sort(const int32_t *ids, int64_t T, int64_t k, int64_t e_begin, int64_t E, const void *x,
+                           bool f32, int64_t H, int64_t cap, void *xs, int32_t *offsets, int32_t *token_row,
+                           int32_t *row_token, hipStream_t stream);
+
+// dx[t] = sum over slots s with 0 <= token_row[t][s] < cap of dxs[token_row[t][s]].
+hipError_t launch_moe_sort_backward(const void *dxs, bool in_f32, int64_t cap, int64_t H, const int32_t *token_row,
+                                    int64_t T, int64_t k, void *dx, bool out_f32, hipStream_t stream);
+
+// Gradients of launch_moe_combine: dout[row] = w[t][s] * dy[t], dw[t][s] = <out[row], dy[t]>.
+hipError_t launch_moe_combine_backward(const void *dy, bool dy_f32, const void *out, bool f32, int64_t cap, int64_t N,
+                                       const int32_t *token_row, const float *w, int64_t T, int64_t k, void *dout,
+                                       float *dw, hipStream_t stream);
+
+// dgu = gradient of h = SiLU(g) * u (layout of gu); h itself too unless null.
+hipError_t launch_swiglu_backward(const uint16_t *gu, const void *dh, bool dh_f32, int64_t M, int64_t I,
+                                  uint16_t *dgu, uint16_t *h, hipStream_t stream);
+
+// Token tiles of expert-sorted rows, none across two experts: xqt[K][Mp], sat[Mp/128][K], Mp =
+// 128 (M / 128 + G); the rows' 1x128 codes xq[M][K], sa[K/128][M] too unless xq is null.
+hipError_t launch_quant_act_grouped(const uint16_t *x, const int32_t *offsets, int64_t G, int64_t M, int64_t K,
+                                    int64_t Mp, uint8_t *xq, float *sa, uint8_t *xqt, float *sat,
+                                    hipStream_t stream);
+
+// C[g] = dequant(aq, sa) dequant(bq, sb)^T over expert g's token tiles.
+hipError_t launch_grouped_gemm_rowscaled(const uint8_t *aq, const float *sa, const uint8_t *bq, const float *sb,
+                                         const int32_t *offsets, int64_t G, int64_t M, int64_t Mp, int64_t P,
+                                         int64_t Q, void *c, bool out_f32, hipStream_t stream);
+
+// One AdamW step over `count` tensors (host array).
+hipError_t launch_adamw(const fp8q_adamw_tensor *tensors, int64_t count, bool grad_f32, bool e4m3,
+                        const fp8q_adamw_hyper &hyper, hipStream_t stream);
 
 }  // namespace fp8q

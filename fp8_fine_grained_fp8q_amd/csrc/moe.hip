@@ -14,9 +14,12 @@
 //     after it, and the payload is the FP8 codes plus 4 bytes per 128 of them);
 //   * combine: y[t] = sum over the token's local slots s of w[t, s] * out[row(t, s)], FP32
 //     accumulation in slot order.
+//   * sort: the same route with BF16 or FP32 rows in place of codes (the weight gradient
+//     quantizes them along the tokens), and the gradients of the sort and of the combine.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "fp8q_device.h"
 #include "fp8q_launch.h"
 
 namespace fp8q {
@@ -228,24 +231,6 @@ __global__ __launch_bounds__(256) void moe_pack_kernel(const uint8_t *__restrict
   for (int64_t kb = lane; kb < K / 128; kb += 64) sa_s[kb * cap + r] = sa[kb * T + t];
 }
 
-template <bool kInF32>
-__device__ __forceinline__ void load8(const void *p, int64_t off, float (&v)[8]) {
-  if (kInF32) {
-    const float4 a = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + off);
-    const float4 b = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + off + 4);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  } else {
-    const uint4 u = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + off);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  }
-}
-
 // One workgroup per token; each thread takes 8 consecutive columns at a time.  The slots
 // are visited in order and each adds w * out[row] with one FMA per element.
 template <bool kInF32, bool kOutF32>
@@ -282,13 +267,100 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const void *__restrict
   }
 }
 
-hipError_t launch_moe_dispatch(const int32_t *ids, int64_t T, int64_t k, int64_t e_begin, int64_t E,
-                               const uint8_t *xq, const float *sa, int64_t K, int64_t cap, uint8_t *xq_s,
-                               float *sa_s, int32_t *offsets, int32_t *token_row, int32_t *row_token,
-                               hipStream_t stream) {
-  if (E < 1 || E > kMaxLocalExperts || (cap + 3) / 4 > 0x7fffffff) return hipErrorInvalidValue;
+// The rows of token t, one per lane: lane s < k holds token_row[t][s] if that is a row of the
+// sorted layout (0 <= row < cap); the set of such lanes is returned.  One coalesced load
+// serves all k slots, and the loops below run over the slots that have a row only.
+__device__ __forceinline__ uint64_t token_rows(const int32_t *__restrict__ token_row, int64_t t, int k, int64_t cap,
+                                               int32_t &row) {
+  const int lane = threadIdx.x & 63;
+  row = lane < k ? token_row[t * k + lane] : -1;
+  return __ballot(row >= 0 && row < cap);
+}
+
+// Sorted rows (the values a weight gradient needs, where the dispatch carries codes):
+// xs[token_row[t][s]] = x[t].  Driven by the tokens, so that each token's row is read once
+// however many local experts it has; a workgroup takes 256 16-byte chunks of one token.
+__global__ __launch_bounds__(256) void moe_spread_kernel(const uint4 *__restrict__ x, int64_t chunks, int64_t segs,
+                                                         const int32_t *__restrict__ token_row, int k, int64_t cap,
+                                                         uint4 *__restrict__ xs) {
+  const int64_t t = blockIdx.x / segs;
+  const int64_t c = (blockIdx.x % segs) * 256 + threadIdx.x;
+  int32_t row;
+  uint64_t todo = token_rows(token_row, t, k, cap, row);
+  if (todo == 0 || c >= chunks) return;
+  const uint4 v = x[t * chunks + c];
+  for (; todo != 0; todo &= todo - 1) {
+    const int64_t r = __builtin_amdgcn_readlane(row, __ffsll(static_cast<unsigned long long>(todo)) - 1);
+    xs[r * chunks + c] = v;
+  }
+}
+
+// Gradient of the sort: dx[t] = sum over the token's slots with a row of dxs[row], FP32, in
+// slot order, rounded once.  A workgroup takes 256 chunks of 8 columns of one token.
+template <bool kInF32, bool kOutF32>
+__global__ __launch_bounds__(256) void moe_sum_kernel(const void *__restrict__ dxs, int64_t H, int64_t segs,
+                                                      const int32_t *__restrict__ token_row, int k, int64_t cap,
+                                                      void *__restrict__ dx) {
+  const int64_t t = blockIdx.x / segs;
+  const int64_t c = (blockIdx.x % segs) * 256 + threadIdx.x;
+  int32_t row;
+  uint64_t todo = token_rows(token_row, t, k, cap, row);
+  if (c >= H / 8) return;
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (; todo != 0; todo &= todo - 1) {
+    const int64_t r = __builtin_amdgcn_readlane(row, __ffsll(static_cast<unsigned long long>(todo)) - 1);
+    float v[8];
+    load8<kInF32>(dxs, r * H + 8 * c, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] += v[i];
+  }
+  store8<kOutF32>(dx, t * H + 8 * c, acc);
+}
+
+// Gradient of the combine, one wave per (token, slot): dout[row] = w * dy[t] in the expert
+// outputs' type and dw = <out[row], dy[t]>, FP32 (each lane sums its columns in order, then
+// a fixed tree over the lanes: the same bits in every run).  A slot without a row gets
+// dw = 0.  The waves of a token share a workgroup or sit in neighbouring ones, so dy comes
+// from the caches after its first read.
+template <bool kF32, bool kDyF32>
+__global__ __launch_bounds__(256) void moe_combine_backward_kernel(const void *__restrict__ dy,
+                                                                   const void *__restrict__ out, int64_t N,
+                                                                   const int32_t *__restrict__ token_row,
+                                                                   const float *__restrict__ w, int64_t n, int k,
+                                                                   int64_t cap, void *__restrict__ dout,
+                                                                   float *__restrict__ dw) {
+  const int lane = threadIdx.x & 63;
+  const int64_t entry = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  if (entry >= n) return;
+  const int64_t r = token_row[entry];
+  float sum = 0.0f;
+  if (r >= 0 && r < cap) {
+    const int64_t t = entry / k;
+    const float ws = w[entry];
+    for (int64_t c = lane; c < N / 8; c += 64) {
+      float d[8], o[8];
+      load8<kDyF32>(dy, t * N + 8 * c, d);
+      load8<kF32>(out, r * N + 8 * c, o);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        sum = __builtin_fmaf(o[i], d[i], sum);
+        d[i] *= ws;
+      }
+      store8<kF32>(dout, r * N + 8 * c, d);
+    }
+#pragma unroll
+    for (int m = 32; m >= 1; m >>= 1) sum += __shfl_xor(sum, m);
+  }
+  if (lane == 0) dw[entry] = sum;
+}
+
+namespace {
+
+// The routing launches shared by the dispatch and the sort: offsets, token_row, row_token.
+hipError_t launch_route(const int32_t *ids, int64_t T, int64_t k, int64_t e_begin, int64_t E, int64_t cap,
+                        int32_t *offsets, int32_t *token_row, int32_t *row_token, hipStream_t stream) {
   const int64_t n = T * k, C = n / kChunk > 1 ? n / kChunk : 1;
-  if (C > 0x7fffffff) return hipErrorInvalidValue;
+  if (E < 1 || E > kMaxLocalExperts || C > 0x7fffffff) return hipErrorInvalidValue;
   const int kk = static_cast<int>(k), EE = static_cast<int>(E);
   if (C > 1) {
     hipLaunchKernelGGL(moe_count_kernel, dim3(static_cast<uint32_t>(C)), dim3(kRouteThreads), 0, stream, ids, n, C,
@@ -297,10 +369,64 @@ hipError_t launch_moe_dispatch(const int32_t *ids, int64_t T, int64_t k, int64_t
   }
   hipLaunchKernelGGL(moe_rank_kernel, dim3(static_cast<uint32_t>(C)), dim3(kRouteThreads), 0, stream, ids, n, C, kk,
                      e_begin, EE, cap, offsets, token_row, row_token);
-  hipError_t e = hipGetLastError();
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_moe_dispatch(const int32_t *ids, int64_t T, int64_t k, int64_t e_begin, int64_t E,
+                               const uint8_t *xq, const float *sa, int64_t K, int64_t cap, uint8_t *xq_s,
+                               float *sa_s, int32_t *offsets, int32_t *token_row, int32_t *row_token,
+                               hipStream_t stream) {
+  if ((cap + 3) / 4 > 0x7fffffff) return hipErrorInvalidValue;
+  hipError_t e = launch_route(ids, T, k, e_begin, E, cap, offsets, token_row, row_token, stream);
   if (e != hipSuccess || cap == 0) return e;
   hipLaunchKernelGGL(moe_pack_kernel, dim3(static_cast<uint32_t>((cap + 3) / 4)), dim3(256), 0, stream, xq, sa, T,
                      K, row_token, offsets, static_cast<int>(E), cap, xq_s, sa_s);
+  return hipGetLastError();
+}
+
+hipError_t launch_moe_sort(const int32_t *ids, int64_t T, int64_t k, int64_t e_begin, int64_t E, const void *x,
+                           bool f32, int64_t H, int64_t cap, void *xs, int32_t *offsets, int32_t *token_row,
+                           int32_t *row_token, hipStream_t stream) {
+  const int64_t chunks = H / (f32 ? 4 : 8), segs = (chunks + 255) / 256;
+  if (T * segs > 0x7fffffff) return hipErrorInvalidValue;
+  hipError_t e = launch_route(ids, T, k, e_begin, E, cap, offsets, token_row, row_token, stream);
+  if (e != hipSuccess || cap == 0 || T * segs == 0) return e;
+  hipLaunchKernelGGL(moe_spread_kernel, dim3(static_cast<uint32_t>(T * segs)), dim3(256), 0, stream,
+                     static_cast<const uint4 *>(x), chunks, segs, token_row, static_cast<int>(k), cap,
+                     static_cast<uint4 *>(xs));
+  return hipGetLastError();
+}
+
+hipError_t launch_moe_sort_backward(const void *dxs, bool in_f32, int64_t cap, int64_t H, const int32_t *token_row,
+                                    int64_t T, int64_t k, void *dx, bool out_f32, hipStream_t stream) {
+  const int64_t segs = (H / 8 + 255) / 256;
+  if (T * segs > 0x7fffffff) return hipErrorInvalidValue;
+  const dim3 grid(static_cast<uint32_t>(T * segs)), block(256);
+  const int kk = static_cast<int>(k);
+  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, dxs, H, segs, token_row, kk, cap, dx); };
+  if (in_f32)
+    out_f32 ? go(moe_sum_kernel<true, true>) : go(moe_sum_kernel<true, false>);
+  else
+    out_f32 ? go(moe_sum_kernel<false, true>) : go(moe_sum_kernel<false, false>);
+  return hipGetLastError();
+}
+
+hipError_t launch_moe_combine_backward(const void *dy, bool dy_f32, const void *out, bool f32, int64_t cap, int64_t N,
+                                       const int32_t *token_row, const float *w, int64_t T, int64_t k, void *dout,
+                                       float *dw, hipStream_t stream) {
+  const int64_t n = T * k;
+  if ((n + 3) / 4 > 0x7fffffff) return hipErrorInvalidValue;
+  const dim3 grid(static_cast<uint32_t>((n + 3) / 4)), block(256);
+  const int kk = static_cast<int>(k);
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, block, 0, stream, dy, out, N, token_row, w, n, kk, cap, dout, dw);
+  };
+  if (f32)
+    dy_f32 ? go(moe_combine_backward_kernel<true, true>) : go(moe_combine_backward_kernel<true, false>);
+  else
+    dy_f32 ? go(moe_combine_backward_kernel<false, true>) : go(moe_combine_backward_kernel<false, false>);
   return hipGetLastError();
 }
 

@@ -12,6 +12,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "expert_tile.h"
 #include "fp8q_device.h"
 #include "fp8q_launch.h"
 
@@ -293,28 +294,33 @@ __device__ __forceinline__ float bf16_elem(const uint4 &v, int e) {
   return (e & 1) ? bf16_hi(w) : bf16_lo(w);
 }
 
-__global__ __launch_bounds__(256) void quant_act_dual_kernel(const uint16_t *__restrict__ x, int64_t M,
-                                                             int64_t K, uint8_t *__restrict__ xq,
-                                                             float *__restrict__ sa,
-                                                             uint8_t *__restrict__ xqt,
-                                                             float *__restrict__ sat) {
+// One 128x128 tile: rows 0 .. rows-1 (of at most 128, all of them with kFull) at `x` (row
+// stride K), the missing rows zero.  kRows: the rows' codes at `xq` and their scales at `sa`
+// (consecutive rows) are written too.  Column codes go to `xqt` (row stride ld), column
+// scales to `sat`.  Every pointer is the tile's own corner.
+template <bool kRows, bool kFull>
+__device__ __forceinline__ void quant_dual_tile(const uint16_t *__restrict__ x, int rows, int64_t K,
+                                                uint8_t *__restrict__ xq, float *__restrict__ sa,
+                                                uint8_t *__restrict__ xqt, int64_t ld, float *__restrict__ sat) {
   __shared__ float colmax[4][128];
   __shared__ float colscale[128], colrcp[128];
   __shared__ int colmode[128];
   __shared__ __attribute__((aligned(16))) uint32_t tile[128 * 32];
-  const int64_t KB = K >> 7;
-  const int64_t kb = blockIdx.x % KB;
-  const int64_t mb = blockIdx.x / KB;
   const int tid = threadIdx.x;
   const int sub = tid & 15;
   const int r0 = tid >> 4;
   const int lane = tid & 63;
   const int wave = tid >> 6;
-  const int64_t base = (mb * 128) * K + kb * 128 + sub * 8;
+  const int64_t base = sub * 8;
 
   uint4 v[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = load16_stream(x + base + (r0 + 16 * i) * K);
+  for (int i = 0; i < 8; ++i) {
+    if (kFull || r0 + 16 * i < rows)
+      v[i] = load16_stream(x + base + (r0 + 16 * i) * K);
+    else
+      v[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
   // values stay packed (two BF16 per register) and are widened where used: one shift or
   // mask each, which keeps the kernel small enough for 8 workgroups per CU
   auto xv = [&](int i, int e) { return bf16_elem(v[i], e); };
@@ -328,7 +334,7 @@ __global__ __launch_bounds__(256) void quant_act_dual_kernel(const uint16_t *__r
 
   // Row tiles (1x128 along K): the forward codes.
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < (kRows ? 8 : 0); ++i) {
     float xr[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) xr[e] = xv(i, e);
@@ -336,8 +342,11 @@ __global__ __launch_bounds__(256) void quant_act_dual_kernel(const uint16_t *__r
 #pragma unroll
     for (int e = 1; e < 8; ++e) m = fmaxf(m, fabsf(xr[e]));
     const float s = row16_max(m) / kE4M3Max;
-    *reinterpret_cast<uint2 *>(xq + base + (r0 + 16 * i) * K) = quant8f<true>(xr, GroupDiv(s));
-    if (sub == 0) sa[kb * M + mb * 128 + r0 + 16 * i] = s;
+    const uint2 q = quant8f<true>(xr, GroupDiv(s));
+    if (kFull || r0 + 16 * i < rows) {
+      *reinterpret_cast<uint2 *>(xq + base + (r0 + 16 * i) * K) = q;
+      if (sub == 0) sa[r0 + 16 * i] = s;
+    }
   }
 
   // Column tiles (128 tokens of one channel).
@@ -364,7 +373,7 @@ __global__ __launch_bounds__(256) void quant_act_dual_kernel(const uint16_t *__r
     colscale[tid] = s;
     colrcp[tid] = d.r;
     colmode[tid] = d.mode;
-    sat[mb * K + kb * 128 + tid] = s;
+    sat[tid] = s;
   }
   __syncthreads();
   fence_values();
@@ -396,7 +405,20 @@ __global__ __launch_bounds__(256) void quant_act_dual_kernel(const uint16_t *__r
     *reinterpret_cast<uint2 *>(tile + (r0 + 16 * i) * 32 + sub * 2) = q;
   }
   __syncthreads();
-  store_transposed_tile(tile, xqt + (kb * 128) * M + mb * 128, M, tid);
+  store_transposed_tile(tile, xqt, ld, tid);
+}
+
+__global__ __launch_bounds__(256) void quant_act_dual_kernel(const uint16_t *__restrict__ x, int64_t M,
+                                                             int64_t K, uint8_t *__restrict__ xq,
+                                                             float *__restrict__ sa,
+                                                             uint8_t *__restrict__ xqt,
+                                                             float *__restrict__ sat) {
+  const int64_t KB = K >> 7;
+  const int64_t kb = blockIdx.x % KB;
+  const int64_t mb = blockIdx.x / KB;
+  const int64_t at = mb * 128 * K + kb * 128;
+  quant_dual_tile<true, true>(x + at, 128, K, xq + at, sa + kb * M + mb * 128, xqt + kb * 128 * M + mb * 128, M,
+                              sat + mb * K + kb * 128);
 }
 
 hipError_t launch_quant_act_dual(const uint16_t *x, int64_t M, int64_t K, uint8_t *xq, float *sa,
@@ -405,6 +427,47 @@ hipError_t launch_quant_act_dual(const uint16_t *x, int64_t M, int64_t K, uint8_
   if (blocks > 0x7fffffff) return hipErrorInvalidValue;
   hipLaunchKernelGGL(quant_act_dual_kernel, dim3(static_cast<uint32_t>(blocks)), dim3(256), 0, stream, x, M, K,
                      xq, sa, xqt, sat);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------------------
+// The same for rows sorted by expert, for the experts' weight gradients dW[g] = dY[g]^T X[g]:
+// a token tile must not mix two experts, so expert g's rows offsets[g] .. offsets[g+1]-1 are
+// cut into ceil(n_g / 128) tiles of their own, the last one filled up with zeros (which
+// change neither a maximum nor a sum), and the tiles of all experts follow each other:
+// X^T[K][Mp] with Mp = 128 (M / 128 + G) columns, which always suffices.  One workgroup per
+// 128x128 tile; each finds its expert from the offsets (expert_tile.h).
+// ---------------------------------------------------------------------------------------
+template <bool kRows>
+__global__ __launch_bounds__(256) void quant_act_grouped_kernel(const uint16_t *__restrict__ x,
+                                                                const int32_t *__restrict__ offsets, int G,
+                                                                int64_t M, int64_t K, int64_t Mp,
+                                                                uint8_t *__restrict__ xq, float *__restrict__ sa,
+                                                                uint8_t *__restrict__ xqt,
+                                                                float *__restrict__ sat) {
+  const int64_t KB = K >> 7;
+  const int64_t kb = blockIdx.x % KB;
+  const int64_t mb = blockIdx.x / KB;
+  int64_t row;
+  int rows;
+  if (!expert_of_tile(offsets, G, M, mb, row, rows)) return;  // behind the last expert's tiles
+  const int64_t at = row * K + kb * 128;
+  quant_dual_tile<kRows, false>(x + at, rows, K, kRows ? xq + at : nullptr, kRows ? sa + kb * M + row : nullptr,
+                                xqt + kb * 128 * Mp + mb * 128, Mp, sat + mb * K + kb * 128);
+}
+
+hipError_t launch_quant_act_grouped(const uint16_t *x, const int32_t *offsets, int64_t G, int64_t M, int64_t K,
+                                    int64_t Mp, uint8_t *xq, float *sa, uint8_t *xqt, float *sat,
+                                    hipStream_t stream) {
+  const int64_t blocks = (Mp / 128) * (K / 128);
+  if (blocks > 0x7fffffff) return hipErrorInvalidValue;
+  const dim3 grid(static_cast<uint32_t>(blocks)), block(256);
+  if (xq != nullptr)
+    hipLaunchKernelGGL(quant_act_grouped_kernel<true>, grid, block, 0, stream, x, offsets, static_cast<int>(G), M, K,
+                       Mp, xq, sa, xqt, sat);
+  else
+    hipLaunchKernelGGL(quant_act_grouped_kernel<false>, grid, block, 0, stream, x, offsets, static_cast<int>(G), M, K,
+                       Mp, xq, sa, xqt, sat);
   return hipGetLastError();
 }
 

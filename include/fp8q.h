@@ -65,7 +65,7 @@
 extern "C" {
 #endif
 
-#define FP8Q_ABI_VERSION 7
+#define FP8Q_ABI_VERSION 8
 
 typedef int32_t fp8q_status;
 
@@ -74,10 +74,11 @@ enum {
   FP8Q_ERR_NULL = -1,   /* a required pointer is NULL                                   */
   FP8Q_ERR_SHAPE = -2,  /* negative size, K or N not a multiple of 128, G < 1, overflow */
   FP8Q_ERR_ALIGN = -3,  /* a base pointer is not 16-byte aligned                        */
-  FP8Q_ERR_DTYPE = -4,  /* out_dtype is neither FP8Q_OUT_BF16 nor FP8Q_OUT_F32          */
+  FP8Q_ERR_DTYPE = -4,  /* a dtype argument is none of the values it can take           */
   FP8Q_ERR_DEVICE = -5, /* no usable HIP device                                          */
   FP8Q_ERR_LAUNCH = -6,  /* the kernel launch failed (hipGetLastError)                  */
-  FP8Q_ERR_OFFSETS = -7  /* grouped GEMM offsets invalid (checked only under FP8Q_DEBUG) */
+  FP8Q_ERR_OFFSETS = -7, /* grouped GEMM offsets invalid (checked only under FP8Q_DEBUG) */
+  FP8Q_ERR_VALUE = -8    /* a hyperparameter out of its range                            */
 };
 
 enum { FP8Q_OUT_BF16 = 0, FP8Q_OUT_F32 = 1 };
@@ -298,6 +299,158 @@ fp8q_status fp8q_moe_dispatch(const int32_t *topk_ids, int64_t T, int64_t k, int
 fp8q_status fp8q_moe_combine(const void *expert_out, int32_t in_dtype, int64_t capacity, int64_t N,
                              const int32_t *token_row, const float *topk_weights, int64_t T, int64_t k, void *y,
                              int32_t out_dtype, void *stream);
+
+/*
+ * Training step of an MoE layer: the sort with values, and the gradients of the sort, of the
+ * combine and of SwiGLU.  With the grouped weight-gradient product below and the grouped GEMM
+ * on transposed weights (fp8q_quantize_w_128x128_t) for the data gradients, one layer's
+ * backward pass runs as
+ *   dys, dw_gate = combine_backward(dy, ys);  dh = grouped GEMM(q(dys), W_down^T);
+ *   dgu, h = swiglu_backward(gu, dh);  dxs = grouped GEMM(q(dgu), W_up^T);
+ *   dx = sort_backward(dxs);  dW_down = dys^T h;  dW_up = dgu^T xs.
+ * Sources: as for the dispatch, the combine and the backward pass above.
+ */
+
+/*
+ * Tokens sorted by expert, as values: the routing of fp8q_moe_dispatch with rows of x in place
+ * of codes and scales, xs[token_row[t][s]] = x[t].
+ *   topk_ids, T, k, e_begin, E, capacity, offsets, token_row, row_token : as fp8q_moe_dispatch
+ *   x  : [T][H] BF16 or FP32 per dtype;  xs : [capacity][H] of the same type (out); rows from
+ *        min(offsets[E], capacity) on are left as they were
+ * Requires H % 8 == 0 and T * ceil(H / 1024) < 2^31.  With T == 0 only `offsets` is written.
+ * Errors: FP8Q_ERR_DTYPE, otherwise as fp8q_moe_dispatch.
+ */
+fp8q_status fp8q_moe_sort(const int32_t *topk_ids, int64_t T, int64_t k, int64_t e_begin, int64_t E, const void *x,
+                          int32_t dtype, int64_t H, int64_t capacity, void *xs, int32_t *offsets, int32_t *token_row,
+                          int32_t *row_token, void *stream);
+
+/*
+ * Gradient of the sort with respect to the tokens:
+ *   dx[t][c] = sum over slots s with 0 <= token_row[t][s] < capacity of dxs[token_row[t][s]][c],
+ * FP32 additions in slot order, rounded once to out_dtype (0 for a token without a row).
+ *   dxs : [capacity][H] in in_dtype;  dx : [T][H] in out_dtype (out).  Requires H % 8 == 0.
+ * Errors: as fp8q_moe_combine.
+ */
+fp8q_status fp8q_moe_sort_backward(const void *dxs, int32_t in_dtype, int64_t capacity, int64_t H,
+                                   const int32_t *token_row, int64_t T, int64_t k, void *dx, int32_t out_dtype,
+                                   void *stream);
+
+/*
+ * Gradients of the combine y[t] = sum_s w[t][s] * out[token_row[t][s]]:
+ *   dout[token_row[t][s]][n] = topk_weights[t][s] * dy[t][n]      (FP32 product, rounded once)
+ *   dw[t][s] = sum_n expert_out[token_row[t][s]][n] * dy[t][n]    (FP32, a fixed order)
+ * for the slots with 0 <= token_row[t][s] < capacity; dw is 0 for the others, and rows of dout
+ * that no slot has are left as they were.  The rows in token_row differ from each other (the
+ * dispatch and the sort give such maps): a row that several slots shared would get one of
+ * their gradients.
+ *   dy : [T][N] in dy_dtype;  expert_out, dout : [capacity][N] in dtype;  dw : [T][k] FP32.
+ * Requires N % 8 == 0.  Errors: as fp8q_moe_combine.
+ */
+fp8q_status fp8q_moe_combine_backward(const void *dy, int32_t dy_dtype, const void *expert_out, int32_t dtype,
+                                      int64_t capacity, int64_t N, const int32_t *token_row,
+                                      const float *topk_weights, int64_t T, int64_t k, void *dout, float *dw,
+                                      void *stream);
+
+/*
+ * Gradient of h = SiLU(g) * u (fp8q_swiglu_quantize_act_1x128 before its quantizer):
+ *   du = dh * SiLU(g),  dg = dh * u * s (1 + g (1 - s)) with s = 1 / (1 + e^-g), FP32, rounded once.
+ *   gu_bf16 : [M][2I] (g = columns 0..I-1, u the rest);  dh : [M][I] BF16 or FP32 per dh_dtype
+ *   dgu_bf16 : [M][2I] (out), the layout of gu
+ *   h_bf16 : [M][I] (out) or NULL: h again, rounded to BF16, for the weight gradient of the
+ *            down projection
+ * Requires I % 8 == 0, M >= 0.  M == 0 or I == 0 is a no-op.
+ * Errors: FP8Q_ERR_DTYPE, FP8Q_ERR_SHAPE, FP8Q_ERR_NULL, FP8Q_ERR_ALIGN, FP8Q_ERR_DEVICE,
+ * FP8Q_ERR_LAUNCH.
+ */
+fp8q_status fp8q_swiglu_backward(const uint16_t *gu_bf16, const void *dh, int32_t dh_dtype, int64_t M, int64_t I,
+                                 uint16_t *dgu_bf16, uint16_t *h_bf16, void *stream);
+
+/*
+ * fp8q_quantize_act_dual for rows sorted by expert, of any number per expert.  Token tiles do
+ * not cross from one expert to the next: expert g's rows offsets[g] .. offsets[g+1]-1 make
+ * ceil(n_g / 128) tiles of 128 tokens, the last one filled up with zeros, and the experts'
+ * tiles follow each other in Mp = 128 * (M_tot / 128 + G) columns (integer division), which
+ * suffices for every division of M_tot rows among G experts.
+ *   x_bf16 : [M_tot][K];  offsets : DEVICE int32 [G+1] as in fp8q_grouped_gemm_blockscaled
+ *            (every range clamped to [0, M_tot), not checked otherwise; rows from offsets[G] on
+ *            belong to no expert and are not read)
+ *   xq, sa : 1x128 tiles along K of the experts' rows, as fp8q_quantize_act_1x128 writes them
+ *            (xq [M_tot][K], sa [K/128][M_tot]); both NULL leaves them out
+ *   xqt    : [K][Mp] E4M3 codes (out), column 128 b + i the token i of tile b
+ *   sat    : [Mp/128][K] FP32 scales (out)
+ * What lies behind the last expert's last tile, and rows of no expert, are left as they were.
+ * Requires G >= 1, K % 128 == 0, Mp <= 2^22.  M_tot == 0 or K == 0 is a no-op.
+ * Errors: FP8Q_ERR_SHAPE, FP8Q_ERR_NULL (also one of xq and sa without the other),
+ * FP8Q_ERR_ALIGN, FP8Q_ERR_DEVICE, FP8Q_ERR_LAUNCH.
+ */
+fp8q_status fp8q_quantize_act_grouped(const uint16_t *x_bf16, const int32_t *offsets, int64_t G, int64_t M_tot,
+                                      int64_t K, uint8_t *xq, float *sa, uint8_t *xqt, float *sat, void *stream);
+
+/*
+ * The experts' weight gradients dW[g] = dY[g]^T X[g], every expert in one launch:
+ *   C[g][p][q] = sum over expert g's token tiles b of
+ *                sa[b][p] * sb[b][q] * sum_{k in tile b} decode(aq[p][k]) decode(bq[q][k])
+ * with FP32 promotion at every tile of 128 tokens, tiles ascending, as fp8q_gemm_rowscaled;
+ * zeros for an expert without rows.
+ *   aq [P][Mp], sa [Mp/128][P] and bq [Q][Mp], sb [Mp/128][Q] : from fp8q_quantize_act_grouped
+ *   with these offsets, G and M_tot (dW: aq = dY^T codes, bq = X^T codes)
+ *   c [G][P][Q], BF16 or FP32 per out_dtype (out)
+ * Requires G >= 1, P % 128 == 0, Q % 128 == 0, M_tot >= 0, Mp <= 2^22.  With M_tot == 0 the
+ * operands are not read (they may be NULL) and C is zeros.  P == 0 or Q == 0 is a no-op.
+ * Errors: FP8Q_ERR_DTYPE, FP8Q_ERR_SHAPE, FP8Q_ERR_NULL, FP8Q_ERR_ALIGN, FP8Q_ERR_DEVICE,
+ * FP8Q_ERR_LAUNCH.
+ */
+fp8q_status fp8q_grouped_gemm_rowscaled(const uint8_t *aq, const float *sa, const uint8_t *bq, const float *sb,
+                                        const int32_t *offsets, int64_t G, int64_t M_tot, int64_t P, int64_t Q,
+                                        void *c, int32_t out_dtype, void *stream);
+
+/*
+ * One AdamW step over many tensors, g = grad_scale * grad and, for step t = 1, 2, ...,
+ *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2,
+ *   p = p (1 - lr weight_decay) - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps),
+ * every operation rounded to FP32 by itself.  The states m and v are FP32, or (after the
+ * codingmall.com page, sections "Dinh luong hat min" and "Dinh dang E4M3 hop nhat", applied
+ * to the optimizer as this library's reading) E4M3 codes of m and of sqrt(v) with one FP32
+ * scale amax/448 per 128 consecutive elements, rounded like the activation tiles; a nonzero
+ * sqrt(v) gets the smallest code rather than zero.  All-zero states (codes and scales) start
+ * a run.  p takes the new m and v before they are rounded to E4M3.
+ *   tensors : HOST array of `count` descriptors, read during the call only; their pointers are
+ *             DEVICE memory, all of it disjoint from each other:
+ *     p [n] FP32 (in, out);  grad [n] BF16 or FP32 per grad_dtype
+ *     m, v : FP32 [n], or E4M3 codes uint8 [n] per state_dtype (in, out)
+ *     m_scale, v_scale : FP32 [ceil(n/128)], E4M3 states only (in, out; else ignored)
+ *     p_bf16 : [n] BF16 (out), the new p rounded to nearest even, or NULL
+ *     n >= 0 elements, any number (n == 0: skipped)
+ *   hyper : HOST struct, read during the call only.  Requires 0 <= beta < 1, eps >= 0, step >= 1,
+ *           every number finite.  `scalars`, if not NULL, is a DEVICE float[4] = {lr,
+ *           1 - beta1^t, 1 - beta2^t, grad_scale} read by the kernels in place of lr, step and
+ *           grad_scale, so that a captured step can be replayed with new values.
+ * Launches: one per 48 nonempty tensors.  Gradients are finite (else unspecified, and an E4M3
+ * tile shares the damage).  Errors: FP8Q_ERR_DTYPE, FP8Q_ERR_VALUE, FP8Q_ERR_SHAPE (n < 0 or
+ * n >= 2^40), FP8Q_ERR_NULL, FP8Q_ERR_ALIGN (scales and scalars 4-byte, the rest 16-byte),
+ * FP8Q_ERR_DEVICE, FP8Q_ERR_LAUNCH.
+ */
+enum { FP8Q_STATE_F32 = 0, FP8Q_STATE_E4M3 = 1 };
+
+typedef struct {
+  float *p;
+  const void *grad;
+  void *m;
+  void *v;
+  float *m_scale;
+  float *v_scale;
+  uint16_t *p_bf16;
+  int64_t n;
+} fp8q_adamw_tensor;
+
+typedef struct {
+  double lr, beta1, beta2, eps, weight_decay, grad_scale;
+  int64_t step;
+  const float *scalars;
+} fp8q_adamw_hyper;
+
+fp8q_status fp8q_adamw(const fp8q_adamw_tensor *tensors, int64_t count, int32_t grad_dtype, int32_t state_dtype,
+                       const fp8q_adamw_hyper *hyper, void *stream);
 
 /* Static, human-readable text for a status code (never NULL). */
 const char *fp8q_status_string(fp8q_status status);
