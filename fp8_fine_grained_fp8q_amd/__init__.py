@@ -545,22 +545,18 @@ def fp8q_swiglu_backward(gu: torch.Tensor, dh: torch.Tensor, dgu: torch.Tensor |
     return dgu, h
 
 
-def _grouped_columns(m_tot: int, groups: int) -> int:
-    return 128 * (m_tot // 128 + groups)
-
-
 def fp8q_quantize_act_grouped(x: torch.Tensor, offsets: torch.Tensor, rows: bool = True, xq=None, sa=None, xqt=None,
                               sat=None, stream=None):
     """x bf16 [M, K] sorted by expert, offsets int32 [G + 1] -> (xq uint8 [M, K], sa float32
-    [K/128, M], xqt uint8 [K, Mp], sat float32 [Mp/128, K]) with Mp = 128 (M // 128 + G): 1x128
-    tiles along K (None, None with rows=False) and tiles of 128 tokens of one expert."""
+    [K/128, M], xqt uint8 [B, K, 128], sat float32 [B, K]) with B = M // 128 + G: 1x128 tiles
+    along K (None, None with rows=False) and tiles of 128 tokens of one expert."""
     _need(x, torch.bfloat16, "x")
     _need(offsets, torch.int32, "offsets")
     if x.dim() != 2 or x.shape[1] % 128 or offsets.dim() != 1 or offsets.shape[0] < 2:
         raise ValueError(f"x must be [M, K] with K a multiple of 128 and offsets [G + 1], got {tuple(x.shape)} and "
                          f"{tuple(offsets.shape)}")
     (M, K), G = x.shape, offsets.shape[0] - 1
-    mp = _grouped_columns(M, G)
+    tiles = M // 128 + G
     if not rows and (xq is not None or sa is not None):
         raise ValueError("xq and sa are written with rows=True only")
     with _on(stream, x, offsets, xq, sa, xqt, sat) as s:
@@ -569,10 +565,10 @@ def fp8q_quantize_act_grouped(x: torch.Tensor, offsets: torch.Tensor, rows: bool
             sa = torch.empty((K // 128, M), dtype=torch.float32, device=x.device) if sa is None else sa
             _need(xq, torch.uint8, "xq", (M, K))
             _need(sa, torch.float32, "sa", (K // 128, M))
-        xqt = torch.empty((K, mp), dtype=torch.uint8, device=x.device) if xqt is None else xqt
-        sat = torch.empty((mp // 128, K), dtype=torch.float32, device=x.device) if sat is None else sat
-        _need(xqt, torch.uint8, "xqt", (K, mp))
-        _need(sat, torch.float32, "sat", (mp // 128, K))
+        xqt = torch.empty((tiles, K, 128), dtype=torch.uint8, device=x.device) if xqt is None else xqt
+        sat = torch.empty((tiles, K), dtype=torch.float32, device=x.device) if sat is None else sat
+        _need(xqt, torch.uint8, "xqt", (tiles, K, 128))
+        _need(sat, torch.float32, "sat", (tiles, K))
         _check(load_library().fp8q_quantize_act_grouped(_ptr(x), _ptr(offsets), G, M, K, _ptr(xq), _ptr(sa), _ptr(xqt),
                                                         _ptr(sat), s), "fp8q_quantize_act_grouped")
     return xq, sa, xqt, sat
@@ -581,19 +577,19 @@ def fp8q_quantize_act_grouped(x: torch.Tensor, offsets: torch.Tensor, rows: bool
 def fp8q_grouped_gemm_rowscaled(aq, sa, bq, sb, offsets, m_tot: int, out_dtype=torch.bfloat16,
                                 out: torch.Tensor | None = None, stream=None):
     """The experts' weight gradients C [G, P, Q]: C[g] = dequant(aq, sa) @ dequant(bq, sb)^T over expert
-    g's token tiles; aq [P, Mp], sa [Mp/128, P], bq [Q, Mp], sb [Mp/128, Q] from
+    g's token tiles; aq [B, P, 128], sa [B, P], bq [B, Q, 128], sb [B, Q] from
     fp8q_quantize_act_grouped of tensors with m_tot rows and these offsets."""
     _need(aq, torch.uint8, "aq")
     _need(bq, torch.uint8, "bq")
     _need(offsets, torch.int32, "offsets")
-    if aq.dim() != 2 or bq.dim() != 2 or offsets.dim() != 1 or offsets.shape[0] < 2 or m_tot < 0:
-        raise ValueError("aq must be [P, Mp], bq [Q, Mp] and offsets [G + 1]")
-    P, Q, G = aq.shape[0], bq.shape[0], offsets.shape[0] - 1
-    mp = _grouped_columns(int(m_tot), G)
-    _need(aq, torch.uint8, "aq", (P, mp))
-    _need(bq, torch.uint8, "bq", (Q, mp))
-    _need(sa, torch.float32, "sa", (mp // 128, P))
-    _need(sb, torch.float32, "sb", (mp // 128, Q))
+    if aq.dim() != 3 or bq.dim() != 3 or offsets.dim() != 1 or offsets.shape[0] < 2 or m_tot < 0:
+        raise ValueError("aq must be [B, P, 128], bq [B, Q, 128] and offsets [G + 1]")
+    P, Q, G = aq.shape[1], bq.shape[1], offsets.shape[0] - 1
+    tiles = int(m_tot) // 128 + G
+    _need(aq, torch.uint8, "aq", (tiles, P, 128))
+    _need(bq, torch.uint8, "bq", (tiles, Q, 128))
+    _need(sa, torch.float32, "sa", (tiles, P))
+    _need(sb, torch.float32, "sb", (tiles, Q))
     with _on(stream, aq, sa, bq, sb, offsets, out) as s:
         out = torch.empty((G, P, Q), dtype=out_dtype, device=aq.device) if out is None else out
         _need(out, out.dtype, "out", (G, P, Q))

@@ -57,9 +57,10 @@ __device__ __forceinline__ bool expert_of_tile(const int32_t *__restrict__ offse
   return false;
 }
 
-// Expert g's first tile and its number of tiles (every lane the same answer).
+// Expert g's first tile, its number of tiles and the rows of the last one (every lane the same
+// answer).
 __device__ __forceinline__ void tiles_of_expert(const int32_t *__restrict__ offsets, int G, int64_t M, int g,
-                                                int64_t &first, int64_t &tiles) {
+                                                int64_t &first, int64_t &tiles, int &rest) {
   const int lane = threadIdx.x & 63;
   int64_t sum = 0;
   for (int g0 = 0; g0 < g; g0 += 64) {
@@ -73,6 +74,7 @@ __device__ __forceinline__ void tiles_of_expert(const int32_t *__restrict__ offs
   expert_rows(offsets, G, M, g, a, b);
   first = sum;
   tiles = (b - a + 127) / 128;
+  rest = static_cast<int>(b - a - (tiles - 1) * 128);
 }
 
 }  // namespace fp8q

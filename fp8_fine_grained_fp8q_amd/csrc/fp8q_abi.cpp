@@ -39,13 +39,6 @@ bool debug_checks() {
 
 bool bad_dtype(int32_t d) { return d != FP8Q_OUT_BF16 && d != FP8Q_OUT_F32; }
 
-// Columns of the grouped token tiles of M rows on G experts; 0 where they exceed what the
-// kernels address (2^22).
-int64_t grouped_columns(int64_t M, int64_t G) {
-  const int64_t mp = 128 * (M / 128 + G);
-  return mp <= kMaxGemmK ? mp : 0;
-}
-
 // Shared checks of the token maps [T][k] and of rows of `width` columns.
 bool bad_rows(int64_t T, int64_t k, int64_t capacity, int64_t width) {
   return bad_dim(T) || k < 1 || k > 64 || bad_dim(width) || width % 8 != 0 || bad_dim(capacity) || too_many(T, k) ||
@@ -306,15 +299,14 @@ fp8q_status fp8q_quantize_act_grouped(const uint16_t *x_bf16, const int32_t *off
                                       int64_t K, uint8_t *xq, float *sa, uint8_t *xqt, float *sat, void *stream) {
   if (G < 1 || bad_dim(G) || bad_dim(M_tot) || bad_dim(K) || K % 128 != 0 || too_many(M_tot, K))
     return FP8Q_ERR_SHAPE;
-  const int64_t Mp = grouped_columns(M_tot, G);
-  if (Mp == 0 || (Mp / 128) * (K / 128) >= kMaxDim) return FP8Q_ERR_SHAPE;
+  if (too_many(M_tot / 128 + G, K) || (M_tot / 128 + G) * (K / 128) >= kMaxDim) return FP8Q_ERR_SHAPE;
   if (M_tot == 0 || K == 0) return FP8Q_OK;
   if (!x_bf16 || !offsets || !xqt || !sat || !xq != !sa) return FP8Q_ERR_NULL;
   if (misaligned(x_bf16) || misaligned(offsets, 4) || misaligned(xq) || misaligned(sa) || misaligned(xqt) ||
       misaligned(sat))
     return FP8Q_ERR_ALIGN;
   if (device_ok() != FP8Q_OK) return FP8Q_ERR_DEVICE;
-  return launched(fp8q::launch_quant_act_grouped(x_bf16, offsets, G, M_tot, K, Mp, xq, sa, xqt, sat,
+  return launched(fp8q::launch_quant_act_grouped(x_bf16, offsets, G, M_tot, K, xq, sa, xqt, sat,
                                                  as_stream(stream)));
 }
 
@@ -324,15 +316,15 @@ fp8q_status fp8q_grouped_gemm_rowscaled(const uint8_t *aq, const float *sa, cons
   if (bad_dtype(out_dtype)) return FP8Q_ERR_DTYPE;
   if (G < 1 || bad_dim(G) || bad_dim(M_tot) || bad_dim(P) || bad_dim(Q) || P % 128 != 0 || Q % 128 != 0)
     return FP8Q_ERR_SHAPE;
+  if (P > kMaxGemmK || Q > kMaxGemmK) return FP8Q_ERR_SHAPE;  // 32-bit offsets within a tile's rows
   if (too_many(G, P) || too_many(G * P, Q)) return FP8Q_ERR_SHAPE;
-  const int64_t Mp = grouped_columns(M_tot, G);
-  if (Mp == 0 || too_many(G * (P / 128), Q / 128) || G * (P / 128) * (Q / 128) >= kMaxDim) return FP8Q_ERR_SHAPE;
+  if (G * (P / 128) * (Q / 128) >= kMaxDim || M_tot / 128 + G >= kMaxDim) return FP8Q_ERR_SHAPE;
   if (P == 0 || Q == 0) return FP8Q_OK;
   if (!c || !offsets || (M_tot > 0 && (!aq || !sa || !bq || !sb))) return FP8Q_ERR_NULL;
   if (misaligned(aq) || misaligned(sa) || misaligned(bq) || misaligned(sb) || misaligned(offsets, 4) || misaligned(c))
     return FP8Q_ERR_ALIGN;
   if (device_ok() != FP8Q_OK) return FP8Q_ERR_DEVICE;
-  return launched(fp8q::launch_grouped_gemm_rowscaled(aq, sa, bq, sb, offsets, G, M_tot, Mp, P, Q, c,
+  return launched(fp8q::launch_grouped_gemm_rowscaled(aq, sa, bq, sb, offsets, G, M_tot, P, Q, c,
                                                       out_dtype == FP8Q_OUT_F32, as_stream(stream)));
 }
 

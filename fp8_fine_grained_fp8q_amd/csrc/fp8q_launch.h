@@ -83,16 +83,16 @@ hipError_t launch_moe_combine_backward(const void *dy, bool dy_f32, const void *
 hipError_t launch_swiglu_backward(const uint16_t *gu, const void *dh, bool dh_f32, int64_t M, int64_t I,
                                   uint16_t *dgu, uint16_t *h, hipStream_t stream);
 
-// Token tiles of expert-sorted rows, none across two experts: xqt[K][Mp], sat[Mp/128][K], Mp =
-// 128 (M / 128 + G); the rows' 1x128 codes xq[M][K], sa[K/128][M] too unless xq is null.
+// Token tiles of expert-sorted rows, none across two experts: xqt[B][K][128], sat[B][K], B =
+// M / 128 + G; the rows' 1x128 codes xq[M][K], sa[K/128][M] too unless xq is null.
 hipError_t launch_quant_act_grouped(const uint16_t *x, const int32_t *offsets, int64_t G, int64_t M, int64_t K,
-                                    int64_t Mp, uint8_t *xq, float *sa, uint8_t *xqt, float *sat,
+                                    uint8_t *xq, float *sa, uint8_t *xqt, float *sat,
                                     hipStream_t stream);
 
 // C[g] = dequant(aq, sa) dequant(bq, sb)^T over expert g's token tiles.
 hipError_t launch_grouped_gemm_rowscaled(const uint8_t *aq, const float *sa, const uint8_t *bq, const float *sb,
-                                         const int32_t *offsets, int64_t G, int64_t M, int64_t Mp, int64_t P,
-                                         int64_t Q, void *c, bool out_f32, hipStream_t stream);
+                                         const int32_t *offsets, int64_t G, int64_t M, int64_t P, int64_t Q,
+                                          void *c, bool out_f32, hipStream_t stream);
 
 // One AdamW step over `count` tensors (host array).
 hipError_t launch_adamw(const fp8q_adamw_tensor *tensors, int64_t count, bool grad_f32, bool e4m3,

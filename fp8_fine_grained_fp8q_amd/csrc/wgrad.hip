@@ -6,12 +6,30 @@
 //                sa[b][p] * sb[b][q] * sum_{k in tile b} e4m3(aq[p][k]) * e4m3(bq[q][k])
 //
 // The contraction runs over the expert's tokens, in the tiles of 128 that
-// quant_act_grouped_kernel writes (channel-major codes, one FP32 scale per tile and
-// channel).  One v_mfma_f32_16x16x128_f8f6f4 covers one tile of a 16x16 block; it starts
-// from zero and its result is scaled and added to an FP32 accumulator, acc = (P * sb) * sa +
-// acc: two vector operations per element and token tile, as both scales vary inside a lane.
+// quant_act_grouped_kernel writes (one FP32 scale per tile and channel).  A tile's sum starts
+// from zero in the matrix core; its result is scaled and added to an FP32 accumulator, acc =
+// (P * sa) * sb + acc: two vector operations per element and token tile, as both scales vary
+// inside a lane.
+//
+// BF16 output takes the FP8 matrix instructions.  Their sums of 64 products are off by 1.4e-5
+// (2-norm, normal data, any of the shapes), far below BF16's rounding but above FP32's: FP32
+// output widens the codes to BF16, exactly, and takes the BF16 instructions (8e-9), at half
+// their rate.
+//
+// Two regimes, measured on one MI355X (product alone, without the quantizers):
+//  * few tokens per expert: the gradient's bytes.  32 experts of 4096 x 7168 over 8192 rows: FP32
+//    1002 us (3.75 TB/s of 3.76 GB), BF16 564 us; stores alone take 650 and 366 us, the loads
+//    and products alone about 780 and 455 us, and the two overlap only in part.
+//  * many: the matrix cores beside the two vector operations per element.  4 experts of 7168 x
+//    2048 over 16384 rows: BF16 output 322 us (1.50 PFLOP/s), FP32 540 us; one expert of 7168 x
+//    7168 over 4096 rows 282 us (1.49 PFLOP/s).
+//
+// A workgroup of 8 waves computes 128 x 128 tiles of one expert, 32 x 64 per wave in 32x32 blocks,
+// two workgroups per CU, so that one's loads and stores run beside the other's products.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "expert_tile.h"
 #include "fp8q_device.h"
@@ -20,223 +38,314 @@
 namespace fp8q {
 
 typedef int v8i __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef float v4f __attribute__((ext_vector_type(4)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 #define FP8Q_LDS __attribute__((address_space(3)))
 
 // Buffer resource over `bytes` bytes at `p`; loads at or past the end return zeros.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *p, int64_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), static_cast<short>(0), static_cast<int>(bytes),
-                                           0x00020000);
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *p, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), static_cast<short>(0), bytes, 0x00020000);
 }
 
-// LDS byte offset of the 16-byte chunk c (0..7) of operand row `row` in a stage.  A 16x16x128
-// fragment is read as lane 16 kg + r taking chunks 2 kg and 2 kg + 1 of row r, so rows r and
-// r + 8 of a group of 16 share a 256-byte line and the chunks of a row are XOR-swizzled by
-// r mod 8: the 16 lanes of a read then touch every bank once.
+constexpr int kTile = 128;            // rows and columns of C per tile
+constexpr int kWaves = 8;             // 4 x 2, 32 rows x 64 columns each
+constexpr int kPanel = kTile * 128;   // bytes of one operand in a stage
+constexpr int kScaleAt = 2 * kPanel;  // then 128 row scales and 128 column scales
+constexpr int kStage = kScaleAt + 2 * kTile * 4;
+
+// LDS byte offset of the 16-byte chunk c (0..7) of operand row `row` in a stage.  A fragment
+// read takes one chunk of 32 rows per half wave; rows r and r + 8 of a group of 16 share a
+// 256-byte line and the chunks of a row are XOR-swizzled by r mod 8, so that every 16 lanes
+// of a read touch each bank once.
 __device__ __forceinline__ int chunk_pos(int row, int c) {
   const int r = row & 15;
   return (row >> 4) * 2048 + (r & 7) * 256 + (r >> 3) * 128 + ((c ^ (r & 7)) << 4);
 }
 
-__device__ __forceinline__ v8i fragment(const FP8Q_LDS uint8_t *lds, int group, int lo, int hi) {
-  const v4i a = *reinterpret_cast<const FP8Q_LDS v4i *>(lds + group * 2048 + lo);
-  const v4i b = *reinterpret_cast<const FP8Q_LDS v4i *>(lds + group * 2048 + hi);
+// Eight E4M3 codes as BF16 (exact).
+__device__ __forceinline__ bf16x8 widen8(int lo, int hi) {
+  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
+  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
+  const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
+  const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
+  return bf16x8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+}
+
+__device__ __forceinline__ uint32_t lds_address(FP8Q_LDS uint8_t *p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p));
+}
+
+__device__ __forceinline__ v8i join(const v4i &a, const v4i &b) {
   return v8i{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 }
 
-// One workgroup of WM x WN waves computes a (16 FM WM) x (16 FN WN) tile of one expert's C,
-// each wave 16 FM rows x 16 FN columns.  Stages of one token tile (operand codes and scales)
-// are double buffered in LDS and filled by direct-to-LDS copies.
-template <int WM, int WN, int FM, int FN>
-struct Wgrad {
-  static constexpr int kWaves = WM * WN;
-  static constexpr int kTM = 16 * FM * WM, kTN = 16 * FN * WN;
-  static constexpr int kA = kTM * 128, kB = kTN * 128;     // bytes of a stage's operands
-  static constexpr int kScales = (kTM + kTN) * 4;          // and of its scales
-  static constexpr int kStage = kA + kB + kScales;
-  static constexpr int kCopiesA = kTM / 8 / kWaves, kCopiesB = kTN / 8 / kWaves;  // 1 KB copies per wave
-  static constexpr int kScaleCopies = (kTM + kTN) / 64 / kWaves;
-  static_assert(kTM % (8 * kWaves) == 0 && kTN % (8 * kWaves) == 0 && (kTM + kTN) % (64 * kWaves) == 0, "whole copies");
-};
+// LDS reads as single asm blocks that wait for themselves.  Written as C++ loads, the compiler
+// has them wait for every direct-to-LDS copy that it cannot prove to be of other bytes, and
+// with copies and stores of a varying number behind them that means vmcnt(0): each second
+// stage then waited for the copies issued just before it and for the tile's stores (the copies
+// that these reads do need are waited for at the stage's start).
+template <int kAt>
+__device__ __forceinline__ void read_chunks(v4i &a, v4i (&b)[2], uint32_t pa, uint32_t pb) {
+  asm volatile(
+      "ds_read_b128 %0, %3 offset:%5\n\tds_read_b128 %1, %4 offset:%6\n\tds_read_b128 %2, %4 offset:%7\n\t"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(a), "=&v"(b[0]), "=&v"(b[1])
+      : "v"(pa), "v"(pb), "n"(kAt), "n"(kAt + kPanel), "n"(kAt + kPanel + 4096)
+      : "memory");
+}
+template <int kAt>
+__device__ __forceinline__ void read_chunks(v4i (&a)[2], v4i (&b)[2][2], uint32_t pa0, uint32_t pa1, uint32_t pb0,
+                                            uint32_t pb1) {
+  asm volatile(
+      "ds_read_b128 %0, %6 offset:%10\n\tds_read_b128 %1, %7 offset:%10\n\t"
+      "ds_read_b128 %2, %8 offset:%11\n\tds_read_b128 %3, %9 offset:%11\n\t"
+      "ds_read_b128 %4, %8 offset:%12\n\tds_read_b128 %5, %9 offset:%12\n\ts_waitcnt lgkmcnt(0)"
+      : "=&v"(a[0]), "=&v"(a[1]), "=&v"(b[0][0]), "=&v"(b[0][1]), "=&v"(b[1][0]), "=&v"(b[1][1])
+      : "v"(pa0), "v"(pa1), "v"(pb0), "v"(pb1), "n"(kAt), "n"(kAt + kPanel), "n"(kAt + kPanel + 4096)
+      : "memory");
+}
+// The scales of the lane's 16 rows and 2 columns.
+template <int kAt>
+__device__ __forceinline__ void read_scales(v4f (&sr)[4], f32x2 &sc, uint32_t pr, uint32_t pc) {
+  asm volatile(
+      "ds_read_b128 %0, %5 offset:%7\n\tds_read_b128 %1, %5 offset:%8\n\tds_read_b128 %2, %5 offset:%9\n\t"
+      "ds_read_b128 %3, %5 offset:%10\n\tds_read_b64 %4, %6 offset:%11\n\ts_waitcnt lgkmcnt(0)"
+      : "=&v"(sr[0]), "=&v"(sr[1]), "=&v"(sr[2]), "=&v"(sr[3]), "=&v"(sc)
+      : "v"(pr), "v"(pc), "n"(kAt), "n"(kAt + 32), "n"(kAt + 64), "n"(kAt + 96), "n"(kAt + kTile * 4)
+      : "memory");
+}
 
-template <int WM, int WN, int FM, int FN>
-__device__ __forceinline__ void wgrad_tile(const uint8_t *__restrict__ aq, const float *__restrict__ sa,
-                                           const uint8_t *__restrict__ bq, const float *__restrict__ sb,
-                                           const int32_t *__restrict__ offsets, int G, int64_t M, int64_t Mp, int P,
-                                           int Q, void *__restrict__ c, int out_f32, FP8Q_LDS uint8_t *s0,
-                                           FP8Q_LDS uint8_t *s1) {
-  using W = Wgrad<WM, WN, FM, FN>;
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
 
-  // Workgroups are dealt round-robin to the 8 XCDs; each XCD gets a contiguous run of tiles,
-  // so that its L2 holds the panels that neighbouring tiles share.
-  const int tp = (P + W::kTM - 1) / W::kTM, tq = (Q + W::kTN - 1) / W::kTN;
+// C tiles (p0, q) for the run of 128-column tiles q0 .. q0 + 128 (count - 1) of expert g.
+template <bool kOutF32>
+__device__ __forceinline__ void wgrad_run(const uint8_t *__restrict__ aq, const float *__restrict__ sa,
+                                          const uint8_t *__restrict__ bq, const float *__restrict__ sb,
+                                          const int32_t *__restrict__ offsets, int G, int64_t M, int64_t all_tiles,
+                                          int64_t P, int64_t Q, int g, int64_t p0, int64_t q0, int count,
+                                          void *__restrict__ c, FP8Q_LDS uint8_t *st) {
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  const int l32 = lane & 31, half = lane >> 5;
+
+  int64_t first64, tiles64;
+  int rest;
+  tiles_of_expert(offsets, G, M, g, first64, tiles64, rest);
+  // valid offsets never reach past the last tile; others are kept inside the operands
+  const int64_t end64 = first64 + tiles64 < all_tiles ? first64 + tiles64 : all_tiles;
+  const int tiles = __builtin_amdgcn_readfirstlane(static_cast<int>(end64 > first64 ? end64 - first64 : 0));
+  const int first = __builtin_amdgcn_readfirstlane(static_cast<int>(tiles > 0 ? first64 : 0));
+  const int last = __builtin_amdgcn_readfirstlane((rest + 31) / 32);
+
+  // Copies: an operand's 16 KB stage is contiguous in memory.  1 KB block b = 8 i + wave of it
+  // in LDS holds 8 of a row group's 16 rows; lane l lands on line 4 (b % 2) + l / 16, half (l / 8)
+  // % 2, slot l % 8 of group b / 2 (the inverse of chunk_pos), on row 64 i + at.  For the
+  // columns' operand, row 64 w + 32 n + l in LDS is column 64 w + 2 l + n: a lane's elements of a
+  // wave's two column blocks are then neighbours in memory.
+  const int line = 4 * (wave & 1) + (lane >> 4);
+  const int at = 16 * (wave >> 1) + line + 8 * ((lane >> 3) & 1), chunk = ((lane & 7) ^ line) * 16;
+  const int off_a = at * 128 + chunk, off_b = (at & 31) * 256 + (at >> 5) * 128 + chunk;
+  auto load = [&](int j, int s, FP8Q_LDS uint8_t *st) {
+    const int64_t at_a = static_cast<int64_t>(first + s) * P + p0;
+    const int64_t at_b = static_cast<int64_t>(first + s) * Q + q0 + j * kTile;
+    const __amdgpu_buffer_rsrc_t ra = buffer_of(aq + at_a * 128, kPanel), rb = buffer_of(bq + at_b * 128, kPanel);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      FP8Q_LDS uint8_t *to = st + (kWaves * i + wave) * 1024;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (FP8Q_LDS void *)to, 16, off_a, i * 8192, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (FP8Q_LDS void *)(to + kPanel), 16, off_b, i * 8192, 0, 0);
+    }
+    // waves 0 and 1 copy 64 of the rows' scales each, waves 2 and 3 of the columns'
+    if (wave >= 4) return;
+    const __amdgpu_buffer_rsrc_t rs = buffer_of((wave < 2 ? sa + at_a : sb + at_b) + (wave & 1) * 64, 256);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (FP8Q_LDS void *)(st + kScaleAt + wave * 256), 4, lane * 4, 0, 0, 0);
+  };
+
+  // Element i of block n is row 8 (i / 4) + 4 half + i % 4, column 2 l32 + n of the wave.
+  v16f acc[2];
+  auto clear = [&]() {
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[n][i] = 0.0f;
+  };
+  // Each store writes two whole rows of 64 columns: full 128-byte lines, which the streaming
+  // stores need (with half lines the FP32 gradient of 32 experts x 4096 x 7168 took 1.3 ms, with
+  // whole ones and ordinary stores 1.4 ms).
+  constexpr int kSize = kOutF32 ? 4 : 2, kStream = 2;  // bytes of an element; the streaming-store flag
+  const int64_t c0 = (static_cast<int64_t>(g) * P + p0 + wm * 32) * Q + q0 + wn * 64;
+  const int ld = static_cast<int>(Q) * kSize, off_c = 4 * half * ld + 2 * l32 * kSize;
+  auto store = [&](int j) {
+    const __amdgpu_buffer_rsrc_t rc = buffer_of(static_cast<uint8_t *>(c) + (c0 + j * kTile) * kSize, 32 * ld);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int row = (8 * (i >> 2) + (i & 3)) * ld;
+      if (kOutF32)
+        __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(acc[0][i]), __float_as_uint(acc[1][i])}, rc, off_c,
+                                              row, kStream);
+      else
+        __builtin_amdgcn_raw_buffer_store_b32(pack2_bf16(acc[0][i], acc[1][i]), rc, off_c, row, kStream);
+    }
+  };
+  clear();
+  if (tiles == 0) {
+    for (int j = 0; j < count; ++j) store(j);
+    return;
+  }
+
+  // LDS addresses, in the first stage, of the lane's rows' chunk 2 m + half: chunks 2 m and 2 m + 1
+  // hold the tokens 32 m .. 32 m + 31.
+  uint32_t at_a[4], at_b[4];
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    const uint32_t pos = lds_address(st) + chunk_pos(l32, 2 * m + half);
+    at_a[m] = pos + wm * 4096;
+    at_b[m] = pos + wn * 8192;
+  }
+  const uint32_t at_sr = lds_address(st) + kScaleAt + (wm * 32 + 4 * half) * 4;
+  const uint32_t at_sc = lds_address(st) + kScaleAt + (wn * 64 + 2 * l32) * 4;
+  // Waits for the LDS reads and then for the other waves.  Not __syncthreads(), whose fence would
+  // wait for the copies and stores in flight.
+  auto meet = [&]() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // Stages run through the run's tiles without a break.  A wave's copies and stores complete in
+  // the order of their issue, so a copy behind a tile's stores would wait for those to drain:
+  // at the end of a tile the copies of the next two stages are issued first, and a stage's start
+  // waits for no more than the operations behind its own copies allow (at least kCopies, five in
+  // waves 0-3, and kStores).
+  constexpr int kStores = 16, kCopies = 4;
+  int j = 0, s = 0;          // the stage being multiplied
+  bool ahead = false;        // the next stage's copies are issued already
+  int stores = 0;            // 2: a tile ended a stage ago; 1: two stages ago
+  auto stage = [&](auto parity) {
+    constexpr int kCur = decltype(parity)::value * kStage;  // the stage's place in LDS
+    FP8Q_LDS uint8_t *cur = st + kCur, *next = st + (kStage - kCur);
+    if (stores == 2 && ahead)
+      wait_loads<kStores + kCopies>();
+    else if (stores != 0)
+      wait_loads<kStores>();
+    else
+      wait_loads<0>();
+    meet();  // every wave's copies have landed, and every wave has read the other buffer
+    const bool ends = s + 1 == tiles;
+    int jn = j, sn = s;
+    auto advance = [&]() {
+      const bool wrap = sn + 1 == tiles;
+      jn += wrap ? 1 : 0;
+      sn = wrap ? 0 : sn + 1;
+      return jn < count;
+    };
+    const bool more = advance();
+    const int j1 = jn, s1 = sn;
+    if (more && !ahead) load(jn, sn, next);
+    stores = stores == 2 && ahead ? 1 : 0;
+    ahead = false;
+    const int used = ends ? last : 4;  // the 32-token parts of the tile that hold tokens
+    v16f part[2] = {};
+    if constexpr (kOutF32) {
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        if (m > 0 && m >= used) break;
+        v4i a, b[2];
+        read_chunks<kCur>(a, b, at_a[m], at_b[m]);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const bf16x8 wa = widen8(a[2 * r], a[2 * r + 1]);
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+            part[n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wa, widen8(b[n][2 * r], b[n][2 * r + 1]), part[n], 0, 0, 0);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (h > 0 && used <= 2) break;
+        v4i a[2], b[2][2];
+        read_chunks<kCur>(a, b, at_a[2 * h], at_a[2 * h + 1], at_b[2 * h], at_b[2 * h + 1]);
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+          part[n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(join(a[0], a[1]), join(b[n][0], b[n][1]), part[n], 0,
+                                                                    0, 0, 0, 0, 0);
+      }
+    }
+    f32x2 sc;
+    v4f sr[4];
+    read_scales<kCur>(sr, sc, at_sr, at_sc);
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[n][i] = __builtin_fmaf(part[n][i] * sr[i >> 2][i & 3], sc[n], acc[n][i]);
+    if (ends) {
+      if (more) {
+        meet();  // every wave has read this stage too: its buffer takes the stage after the next
+        if (advance()) {
+          load(jn, sn, cur);
+          ahead = true;
+        }
+      }
+      store(j);
+      clear();
+      stores = 2;
+    }
+    j = j1;
+    s = s1;
+    return more;
+  };
+  load(0, 0, st);
+  while (stage(std::integral_constant<int, 0>{}) && stage(std::integral_constant<int, 1>{})) {
+  }
+}
+
+template <bool kOutF32>
+__global__ __launch_bounds__(64 * kWaves, 4) void wgrad_kernel(
+    const uint8_t *__restrict__ aq, const float *__restrict__ sa, const uint8_t *__restrict__ bq,
+    const float *__restrict__ sb, const int32_t *__restrict__ offsets, int G, int64_t M, int64_t all_tiles, int P,
+    int Q, int run, void *__restrict__ c) {
+  __shared__ __attribute__((aligned(1024))) uint8_t stages[2 * kStage];
+  // Workgroups are dealt round-robin to the 8 XCDs; each XCD gets a contiguous piece of the
+  // runs, ordered by expert, then by rows, then by columns: neighbouring workgroups write
+  // neighbouring parts of the same rows.
+  const int tp = P / kTile, tq = Q / kTile, runs = (tq + run - 1) / run;
   const int total = gridDim.x, per = total / 8, rem = total % 8;
   const int xcd = blockIdx.x % 8, idx = blockIdx.x / 8;
   const int logical = xcd * per + (xcd < rem ? xcd : rem) + idx;
-  const int g = logical / (tp * tq), in_g = logical - g * (tp * tq);
-  const int64_t p0 = static_cast<int64_t>(in_g % tp) * W::kTM, q0 = static_cast<int64_t>(in_g / tp) * W::kTN;
-
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave / WN, wn = wave % WN;
-  const int l16 = lane & 15, kg = lane >> 4;
-
-  int64_t first64, tiles64;
-  tiles_of_expert(offsets, G, M, g, first64, tiles64);
-  // valid offsets never reach past the Mp / 128 tiles; others are kept inside the operands
-  const int64_t end64 = first64 + tiles64 < Mp / 128 ? first64 + tiles64 : Mp / 128;
-  const int tiles = __builtin_amdgcn_readfirstlane(static_cast<int>(end64 > first64 ? end64 - first64 : 0));
-  const int first = __builtin_amdgcn_readfirstlane(static_cast<int>(tiles > 0 ? first64 : 0));
-
-  const int rows_a = static_cast<int>(P - p0 < W::kTM ? P - p0 : W::kTM);
-  const int rows_b = static_cast<int>(Q - q0 < W::kTN ? Q - q0 : W::kTN);
-  const __amdgpu_buffer_rsrc_t ra = buffer_of(aq + p0 * Mp, rows_a * Mp);
-  const __amdgpu_buffer_rsrc_t rb = buffer_of(bq + q0 * Mp, rows_b * Mp);
-
-  // Copies: 1 KB block b of an operand holds 8 of a row group's 16 rows; lane l lands on line
-  // 4 (b % 2) + l / 16, half (l / 8) % 2, slot l % 8 of group b / 2 (the inverse of chunk_pos).
-  auto row_of = [&](int b, int &chunk) {
-    const int line = 4 * (b & 1) + (lane >> 4);
-    chunk = (lane & 7) ^ line;
-    return 16 * (b >> 1) + line + 8 * ((lane >> 3) & 1);
-  };
-  int off_a[W::kCopiesA], off_b[W::kCopiesB];
-#pragma unroll
-  for (int i = 0; i < W::kCopiesA; ++i) {
-    int chunk;
-    const int row = row_of(i * W::kWaves + wave, chunk);
-    off_a[i] = row * static_cast<int>(Mp) + chunk * 16;
-  }
-#pragma unroll
-  for (int i = 0; i < W::kCopiesB; ++i) {
-    int chunk;
-    const int row = row_of(i * W::kWaves + wave, chunk);
-    off_b[i] = row * static_cast<int>(Mp) + chunk * 16;
-  }
-  auto load = [&](int s, FP8Q_LDS uint8_t *st) {
-    const int at = (first + s) * 128;
-#pragma unroll
-    for (int i = 0; i < W::kCopiesA; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (FP8Q_LDS void *)(st + (i * W::kWaves + wave) * 1024), 16, off_a[i],
-                                               at, 0, 0);
-#pragma unroll
-    for (int i = 0; i < W::kCopiesB; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (FP8Q_LDS void *)(st + W::kA + (i * W::kWaves + wave) * 1024), 16,
-                                               off_b[i], at, 0, 0);
-    // scales: 64 of them per copy, first the tile's rows, then its columns; past the last row
-    // or column nothing is read and zeros land
-#pragma unroll
-    for (int i = 0; i < W::kScaleCopies; ++i) {
-      const int block = i * W::kWaves + wave;
-      const bool is_a = block < W::kTM / 64;
-      const int64_t tile = first + s;
-      const int part = (is_a ? block : block - W::kTM / 64) * 64;
-      const __amdgpu_buffer_rsrc_t r =
-          buffer_of(is_a ? sa + tile * P + p0 : sb + tile * Q + q0, (is_a ? rows_a : rows_b) * 4);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (FP8Q_LDS void *)(st + W::kA + W::kB + block * 256), 4,
-                                               (part + lane) * 4, 0, 0, 0);
-    }
-  };
-
-  v4f acc[FM][FN];
-#pragma unroll
-  for (int f = 0; f < FM; ++f)
-#pragma unroll
-    for (int j = 0; j < FN; ++j) acc[f][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-  const int lo = chunk_pos(l16, 2 * kg), hi = chunk_pos(l16, 2 * kg + 1);
-
-  auto step = [&](const FP8Q_LDS uint8_t *cur, FP8Q_LDS uint8_t *next, int s) {
-    // this wave's copies of stage s have landed; after the barrier every wave's have, and
-    // every wave is done reading the other buffer
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    if (s + 1 < tiles) load(s + 1, next);
-    const FP8Q_LDS uint8_t *ca = cur, *cb = cur + W::kA, *cs = cur + W::kA + W::kB;
-    v8i af[FM];
-    float sr[FM];
-#pragma unroll
-    for (int f = 0; f < FM; ++f) {
-      af[f] = fragment(ca, wm * FM + f, lo, hi);
-      sr[f] = *reinterpret_cast<const FP8Q_LDS float *>(cs + (wm * 16 * FM + f * 16 + l16) * 4);
-    }
-#pragma unroll
-    for (int j = 0; j < FN; ++j) {
-      const v8i bf = fragment(cb, wn * FN + j, lo, hi);
-      const v4f sc =
-          *reinterpret_cast<const FP8Q_LDS v4f *>(cs + (W::kTM + wn * 16 * FN + j * 16 + 4 * kg) * 4);
-#pragma unroll
-      for (int f = 0; f < FM; ++f) {
-        const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
-        const v4f part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bf, af[f], zero, 0, 0, 0, 0, 0, 0);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[f][j][i] = __builtin_fmaf(part[i] * sc[i], sr[f], acc[f][j][i]);
-      }
-    }
-  };
-
-  if (tiles > 0) {
-    load(0, s0);
-    int s = 0;
-    for (; s + 1 < tiles; s += 2) {
-      step(s0, s1, s);
-      step(s1, s0, s + 1);
-    }
-    if (s < tiles) step(s0, s1, s);
-  }
-
-  // Lane 16 kg + r owns row r and columns 4 kg .. 4 kg + 3 of each 16x16 block.
-#pragma unroll
-  for (int f = 0; f < FM; ++f) {
-    const int64_t p = p0 + wm * 16 * FM + f * 16 + l16;
-    if (p >= P) continue;
-    const int64_t base = (static_cast<int64_t>(g) * P + p) * Q;
-#pragma unroll
-    for (int j = 0; j < FN; ++j) {
-      const int64_t q = q0 + wn * 16 * FN + j * 16 + 4 * kg;
-      if (q >= Q) continue;
-      const v4f v = acc[f][j];
-      if (out_f32)
-        *reinterpret_cast<v4f *>(static_cast<float *>(c) + base + q) = v;
-      else
-        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(c) + base + q) =
-            make_uint2(pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3]));
-    }
-  }
+  const int g = logical / (tp * runs), in_g = logical - g * (tp * runs);
+  const int q = in_g % runs * run;
+  wgrad_run<kOutF32>(aq, sa, bq, sb, offsets, G, M, all_tiles, P, Q, g, static_cast<int64_t>(in_g / runs) * kTile,
+                     static_cast<int64_t>(q) * kTile, tq - q < run ? tq - q : run, c, (FP8Q_LDS uint8_t *)stages);
 }
-
-template <int WM, int WN, int FM, int FN>
-__global__ __launch_bounds__(64 * WM * WN, (WM * WN == 8 ? 1 : 2)) void wgrad_kernel(
-    const uint8_t *__restrict__ aq, const float *__restrict__ sa, const uint8_t *__restrict__ bq,
-    const float *__restrict__ sb, const int32_t *__restrict__ offsets, int G, int64_t M, int64_t Mp, int P, int Q,
-    void *__restrict__ c, int out_f32) {
-  __shared__ __attribute__((aligned(1024))) uint8_t stage0[Wgrad<WM, WN, FM, FN>::kStage];
-  __shared__ __attribute__((aligned(1024))) uint8_t stage1[Wgrad<WM, WN, FM, FN>::kStage];
-  wgrad_tile<WM, WN, FM, FN>(aq, sa, bq, sb, offsets, G, M, Mp, P, Q, c, out_f32, (FP8Q_LDS uint8_t *)stage0,
-                             (FP8Q_LDS uint8_t *)stage1);
-}
-
-namespace {
-
-template <int WM, int WN, int FM, int FN>
-hipError_t launch_tiles(const uint8_t *aq, const float *sa, const uint8_t *bq, const float *sb, const int32_t *offsets,
-                        int64_t G, int64_t M, int64_t Mp, int64_t P, int64_t Q, void *c, bool out_f32,
-                        hipStream_t stream) {
-  using W = Wgrad<WM, WN, FM, FN>;
-  const int64_t grid = G * ((P + W::kTM - 1) / W::kTM) * ((Q + W::kTN - 1) / W::kTN);
-  if (grid > 0x7fffffff) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((wgrad_kernel<WM, WN, FM, FN>), dim3(static_cast<uint32_t>(grid)), dim3(64 * WM * WN), 0, stream,
-                     aq, sa, bq, sb, offsets, static_cast<int>(G), M, Mp, static_cast<int>(P), static_cast<int>(Q), c,
-                     out_f32 ? 1 : 0);
-  return hipGetLastError();
-}
-
-}  // namespace
 
 hipError_t launch_grouped_gemm_rowscaled(const uint8_t *aq, const float *sa, const uint8_t *bq, const float *sb,
-                                         const int32_t *offsets, int64_t G, int64_t M, int64_t Mp, int64_t P,
-                                         int64_t Q, void *c, bool out_f32, hipStream_t stream) {
-  return launch_tiles<2, 2, 4, 4>(aq, sa, bq, sb, offsets, G, M, Mp, P, Q, c, out_f32, stream);
+                                         const int32_t *offsets, int64_t G, int64_t M, int64_t P, int64_t Q,
+                                         void *c, bool out_f32, hipStream_t stream) {
+  // Tiles per workgroup, one after the other in a row of tiles: with few tokens per expert the
+  // start of a workgroup (its expert's offsets, the first copies) costs as much as a tile, so a
+  // workgroup takes about 16 token tiles' work as long as four workgroups per slot remain.  32
+  // experts over 8192 rows: 7 tiles instead of one, FP32 1115 -> 1002 us, BF16 690 -> 564 us; 4
+  // experts over 16384 rows, where a tile is 32 token tiles: 7 would cost 365 against 322 us.
+  const int64_t tiles = G * (P / kTile) * (Q / kTile), slots = 2 * device_cu_count();
+  const int64_t depth = M / (128 * G) + 1;  // about the token tiles of an expert
+  const int64_t want = (16 + depth - 1) / depth, most = tiles / (4 * slots);
+  int64_t run = want < most ? want : most;
+  run = run < 1 ? 1 : (run > Q / kTile ? Q / kTile : run);
+  const int64_t grid = G * (P / kTile) * ((Q / kTile + run - 1) / run);
+  if (grid > 0x7fffffff) return hipErrorInvalidValue;
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(grid)), dim3(64 * kWaves), 0, stream, aq, sa, bq, sb, offsets,
+                       static_cast<int>(G), M, M / 128 + G, static_cast<int>(P), static_cast<int>(Q), static_cast<int>(run), c);
+  };
+  out_f32 ? go(wgrad_kernel<true>) : go(wgrad_kernel<false>);
+  return hipGetLastError();
 }
 
 }  // namespace fp8q

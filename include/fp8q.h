@@ -369,17 +369,17 @@ fp8q_status fp8q_swiglu_backward(const uint16_t *gu_bf16, const void *dh, int32_
  * fp8q_quantize_act_dual for rows sorted by expert, of any number per expert.  Token tiles do
  * not cross from one expert to the next: expert g's rows offsets[g] .. offsets[g+1]-1 make
  * ceil(n_g / 128) tiles of 128 tokens, the last one filled up with zeros, and the experts'
- * tiles follow each other in Mp = 128 * (M_tot / 128 + G) columns (integer division), which
- * suffices for every division of M_tot rows among G experts.
+ * tiles follow each other; B = M_tot / 128 + G of them (integer division) suffice for every
+ * division of M_tot rows among G experts.
  *   x_bf16 : [M_tot][K];  offsets : DEVICE int32 [G+1] as in fp8q_grouped_gemm_blockscaled
  *            (every range clamped to [0, M_tot), not checked otherwise; rows from offsets[G] on
  *            belong to no expert and are not read)
  *   xq, sa : 1x128 tiles along K of the experts' rows, as fp8q_quantize_act_1x128 writes them
  *            (xq [M_tot][K], sa [K/128][M_tot]); both NULL leaves them out
- *   xqt    : [K][Mp] E4M3 codes (out), column 128 b + i the token i of tile b
- *   sat    : [Mp/128][K] FP32 scales (out)
+ *   xqt    : [B][K][128] E4M3 codes (out): xqt[b][k][i] is channel k of token i of tile b
+ *   sat    : [B][K] FP32 scales (out)
  * What lies behind the last expert's last tile, and rows of no expert, are left as they were.
- * Requires G >= 1, K % 128 == 0, Mp <= 2^22.  M_tot == 0 or K == 0 is a no-op.
+ * Requires G >= 1, K % 128 == 0, B * K / 128 < 2^31.  M_tot == 0 or K == 0 is a no-op.
  * Errors: FP8Q_ERR_SHAPE, FP8Q_ERR_NULL (also one of xq and sa without the other),
  * FP8Q_ERR_ALIGN, FP8Q_ERR_DEVICE, FP8Q_ERR_LAUNCH.
  */
@@ -389,14 +389,16 @@ fp8q_status fp8q_quantize_act_grouped(const uint16_t *x_bf16, const int32_t *off
 /*
  * The experts' weight gradients dW[g] = dY[g]^T X[g], every expert in one launch:
  *   C[g][p][q] = sum over expert g's token tiles b of
- *                sa[b][p] * sb[b][q] * sum_{k in tile b} decode(aq[p][k]) decode(bq[q][k])
- * with FP32 promotion at every tile of 128 tokens, tiles ascending, as fp8q_gemm_rowscaled;
- * zeros for an expert without rows.
- *   aq [P][Mp], sa [Mp/128][P] and bq [Q][Mp], sb [Mp/128][Q] : from fp8q_quantize_act_grouped
- *   with these offsets, G and M_tot (dW: aq = dY^T codes, bq = X^T codes)
+ *                sa[b][p] * sb[b][q] * sum_i decode(aq[b][p][i]) decode(bq[b][q][i])
+ * with FP32 promotion at every tile of 128 tokens, tiles ascending; zeros for an expert
+ * without rows.  With BF16 output a tile's sum comes from the FP8 matrix instructions (off by
+ * about 1.4e-5 of the sum's norm); with FP32 output the codes are widened to BF16, exactly, and
+ * multiplied by the BF16 instructions, whose sums are good to FP32.
+ *   aq [B][P][128], sa [B][P] and bq [B][Q][128], sb [B][Q], B = M_tot / 128 + G : from
+ *   fp8q_quantize_act_grouped with these offsets, G and M_tot (dW: aq of dY, bq of X)
  *   c [G][P][Q], BF16 or FP32 per out_dtype (out)
- * Requires G >= 1, P % 128 == 0, Q % 128 == 0, M_tot >= 0, Mp <= 2^22.  With M_tot == 0 the
- * operands are not read (they may be NULL) and C is zeros.  P == 0 or Q == 0 is a no-op.
+ * Requires G >= 1, P % 128 == 0, Q % 128 == 0, P and Q <= 2^22, M_tot >= 0.  With M_tot == 0 the operands are not
+ * read (they may be NULL) and C is zeros.  P == 0 or Q == 0 is a no-op.
  * Errors: FP8Q_ERR_DTYPE, FP8Q_ERR_SHAPE, FP8Q_ERR_NULL, FP8Q_ERR_ALIGN, FP8Q_ERR_DEVICE,
  * FP8Q_ERR_LAUNCH.
  */
