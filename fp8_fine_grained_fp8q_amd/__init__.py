@@ -33,7 +33,6 @@ Layouts: xq uint8 [M, K]; sa float32 [K/128, M]; wq uint8 [G, N, K]; sb float32
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -150,21 +149,42 @@ def _need(t: torch.Tensor, dtype, name: str, shape=None):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-@contextlib.contextmanager
-def _on(stream, *tensors):
+class _on:
     """Checks that the tensors are on the current device, and makes `stream` the current one, so
-    that outputs allocated inside belong to the stream that writes them; yields its handle."""
-    device = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != device:
-            raise ValueError(f"tensors must be on the current device cuda:{device}, got {t.device}")
-    if stream is None:
-        yield torch.cuda.current_stream().cuda_stream
-        return
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream))
-    with torch.cuda.stream(stream):
-        yield stream.cuda_stream
+    that outputs allocated inside belong to the stream that writes them; gives its handle."""
+    __slots__ = ("handle", "context")
+
+    def __init__(self, stream, *tensors):
+        device = torch.cuda.current_device()
+        for t in tensors:
+            if t is not None and t.get_device() != device:
+                raise ValueError(f"tensors must be on the current device cuda:{device}, got {t.device}")
+        self.context = None
+        if stream is None:
+            # the current stream's handle; torch.cuda.current_stream() wraps it in an object first,
+            # 3 us of a call that takes 10
+            self.handle = torch._C._cuda_getCurrentRawStream(device)
+            return
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream))
+        self.handle, self.context = stream.cuda_stream, torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self.context is not None:
+            self.context.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        if self.context is not None:
+            self.context.__exit__(*exc)
+
+
+def _out(t, dtype, name: str, shape, like: torch.Tensor):
+    """The caller's output, checked, or a new one on `like`'s device."""
+    if t is None:
+        return like.new_empty(shape, dtype=dtype)
+    _need(t, dtype, name, shape)
+    return t
 
 
 def _need_rows(t, name: str, columns: int = 8, rows=None):
@@ -465,10 +485,8 @@ def fp8q_moe_sort(topk_ids: torch.Tensor, x: torch.Tensor, e_begin: int, n_exper
     if cap < 0 or n_experts < 1:
         raise ValueError("capacity must not be negative and n_experts must be positive")
     with _on(stream, topk_ids, x, xs, row_token) as s:
-        xs = torch.empty((cap, H), dtype=x.dtype, device=x.device) if xs is None else xs
-        row_token = torch.empty(cap, dtype=torch.int32, device=x.device) if row_token is None else row_token
-        _need(xs, x.dtype, "xs", (cap, H))
-        _need(row_token, torch.int32, "row_token", (cap,))
+        xs = _out(xs, x.dtype, "xs", (cap, H), x)
+        row_token = _out(row_token, torch.int32, "row_token", (cap,), x)
         offsets = torch.empty(n_experts + 1, dtype=torch.int32, device=x.device)
         token_row = torch.empty((T, k), dtype=torch.int32, device=x.device)
         _check(load_library().fp8q_moe_sort(_ptr(topk_ids), T, k, e_begin, n_experts, _ptr(x), _out_code(x.dtype), H, cap,
@@ -487,8 +505,7 @@ def fp8q_moe_sort_backward(dxs: torch.Tensor, token_row: torch.Tensor, dx: torch
         raise ValueError("token_row must be 2-D [T, k]")
     (T, k), (cap, H) = token_row.shape, dxs.shape
     with _on(stream, dxs, token_row, dx) as s:
-        dx = torch.empty((T, H), dtype=out_dtype, device=dxs.device) if dx is None else dx
-        _need(dx, dx.dtype, "dx", (T, H))
+        dx = _out(dx, out_dtype if dx is None else dx.dtype, "dx", (T, H), dxs)
         _check(load_library().fp8q_moe_sort_backward(_ptr(dxs), _out_code(dxs.dtype), cap, H, _ptr(token_row), T, k,
                                                      _ptr(dx), _out_code(dx.dtype), s), "fp8q_moe_sort_backward")
     return dx
@@ -512,10 +529,8 @@ def fp8q_moe_combine_backward(dy: torch.Tensor, expert_out: torch.Tensor, token_
         raise ValueError(f"expert_out must be [capacity, {N}], got {tuple(expert_out.shape)}")
     _need(topk_w, torch.float32, "topk_w", (T, k))
     with _on(stream, dy, expert_out, token_row, topk_w, dout, dw) as s:
-        dout = torch.empty_like(expert_out) if dout is None else dout
-        dw = torch.empty_like(topk_w) if dw is None else dw
-        _need(dout, expert_out.dtype, "dout", expert_out.shape)
-        _need(dw, torch.float32, "dw", (T, k))
+        dout = _out(dout, expert_out.dtype, "dout", expert_out.shape, expert_out)
+        dw = _out(dw, torch.float32, "dw", (T, k), topk_w)
         _check(load_library().fp8q_moe_combine_backward(_ptr(dy), _out_code(dy.dtype), _ptr(expert_out),
                                                         _out_code(expert_out.dtype), expert_out.shape[0], N,
                                                         _ptr(token_row), _ptr(topk_w), T, k, _ptr(dout), _ptr(dw), s),
@@ -535,11 +550,9 @@ def fp8q_swiglu_backward(gu: torch.Tensor, dh: torch.Tensor, dgu: torch.Tensor |
     if dh.shape[1] != I:
         raise ValueError(f"dh must be [{M}, {I}], got {tuple(dh.shape)}")
     with _on(stream, gu, dh, dgu, h) as s:
-        dgu = torch.empty_like(gu) if dgu is None else dgu
-        h = torch.empty((M, I), dtype=torch.bfloat16, device=gu.device) if h is None and want_h else h
-        _need(dgu, torch.bfloat16, "dgu", (M, 2 * I))
-        if h is not None:
-            _need(h, torch.bfloat16, "h", (M, I))
+        dgu = _out(dgu, torch.bfloat16, "dgu", (M, 2 * I), gu)
+        if want_h or h is not None:
+            h = _out(h, torch.bfloat16, "h", (M, I), gu)
         _check(load_library().fp8q_swiglu_backward(_ptr(gu), _ptr(dh), _out_code(dh.dtype), M, I, _ptr(dgu), _ptr(h), s),
                "fp8q_swiglu_backward")
     return dgu, h
@@ -561,14 +574,10 @@ def fp8q_quantize_act_grouped(x: torch.Tensor, offsets: torch.Tensor, rows: bool
         raise ValueError("xq and sa are written with rows=True only")
     with _on(stream, x, offsets, xq, sa, xqt, sat) as s:
         if rows:
-            xq = torch.empty((M, K), dtype=torch.uint8, device=x.device) if xq is None else xq
-            sa = torch.empty((K // 128, M), dtype=torch.float32, device=x.device) if sa is None else sa
-            _need(xq, torch.uint8, "xq", (M, K))
-            _need(sa, torch.float32, "sa", (K // 128, M))
-        xqt = torch.empty((tiles, K, 128), dtype=torch.uint8, device=x.device) if xqt is None else xqt
-        sat = torch.empty((tiles, K), dtype=torch.float32, device=x.device) if sat is None else sat
-        _need(xqt, torch.uint8, "xqt", (tiles, K, 128))
-        _need(sat, torch.float32, "sat", (tiles, K))
+            xq = _out(xq, torch.uint8, "xq", (M, K), x)
+            sa = _out(sa, torch.float32, "sa", (K // 128, M), x)
+        xqt = _out(xqt, torch.uint8, "xqt", (tiles, K, 128), x)
+        sat = _out(sat, torch.float32, "sat", (tiles, K), x)
         _check(load_library().fp8q_quantize_act_grouped(_ptr(x), _ptr(offsets), G, M, K, _ptr(xq), _ptr(sa), _ptr(xqt),
                                                         _ptr(sat), s), "fp8q_quantize_act_grouped")
     return xq, sa, xqt, sat
@@ -591,8 +600,7 @@ def fp8q_grouped_gemm_rowscaled(aq, sa, bq, sb, offsets, m_tot: int, out_dtype=t
     _need(sa, torch.float32, "sa", (tiles, P))
     _need(sb, torch.float32, "sb", (tiles, Q))
     with _on(stream, aq, sa, bq, sb, offsets, out) as s:
-        out = torch.empty((G, P, Q), dtype=out_dtype, device=aq.device) if out is None else out
-        _need(out, out.dtype, "out", (G, P, Q))
+        out = _out(out, out_dtype if out is None else out.dtype, "out", (G, P, Q), aq)
         _check(load_library().fp8q_grouped_gemm_rowscaled(_ptr(aq), _ptr(sa), _ptr(bq), _ptr(sb), _ptr(offsets), G,
                                                           int(m_tot), P, Q, _ptr(out), _out_code(out.dtype), s),
                "fp8q_grouped_gemm_rowscaled")

@@ -15,7 +15,7 @@
 // (p 4 + 4, g 4, m and r 1 + 1 each, two scales per 128).  Each thread takes 8 consecutive
 // elements, so a tile of 128 is one 16-lane DPP row; a workgroup takes 2048.  The tensors'
 // addresses and sizes travel in the kernel arguments (no table in device memory to fill,
-// nothing to wait for): up to kMaxTensors of them per launch.
+// nothing to wait for): 76 or 58 of them per launch.
 //
 // Every operation is rounded to FP32 by itself (no contraction), in the order above, so the
 // result is the same as that of separate FP32 operations, bit for bit.
@@ -23,18 +23,39 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "fp8q.h"
 #include "fp8q_device.h"
 #include "fp8q_launch.h"
 
 namespace fp8q {
 
-constexpr int kMaxTensors = 48;
 constexpr int64_t kPerBlock = 2048;
 
+// The descriptors of a launch: as many as its 4 KB of kernel arguments hold.
+struct AdamE4M3 {
+  float *p;
+  const void *grad;
+  void *m, *v;
+  float *m_scale, *v_scale;
+  uint16_t *p_bf16;
+  int64_t n;
+};
+struct AdamF32 {
+  float *p;
+  const void *grad;
+  void *m, *v;
+  uint16_t *p_bf16;
+  int64_t n;
+};
+
+template <bool kE4M3>
 struct AdamTable {
-  fp8q_adamw_tensor t[kMaxTensors];
-  uint32_t first[kMaxTensors + 1];  // first workgroup of each tensor, and the end
+  using Tensor = std::conditional_t<kE4M3, AdamE4M3, AdamF32>;
+  static constexpr int kMax = kE4M3 ? 58 : 76;
+  Tensor t[kMax];
+  uint32_t first[kMax + 1];  // first workgroup of each tensor, and the end
   int count;
 };
 
@@ -46,7 +67,8 @@ struct AdamHyper {
   const float *scalars;  // device {lr, 1 - b1^t, 1 - b2^t, grad_scale} in place of the host's, or null
 };
 
-static_assert(sizeof(AdamTable) + sizeof(AdamHyper) <= 4096, "kernel arguments");
+static_assert(sizeof(AdamTable<true>) + sizeof(AdamHyper) <= 4096, "kernel arguments");
+static_assert(sizeof(AdamTable<false>) + sizeof(AdamHyper) <= 4096, "kernel arguments");
 
 // Values [at, at + 8) of an array of n, zeros past its end.
 template <bool kF32>
@@ -130,7 +152,7 @@ __device__ __forceinline__ uint2 encode8(const float (&x)[8], float &s) {
 }
 
 template <bool kE4M3, bool kGradF32>
-__global__ __launch_bounds__(256) void adamw_kernel(const AdamTable table, const AdamHyper hy) {
+__global__ __launch_bounds__(256) void adamw_kernel(const AdamTable<kE4M3> table, const AdamHyper hy) {
 #pragma clang fp contract(off)
   int lo = 0, hi = table.count - 1;  // the last tensor whose first workgroup is not behind this one
   while (lo < hi) {
@@ -140,7 +162,7 @@ __global__ __launch_bounds__(256) void adamw_kernel(const AdamTable table, const
     else
       hi = mid - 1;
   }
-  const fp8q_adamw_tensor &t = table.t[lo];
+  const auto &t = table.t[lo];
   const int64_t n = t.n;
   const int64_t at = (static_cast<int64_t>(blockIdx.x - table.first[lo]) * 256 + threadIdx.x) * 8;
   float decay = hy.decay, step = hy.step, root = hy.root, scale = hy.grad_scale;
@@ -157,7 +179,7 @@ __global__ __launch_bounds__(256) void adamw_kernel(const AdamTable table, const
   float p[8], g[8], m[8], v[8];
   load8_tail<true>(t.p, at, n, p);
   load8_tail<kGradF32>(t.grad, at, n, g);
-  if (kE4M3) {
+  if constexpr (kE4M3) {
     const int64_t tile = at >> 7;
     decode8(load_codes(static_cast<const uint8_t *>(t.m), at, n), t.m_scale[tile], m);
     decode8(load_codes(static_cast<const uint8_t *>(t.v), at, n), t.v_scale[tile], v);
@@ -178,7 +200,7 @@ __global__ __launch_bounds__(256) void adamw_kernel(const AdamTable table, const
   }
   store8_tail<true>(t.p, at, n, p);
   if (t.p_bf16 != nullptr) store8_tail<false>(t.p_bf16, at, n, p);
-  if (kE4M3) {
+  if constexpr (kE4M3) {
     // elements past the end are zeros in every array, so they change no maximum
     float ms, vs;
     const uint2 mq = encode8<false>(m, ms), vq = encode8<true>(r, vs);
@@ -193,6 +215,41 @@ __global__ __launch_bounds__(256) void adamw_kernel(const AdamTable table, const
     store8_tail<true>(t.v, at, n, v);
   }
 }
+
+namespace {
+
+AdamE4M3 descriptor(const fp8q_adamw_tensor &t, const AdamE4M3 *) {
+  return {t.p, t.grad, t.m, t.v, t.m_scale, t.v_scale, t.p_bf16, t.n};
+}
+AdamF32 descriptor(const fp8q_adamw_tensor &t, const AdamF32 *) { return {t.p, t.grad, t.m, t.v, t.p_bf16, t.n}; }
+
+template <bool kE4M3>
+hipError_t launch_batches(const fp8q_adamw_tensor *tensors, int64_t count, bool grad_f32, const AdamHyper &hy,
+                          hipStream_t stream) {
+  for (int64_t i = 0; i < count;) {
+    AdamTable<kE4M3> table;
+    table.count = 0;
+    int64_t blocks = 0;
+    for (; i < count && table.count < AdamTable<kE4M3>::kMax; ++i) {
+      const int64_t b = (tensors[i].n + kPerBlock - 1) / kPerBlock;
+      if (b == 0) continue;
+      if (blocks + b > 0x7fffffff) break;  // the caller has checked that one tensor fits
+      table.t[table.count] = descriptor(tensors[i], table.t);
+      table.first[table.count++] = static_cast<uint32_t>(blocks);
+      blocks += b;
+    }
+    if (table.count == 0) continue;
+    table.first[table.count] = static_cast<uint32_t>(blocks);
+    const dim3 grid(static_cast<uint32_t>(blocks)), block(256);
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, table, hy); };
+    grad_f32 ? go(adamw_kernel<kE4M3, true>) : go(adamw_kernel<kE4M3, false>);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace
 
 hipError_t launch_adamw(const fp8q_adamw_tensor *tensors, int64_t count, bool grad_f32, bool e4m3,
                         const fp8q_adamw_hyper &h, hipStream_t stream) {
@@ -209,30 +266,8 @@ hipError_t launch_adamw(const fp8q_adamw_tensor *tensors, int64_t count, bool gr
   hy.root = static_cast<float>(1.0 / sqrt(1.0 - pow(h.beta2, static_cast<double>(h.step))));
   hy.grad_scale = static_cast<float>(h.grad_scale);
   hy.scalars = h.scalars;
-  for (int64_t i = 0; i < count;) {
-    AdamTable table;
-    table.count = 0;
-    int64_t blocks = 0;
-    for (; i < count && table.count < kMaxTensors; ++i) {
-      const int64_t b = (tensors[i].n + kPerBlock - 1) / kPerBlock;
-      if (b == 0) continue;
-      if (blocks + b > 0x7fffffff) break;  // the caller has checked that one tensor fits
-      table.t[table.count] = tensors[i];
-      table.first[table.count++] = static_cast<uint32_t>(blocks);
-      blocks += b;
-    }
-    if (table.count == 0) continue;
-    table.first[table.count] = static_cast<uint32_t>(blocks);
-    const dim3 grid(static_cast<uint32_t>(blocks)), block(256);
-    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, table, hy); };
-    if (e4m3)
-      grad_f32 ? go(adamw_kernel<true, true>) : go(adamw_kernel<true, false>);
-    else
-      grad_f32 ? go(adamw_kernel<false, true>) : go(adamw_kernel<false, false>);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  return hipSuccess;
+  return e4m3 ? launch_batches<true>(tensors, count, grad_f32, hy, stream)
+              : launch_batches<false>(tensors, count, grad_f32, hy, stream);
 }
 
 }  // namespace fp8q

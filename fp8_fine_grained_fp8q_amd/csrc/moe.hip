@@ -295,6 +295,75 @@ __global__ __launch_bounds__(256) void moe_spread_kernel(const uint4 *__restrict
   }
 }
 
+// The whole sort of at most kSmallSort entries in one launch (a lone routing chunk: the routing
+// kernel and the copy would be two).  Every workgroup holds all local expert indices in LDS and
+// finds its token's rows by counting, row = the entries of an earlier expert, or of the same
+// one and earlier in order: one ballot per 64 entries and slot.  The last workgroup counts the
+// offsets.  64 tokens x 8 slots x 7168 BF16 columns: 14.3 -> see the figures at launch_moe_sort.
+constexpr int kSmallSort = 2 * static_cast<int>(kChunk) - 1;
+
+__global__ __launch_bounds__(256) void moe_sort_small_kernel(const int32_t *__restrict__ ids, int n, int k,
+                                                             int64_t e_begin, int E, const uint4 *__restrict__ x,
+                                                             int64_t chunks, int segs, int64_t cap,
+                                                             uint4 *__restrict__ xs, int32_t *__restrict__ offsets,
+                                                             int32_t *__restrict__ token_row,
+                                                             int32_t *__restrict__ row_token) {
+  __shared__ int32_t key[kSmallSort + 1];  // local expert index, E where there is none
+  __shared__ int32_t rows[64];
+  __shared__ int32_t hist[kMaxLocalExperts + 1];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  for (int i = tid; i < n; i += 256) {
+    const int e = local_expert(ids, i, n, e_begin, E);
+    key[i] = e < 0 ? E : e;
+  }
+  if (blockIdx.x == gridDim.x - 1) {  // offsets[e] = the entries of the experts before e
+    for (int e = tid; e <= E; e += 256) hist[e] = 0;
+    __syncthreads();
+    for (int i = tid; i < n; i += 256) atomicAdd(&hist[key[i]], 1);
+    __syncthreads();
+    if (wave != 0) return;
+    int before = 0;
+    for (int e0 = 0; e0 <= E; e0 += 64) {
+      const int e = e0 + lane, own = e < E ? hist[e] : 0;
+      int sum = own;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int u = __shfl_up(sum, d);
+        sum += lane >= d ? u : 0;
+      }
+      if (e <= E) offsets[e] = before + sum - own;
+      before += __shfl(sum, 63);
+    }
+    return;
+  }
+  __syncthreads();
+  const int t = blockIdx.x / segs, seg = blockIdx.x % segs;
+  for (int s = wave; s < k; s += 4) {
+    const int i = t * k + s, own = key[i];
+    int row = 0;
+    for (int j0 = 0; own < E && j0 < n; j0 += 64) {
+      const int j = j0 + lane, e = j < n ? key[j] : E;
+      row += __popcll(__ballot(e < own || (e == own && j < i)));
+    }
+    if (own >= E || row >= cap) row = -1;
+    if (lane == 0) {
+      rows[s] = row;
+      if (seg == 0) {
+        token_row[i] = row;
+        if (row >= 0) row_token[row] = t;
+      }
+    }
+  }
+  __syncthreads();
+  const int64_t c = static_cast<int64_t>(seg) * 256 + tid;
+  if (c >= chunks) return;
+  const uint4 v = x[t * chunks + c];
+  for (int s = 0; s < k; ++s) {
+    const int64_t r = rows[s];
+    if (r >= 0) xs[r * chunks + c] = v;
+  }
+}
+
 // Gradient of the sort: dx[t] = sum over the token's slots with a row of dxs[row], FP32, in
 // slot order, rounded once.  A workgroup takes 256 chunks of 8 columns of one token.
 template <bool kInF32, bool kOutF32>
@@ -390,7 +459,15 @@ hipError_t launch_moe_sort(const int32_t *ids, int64_t T, int64_t k, int64_t e_b
                            bool f32, int64_t H, int64_t cap, void *xs, int32_t *offsets, int32_t *token_row,
                            int32_t *row_token, hipStream_t stream) {
   const int64_t chunks = H / (f32 ? 4 : 8), segs = (chunks + 255) / 256;
-  if (T * segs > 0x7fffffff) return hipErrorInvalidValue;
+  if (T * segs > 0x7ffffffe) return hipErrorInvalidValue;
+  if (E < 1 || E > kMaxLocalExperts) return hipErrorInvalidValue;
+  if (T * k <= kSmallSort && segs > 0) {
+    hipLaunchKernelGGL(moe_sort_small_kernel, dim3(static_cast<uint32_t>(T * segs + 1)), dim3(256), 0, stream, ids,
+                       static_cast<int>(T * k), static_cast<int>(k), e_begin, static_cast<int>(E),
+                       static_cast<const uint4 *>(x), chunks, static_cast<int>(segs), cap, static_cast<uint4 *>(xs),
+                       offsets, token_row, row_token);
+    return hipGetLastError();
+  }
   hipError_t e = launch_route(ids, T, k, e_begin, E, cap, offsets, token_row, row_token, stream);
   if (e != hipSuccess || cap == 0 || T * segs == 0) return e;
   hipLaunchKernelGGL(moe_spread_kernel, dim3(static_cast<uint32_t>(T * segs)), dim3(256), 0, stream,

@@ -427,7 +427,7 @@ fp8q_status fp8q_grouped_gemm_rowscaled(const uint8_t *aq, const float *sa, cons
  *           every number finite.  `scalars`, if not NULL, is a DEVICE float[4] = {lr,
  *           1 - beta1^t, 1 - beta2^t, grad_scale} read by the kernels in place of lr, step and
  *           grad_scale, so that a captured step can be replayed with new values.
- * Launches: one per 48 nonempty tensors.  Gradients are finite (else unspecified, and an E4M3
+ * Launches: one per 76 nonempty tensors (58 with E4M3 states).  Gradients are finite (else unspecified, and an E4M3
  * tile shares the damage).  Errors: FP8Q_ERR_DTYPE, FP8Q_ERR_VALUE, FP8Q_ERR_SHAPE (n < 0 or
  * n >= 2^40), FP8Q_ERR_NULL, FP8Q_ERR_ALIGN (scales and scalars 4-byte, the rest 16-byte),
  * FP8Q_ERR_DEVICE, FP8Q_ERR_LAUNCH.
