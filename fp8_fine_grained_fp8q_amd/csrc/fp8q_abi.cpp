@@ -299,7 +299,7 @@ fp8q_status fp8q_quantize_act_grouped(const uint16_t *x_bf16, const int32_t *off
                                       int64_t K, uint8_t *xq, float *sa, uint8_t *xqt, float *sat, void *stream) {
   if (G < 1 || bad_dim(G) || bad_dim(M_tot) || bad_dim(K) || K % 128 != 0 || too_many(M_tot, K))
     return FP8Q_ERR_SHAPE;
-  if (too_many(M_tot / 128 + G, K) || (M_tot / 128 + G) * (K / 128) >= kMaxDim) return FP8Q_ERR_SHAPE;
+  if (too_many(M_tot / 128 + G, K) || (M_tot / 128 + G) * (K / 64) >= kMaxDim) return FP8Q_ERR_SHAPE;
   if (M_tot == 0 || K == 0) return FP8Q_OK;
   if (!x_bf16 || !offsets || !xqt || !sat || !xq != !sa) return FP8Q_ERR_NULL;
   if (misaligned(x_bf16) || misaligned(offsets, 4) || misaligned(xq) || misaligned(sa) || misaligned(xqt) ||

@@ -135,14 +135,14 @@ __device__ __forceinline__ void wgrad_run(const uint8_t *__restrict__ aq, const 
   const int wm = wave >> 1, wn = wave & 1;
   const int l32 = lane & 31, half = lane >> 5;
 
-  int64_t first64, tiles64;
-  int rest;
-  tiles_of_expert(offsets, G, M, g, first64, tiles64, rest);
+  int64_t first64;
+  int tiles, rest;
+  tiles_of_expert(offsets, G, M, g, first64, tiles, rest);
   // valid offsets never reach past the last tile; others are kept inside the operands
-  const int64_t end64 = first64 + tiles64 < all_tiles ? first64 + tiles64 : all_tiles;
-  const int tiles = __builtin_amdgcn_readfirstlane(static_cast<int>(end64 > first64 ? end64 - first64 : 0));
-  const int first = __builtin_amdgcn_readfirstlane(static_cast<int>(tiles > 0 ? first64 : 0));
-  const int last = __builtin_amdgcn_readfirstlane((rest + 31) / 32);
+  const int64_t room = all_tiles - first64;
+  tiles = room <= 0 ? 0 : (tiles < room ? tiles : static_cast<int>(room));
+  const int first = tiles > 0 ? static_cast<int>(first64) : 0;
+  const int last = (rest + 31) / 32;
 
   // Copies: an operand's 16 KB stage is contiguous in memory.  1 KB block b = 8 i + wave of it
   // in LDS holds 8 of a row group's 16 rows; lane l lands on line 4 (b % 2) + l / 16, half (l / 8)

@@ -379,7 +379,7 @@ fp8q_status fp8q_swiglu_backward(const uint16_t *gu_bf16, const void *dh, int32_
  *   xqt    : [B][K][128] E4M3 codes (out): xqt[b][k][i] is channel k of token i of tile b
  *   sat    : [B][K] FP32 scales (out)
  * What lies behind the last expert's last tile, and rows of no expert, are left as they were.
- * Requires G >= 1, K % 128 == 0, B * K / 128 < 2^31.  M_tot == 0 or K == 0 is a no-op.
+ * Requires G >= 1, K % 128 == 0, B * K / 64 < 2^31.  M_tot == 0 or K == 0 is a no-op.
  * Errors: FP8Q_ERR_SHAPE, FP8Q_ERR_NULL (also one of xq and sa without the other),
  * FP8Q_ERR_ALIGN, FP8Q_ERR_DEVICE, FP8Q_ERR_LAUNCH.
  */
