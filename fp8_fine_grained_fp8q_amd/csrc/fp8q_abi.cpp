@@ -318,7 +318,7 @@ fp8q_status fp8q_grouped_gemm_rowscaled(const uint8_t *aq, const float *sa, cons
     return FP8Q_ERR_SHAPE;
   if (P > kMaxGemmK || Q > kMaxGemmK) return FP8Q_ERR_SHAPE;  // 32-bit offsets within a tile's rows
   if (too_many(G, P) || too_many(G * P, Q)) return FP8Q_ERR_SHAPE;
-  if (G * (P / 128) * (Q / 128) >= kMaxDim || M_tot / 128 + G >= kMaxDim) return FP8Q_ERR_SHAPE;
+  if (G * ((P / 128) * (Q / 128) + 7) >= kMaxDim || M_tot / 128 + G >= kMaxDim) return FP8Q_ERR_SHAPE;
   if (P == 0 || Q == 0) return FP8Q_OK;
   if (!c || !offsets || (M_tot > 0 && (!aq || !sa || !bq || !sb))) return FP8Q_ERR_NULL;
   if (misaligned(aq) || misaligned(sa) || misaligned(bq) || misaligned(sb) || misaligned(offsets, 4) || misaligned(c))

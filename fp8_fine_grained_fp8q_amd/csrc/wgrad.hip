@@ -16,13 +16,14 @@
 // output widens the codes to BF16, exactly, and takes the BF16 instructions (8e-9), at half
 // their rate.
 //
-// Two regimes, measured on one MI355X (product alone, without the quantizers):
+// Two regimes, measured on one MI355X (product alone, behind its quantizers):
 //  * few tokens per expert: the gradient's bytes.  32 experts of 4096 x 7168 over 8192 rows: FP32
-//    1002 us (3.75 TB/s of 3.76 GB), BF16 564 us; stores alone take 650 and 366 us, the loads
-//    and products alone about 780 and 455 us, and the two overlap only in part.
-//  * many: the matrix cores beside the two vector operations per element.  4 experts of 7168 x
-//    2048 over 16384 rows: BF16 output 322 us (1.50 PFLOP/s), FP32 540 us; one expert of 7168 x
-//    7168 over 4096 rows 282 us (1.49 PFLOP/s).
+//    870 us (4.3 TB/s of 3.76 GB), BF16 534 us.  Stores alone take 650 and 366 us, loads and
+//    products alone about 700 and 450; the two overlap only in part.
+//  * many: the matrix cores and the vector units.  4 experts of 7168 x 2048 over 16384 rows: BF16
+//    output 310 us (1.55 PFLOP/s), FP32 520 us.  Beside the FP8 instructions the vector unit
+//    issues once in 8 cycles (without them, in 4 to 5), so the two operations per element
+//    take half as long again as the products; the time is near the sum of the two.
 //
 // A workgroup of 8 waves computes 128 x 128 tiles of one expert, 32 x 64 per wave in 32x32 blocks,
 // two workgroups per CU, so that one's loads and stores run beside the other's products.
@@ -312,16 +313,19 @@ __global__ __launch_bounds__(64 * kWaves, 4) void wgrad_kernel(
     const float *__restrict__ sb, const int32_t *__restrict__ offsets, int G, int64_t M, int64_t all_tiles, int P,
     int Q, int run, void *__restrict__ c) {
   __shared__ __attribute__((aligned(1024))) uint8_t stages[2 * kStage];
-  // Workgroups are dealt round-robin to the 8 XCDs; each XCD gets a contiguous piece of the
-  // runs, ordered by expert, then by rows, then by columns: neighbouring workgroups write
-  // neighbouring parts of the same rows.
+  // Workgroups are dealt round-robin to the 8 XCDs.  Each XCD gets a contiguous eighth of every
+  // expert's runs, four rows of tiles at a time, column by column: neighbouring workgroups share
+  // operands in their L2 and write neighbouring parts of the same rows, and experts of different sizes load
+  // all XCDs alike (whole experts per XCD: 4 uneven experts over 16384 rows 350 us instead of
+  // 314 us).  Workgroups past an expert's last run exit.
   const int tp = P / kTile, tq = Q / kTile, runs = (tq + run - 1) / run;
-  const int total = gridDim.x, per = total / 8, rem = total % 8;
+  const int per = (tp * runs + 7) / 8;
   const int xcd = blockIdx.x % 8, idx = blockIdx.x / 8;
-  const int logical = xcd * per + (xcd < rem ? xcd : rem) + idx;
-  const int g = logical / (tp * runs), in_g = logical - g * (tp * runs);
-  const int q = in_g % runs * run;
-  wgrad_run<kOutF32>(aq, sa, bq, sb, offsets, G, M, all_tiles, P, Q, g, static_cast<int64_t>(in_g / runs) * kTile,
+  const int g = idx / per, in_g = xcd * per + idx % per;
+  if (in_g >= tp * runs) return;
+  const int span = 4 * runs, first = in_g / span * 4, high = tp - first < 4 ? tp - first : 4, in_s = in_g % span;
+  const int p = first + in_s % high, q = in_s / high * run;
+  wgrad_run<kOutF32>(aq, sa, bq, sb, offsets, G, M, all_tiles, P, Q, g, static_cast<int64_t>(p) * kTile,
                      static_cast<int64_t>(q) * kTile, tq - q < run ? tq - q : run, c, (FP8Q_LDS uint8_t *)stages);
 }
 
@@ -330,15 +334,16 @@ hipError_t launch_grouped_gemm_rowscaled(const uint8_t *aq, const float *sa, con
                                          void *c, bool out_f32, hipStream_t stream) {
   // Tiles per workgroup, one after the other in a row of tiles: with few tokens per expert the
   // start of a workgroup (its expert's offsets, the first copies) costs as much as a tile, so a
-  // workgroup takes about 16 token tiles' work as long as four workgroups per slot remain.  32
-  // experts over 8192 rows: 7 tiles instead of one, FP32 1115 -> 1002 us, BF16 690 -> 564 us; 4
-  // experts over 16384 rows, where a tile is 32 token tiles: 7 would cost 365 against 322 us.
+  // workgroup takes about 8 token tiles' work as long as four workgroups per slot remain.  32
+  // experts over 8192 rows: 3 tiles instead of one, FP32
+  // 940 -> 870 us, BF16 622 -> 534 us; 4 experts over 16384 rows, where a tile is
+  // 32 token tiles: one instead of 3, BF16 345 -> 310 us.
   const int64_t tiles = G * (P / kTile) * (Q / kTile), slots = 2 * device_cu_count();
   const int64_t depth = M / (128 * G) + 1;  // about the token tiles of an expert
-  const int64_t want = (16 + depth - 1) / depth, most = tiles / (4 * slots);
+  const int64_t want = (8 + depth - 1) / depth, most = tiles / (4 * slots);
   int64_t run = want < most ? want : most;
   run = run < 1 ? 1 : (run > Q / kTile ? Q / kTile : run);
-  const int64_t grid = G * (P / kTile) * ((Q / kTile + run - 1) / run);
+  const int64_t grid = 8 * G * (((P / kTile) * ((Q / kTile + run - 1) / run) + 7) / 8);
   if (grid > 0x7fffffff) return hipErrorInvalidValue;
   auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(grid)), dim3(64 * kWaves), 0, stream, aq, sa, bq, sb, offsets,
