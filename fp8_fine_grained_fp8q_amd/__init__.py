@@ -145,54 +145,42 @@ def _check(status: int, what: str):
 def _need(t: torch.Tensor, dtype, name: str, shape=None):
     if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-class _on:
-    """Checks that the tensors are on the current device, and makes `stream` the current one, so
-    that outputs allocated inside belong to the stream that writes them; gives its handle."""
-    __slots__ = ("handle", "context")
+def _here(*tensors) -> int:
+    """Checks that the tensors are on the current device; the current stream's handle.
+    (torch.cuda.current_stream() wraps it in an object first, 3 us of a call that takes 8.)"""
+    device = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and (not isinstance(t, torch.Tensor) or t.get_device() != device):
+            raise ValueError(f"tensors must be on the current device cuda:{device}, got {getattr(t, 'device', type(t))}")
+    return torch._C._cuda_getCurrentRawStream(device)
 
-    def __init__(self, stream, *tensors):
-        device = torch.cuda.current_device()
-        for t in tensors:
-            if t is not None and t.get_device() != device:
-                raise ValueError(f"tensors must be on the current device cuda:{device}, got {t.device}")
-        self.context = None
-        if stream is None:
-            # the current stream's handle; torch.cuda.current_stream() wraps it in an object first,
-            # 3 us of a call that takes 10
-            self.handle = torch._C._cuda_getCurrentRawStream(device)
-            return
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream))
-        self.handle, self.context = stream.cuda_stream, torch.cuda.stream(stream)
 
-    def __enter__(self):
-        if self.context is not None:
-            self.context.__enter__()
-        return self.handle
-
-    def __exit__(self, *exc):
-        if self.context is not None:
-            self.context.__exit__(*exc)
+def _on(stream):
+    """`stream` (a torch stream or a handle) as the current one, so that what is allocated inside
+    belongs to the stream that writes it."""
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
 
 
 def _out(t, dtype, name: str, shape, like: torch.Tensor):
     """The caller's output, checked, or a new one on `like`'s device."""
     if t is None:
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty_like(like) if shape == like.shape and dtype == like.dtype else like.new_empty(shape, dtype=dtype)
     _need(t, dtype, name, shape)
     return t
 
 
 def _need_rows(t, name: str, columns: int = 8, rows=None):
     """A contiguous bf16 or float32 [rows, C] with C a multiple of `columns`."""
-    if not isinstance(t, torch.Tensor) or t.dtype not in (torch.bfloat16, torch.float32):
+    if not isinstance(t, torch.Tensor) or (t.dtype != torch.bfloat16 and t.dtype != torch.float32):
         raise ValueError(f"{name} must be a bfloat16 or float32 tensor")
-    _need(t, t.dtype, name)
-    if t.dim() != 2 or t.shape[1] % columns or (rows is not None and t.shape[0] != rows):
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    shape = t.shape
+    if len(shape) != 2 or shape[1] % columns or (rows is not None and shape[0] != rows):
         raise ValueError(f"{name} must be [{'rows' if rows is None else rows}, C] with C a multiple of {columns}, "
                          f"got {tuple(t.shape)}")
 
@@ -475,6 +463,9 @@ def fp8q_moe_sort(topk_ids: torch.Tensor, x: torch.Tensor, e_begin: int, n_exper
     token_row int32 [T, k], row_token int32 [capacity]), the maps as fp8q_moe_dispatch gives
     them; capacity defaults to xs's rows, or to T*k.  Rows of xs and row_token behind the last
     routed one are left as they were."""
+    if stream is not None:
+        with _on(stream):
+            return fp8q_moe_sort(topk_ids, x, e_begin, n_experts, capacity, xs, row_token)
     _need(topk_ids, torch.int32, "topk_ids")
     if topk_ids.dim() != 2:
         raise ValueError("topk_ids must be 2-D [T, k]")
@@ -484,14 +475,14 @@ def fp8q_moe_sort(topk_ids: torch.Tensor, x: torch.Tensor, e_begin: int, n_exper
     cap = int(capacity) if capacity is not None else (xs.shape[0] if xs is not None else T * k)
     if cap < 0 or n_experts < 1:
         raise ValueError("capacity must not be negative and n_experts must be positive")
-    with _on(stream, topk_ids, x, xs, row_token) as s:
-        xs = _out(xs, x.dtype, "xs", (cap, H), x)
-        row_token = _out(row_token, torch.int32, "row_token", (cap,), x)
-        offsets = torch.empty(n_experts + 1, dtype=torch.int32, device=x.device)
-        token_row = torch.empty((T, k), dtype=torch.int32, device=x.device)
-        _check(load_library().fp8q_moe_sort(_ptr(topk_ids), T, k, e_begin, n_experts, _ptr(x), _out_code(x.dtype), H, cap,
-                                            _ptr(xs), _ptr(offsets), _ptr(token_row), _ptr(row_token), s),
-               "fp8q_moe_sort")
+    s = _here(topk_ids, x, xs, row_token)
+    xs = _out(xs, x.dtype, "xs", (cap, H), x)
+    row_token = _out(row_token, torch.int32, "row_token", (cap,), x)
+    offsets = torch.empty(n_experts + 1, dtype=torch.int32, device=x.device)
+    token_row = torch.empty((T, k), dtype=torch.int32, device=x.device)
+    _check(load_library().fp8q_moe_sort(_ptr(topk_ids), T, k, e_begin, n_experts, _ptr(x), _out_code(x.dtype), H, cap,
+                                        _ptr(xs), _ptr(offsets), _ptr(token_row), _ptr(row_token), s),
+           "fp8q_moe_sort")
     return xs, offsets, token_row, row_token
 
 
@@ -499,15 +490,18 @@ def fp8q_moe_sort_backward(dxs: torch.Tensor, token_row: torch.Tensor, dx: torch
                            out_dtype=torch.bfloat16, stream=None):
     """Gradient of the sort: dx[t] = sum over the token's rows of dxs[row] (dxs bf16 or float32
     [capacity, H], token_row int32 [T, k]) -> dx [T, H] in out_dtype."""
+    if stream is not None:
+        with _on(stream):
+            return fp8q_moe_sort_backward(dxs, token_row, dx, out_dtype)
     _need_rows(dxs, "dxs")
     _need(token_row, torch.int32, "token_row")
     if token_row.dim() != 2:
         raise ValueError("token_row must be 2-D [T, k]")
     (T, k), (cap, H) = token_row.shape, dxs.shape
-    with _on(stream, dxs, token_row, dx) as s:
-        dx = _out(dx, out_dtype if dx is None else dx.dtype, "dx", (T, H), dxs)
-        _check(load_library().fp8q_moe_sort_backward(_ptr(dxs), _out_code(dxs.dtype), cap, H, _ptr(token_row), T, k,
-                                                     _ptr(dx), _out_code(dx.dtype), s), "fp8q_moe_sort_backward")
+    s = _here(dxs, token_row, dx)
+    dx = _out(dx, out_dtype if dx is None else dx.dtype, "dx", (T, H), dxs)
+    _check(load_library().fp8q_moe_sort_backward(_ptr(dxs), _out_code(dxs.dtype), cap, H, _ptr(token_row), T, k,
+                                                 _ptr(dx), _out_code(dx.dtype), s), "fp8q_moe_sort_backward")
     return dx
 
 
@@ -518,6 +512,9 @@ def fp8q_moe_combine_backward(dy: torch.Tensor, expert_out: torch.Tensor, token_
     each), token_row int32 / topk_w float32 [T, k] -> (dout like expert_out with dout[row] =
     topk_w[t, s] * dy[t], dw float32 [T, k] with dw[t, s] = <expert_out[row], dy[t]>).  Rows of
     dout without a slot are left as they were; dw is 0 for slots without a row."""
+    if stream is not None:
+        with _on(stream):
+            return fp8q_moe_combine_backward(dy, expert_out, token_row, topk_w, dout, dw)
     _need(token_row, torch.int32, "token_row")
     if token_row.dim() != 2:
         raise ValueError("token_row must be 2-D [T, k]")
@@ -528,13 +525,13 @@ def fp8q_moe_combine_backward(dy: torch.Tensor, expert_out: torch.Tensor, token_
     if expert_out.shape[1] != N:
         raise ValueError(f"expert_out must be [capacity, {N}], got {tuple(expert_out.shape)}")
     _need(topk_w, torch.float32, "topk_w", (T, k))
-    with _on(stream, dy, expert_out, token_row, topk_w, dout, dw) as s:
-        dout = _out(dout, expert_out.dtype, "dout", expert_out.shape, expert_out)
-        dw = _out(dw, torch.float32, "dw", (T, k), topk_w)
-        _check(load_library().fp8q_moe_combine_backward(_ptr(dy), _out_code(dy.dtype), _ptr(expert_out),
-                                                        _out_code(expert_out.dtype), expert_out.shape[0], N,
-                                                        _ptr(token_row), _ptr(topk_w), T, k, _ptr(dout), _ptr(dw), s),
-               "fp8q_moe_combine_backward")
+    s = _here(dy, expert_out, token_row, topk_w, dout, dw)
+    dout = _out(dout, expert_out.dtype, "dout", expert_out.shape, expert_out)
+    dw = _out(dw, torch.float32, "dw", (T, k), topk_w)
+    _check(load_library().fp8q_moe_combine_backward(_ptr(dy), _out_code(dy.dtype), _ptr(expert_out),
+                                                    _out_code(expert_out.dtype), expert_out.shape[0], N,
+                                                    _ptr(token_row), _ptr(topk_w), T, k, _ptr(dout), _ptr(dw), s),
+           "fp8q_moe_combine_backward")
     return dout, dw
 
 
@@ -542,6 +539,9 @@ def fp8q_swiglu_backward(gu: torch.Tensor, dh: torch.Tensor, dgu: torch.Tensor |
                          h: torch.Tensor | None = None, want_h: bool = False, stream=None):
     """Gradient of h = SiLU(g) * u: gu bf16 [M, 2I] (g | u), dh bf16 or float32 [M, I] -> (dgu bf16
     [M, 2I], h bf16 [M, I] if want_h or a buffer for it is given, else None)."""
+    if stream is not None:
+        with _on(stream):
+            return fp8q_swiglu_backward(gu, dh, dgu, h, want_h)
     _need(gu, torch.bfloat16, "gu")
     if gu.dim() != 2 or gu.shape[1] % 16:
         raise ValueError(f"gu must be [M, 2I] with I a multiple of 8, got {tuple(gu.shape)}")
@@ -549,12 +549,12 @@ def fp8q_swiglu_backward(gu: torch.Tensor, dh: torch.Tensor, dgu: torch.Tensor |
     _need_rows(dh, "dh", rows=M)
     if dh.shape[1] != I:
         raise ValueError(f"dh must be [{M}, {I}], got {tuple(dh.shape)}")
-    with _on(stream, gu, dh, dgu, h) as s:
-        dgu = _out(dgu, torch.bfloat16, "dgu", (M, 2 * I), gu)
-        if want_h or h is not None:
-            h = _out(h, torch.bfloat16, "h", (M, I), gu)
-        _check(load_library().fp8q_swiglu_backward(_ptr(gu), _ptr(dh), _out_code(dh.dtype), M, I, _ptr(dgu), _ptr(h), s),
-               "fp8q_swiglu_backward")
+    s = _here(gu, dh, dgu, h)
+    dgu = _out(dgu, torch.bfloat16, "dgu", (M, 2 * I), gu)
+    if want_h or h is not None:
+        h = _out(h, torch.bfloat16, "h", (M, I), gu)
+    _check(load_library().fp8q_swiglu_backward(_ptr(gu), _ptr(dh), _out_code(dh.dtype), M, I, _ptr(dgu), _ptr(h), s),
+           "fp8q_swiglu_backward")
     return dgu, h
 
 
@@ -563,6 +563,9 @@ def fp8q_quantize_act_grouped(x: torch.Tensor, offsets: torch.Tensor, rows: bool
     """x bf16 [M, K] sorted by expert, offsets int32 [G + 1] -> (xq uint8 [M, K], sa float32
     [K/128, M], xqt uint8 [B, K, 128], sat float32 [B, K]) with B = M // 128 + G: 1x128 tiles
     along K (None, None with rows=False) and tiles of 128 tokens of one expert."""
+    if stream is not None:
+        with _on(stream):
+            return fp8q_quantize_act_grouped(x, offsets, rows, xq, sa, xqt, sat)
     _need(x, torch.bfloat16, "x")
     _need(offsets, torch.int32, "offsets")
     if x.dim() != 2 or x.shape[1] % 128 or offsets.dim() != 1 or offsets.shape[0] < 2:
@@ -572,14 +575,14 @@ def fp8q_quantize_act_grouped(x: torch.Tensor, offsets: torch.Tensor, rows: bool
     tiles = M // 128 + G
     if not rows and (xq is not None or sa is not None):
         raise ValueError("xq and sa are written with rows=True only")
-    with _on(stream, x, offsets, xq, sa, xqt, sat) as s:
-        if rows:
-            xq = _out(xq, torch.uint8, "xq", (M, K), x)
-            sa = _out(sa, torch.float32, "sa", (K // 128, M), x)
-        xqt = _out(xqt, torch.uint8, "xqt", (tiles, K, 128), x)
-        sat = _out(sat, torch.float32, "sat", (tiles, K), x)
-        _check(load_library().fp8q_quantize_act_grouped(_ptr(x), _ptr(offsets), G, M, K, _ptr(xq), _ptr(sa), _ptr(xqt),
-                                                        _ptr(sat), s), "fp8q_quantize_act_grouped")
+    s = _here(x, offsets, xq, sa, xqt, sat)
+    if rows:
+        xq = _out(xq, torch.uint8, "xq", (M, K), x)
+        sa = _out(sa, torch.float32, "sa", (K // 128, M), x)
+    xqt = _out(xqt, torch.uint8, "xqt", (tiles, K, 128), x)
+    sat = _out(sat, torch.float32, "sat", (tiles, K), x)
+    _check(load_library().fp8q_quantize_act_grouped(_ptr(x), _ptr(offsets), G, M, K, _ptr(xq), _ptr(sa), _ptr(xqt),
+                                                    _ptr(sat), s), "fp8q_quantize_act_grouped")
     return xq, sa, xqt, sat
 
 
@@ -588,6 +591,9 @@ def fp8q_grouped_gemm_rowscaled(aq, sa, bq, sb, offsets, m_tot: int, out_dtype=t
     """The experts' weight gradients C [G, P, Q]: C[g] = dequant(aq, sa) @ dequant(bq, sb)^T over expert
     g's token tiles; aq [B, P, 128], sa [B, P], bq [B, Q, 128], sb [B, Q] from
     fp8q_quantize_act_grouped of tensors with m_tot rows and these offsets."""
+    if stream is not None:
+        with _on(stream):
+            return fp8q_grouped_gemm_rowscaled(aq, sa, bq, sb, offsets, m_tot, out_dtype, out)
     _need(aq, torch.uint8, "aq")
     _need(bq, torch.uint8, "bq")
     _need(offsets, torch.int32, "offsets")
@@ -599,11 +605,11 @@ def fp8q_grouped_gemm_rowscaled(aq, sa, bq, sb, offsets, m_tot: int, out_dtype=t
     _need(bq, torch.uint8, "bq", (tiles, Q, 128))
     _need(sa, torch.float32, "sa", (tiles, P))
     _need(sb, torch.float32, "sb", (tiles, Q))
-    with _on(stream, aq, sa, bq, sb, offsets, out) as s:
-        out = _out(out, out_dtype if out is None else out.dtype, "out", (G, P, Q), aq)
-        _check(load_library().fp8q_grouped_gemm_rowscaled(_ptr(aq), _ptr(sa), _ptr(bq), _ptr(sb), _ptr(offsets), G,
-                                                          int(m_tot), P, Q, _ptr(out), _out_code(out.dtype), s),
-               "fp8q_grouped_gemm_rowscaled")
+    s = _here(aq, sa, bq, sb, offsets, out)
+    out = _out(out, out_dtype if out is None else out.dtype, "out", (G, P, Q), aq)
+    _check(load_library().fp8q_grouped_gemm_rowscaled(_ptr(aq), _ptr(sa), _ptr(bq), _ptr(sb), _ptr(offsets), G,
+                                                      int(m_tot), P, Q, _ptr(out), _out_code(out.dtype), s),
+           "fp8q_grouped_gemm_rowscaled")
     return out
 
 
@@ -670,6 +676,9 @@ def fp8q_adamw(plan: AdamwPlan, lr: float, betas=(0.9, 0.95), eps: float = 1e-8,
     """One AdamW step over the plan's tensors, in place.  `step` counts from 1.  `scalars`: a device
     float32 [4] holding {lr, 1 - beta1^step, 1 - beta2^step, grad_scale}, read by the kernels in
     place of those arguments (a captured step is replayed with new values in it)."""
+    if stream is not None:
+        with _on(stream):
+            return fp8q_adamw(plan, lr, betas, eps, weight_decay, step, grad_scale, scalars)
     if not isinstance(plan, AdamwPlan):
         raise ValueError("plan must come from fp8q_adamw_plan")
     if scalars is not None:
@@ -677,9 +686,9 @@ def fp8q_adamw(plan: AdamwPlan, lr: float, betas=(0.9, 0.95), eps: float = 1e-8,
     if plan.device is None:
         return
     hyper = _AdamwHyper(lr, betas[0], betas[1], eps, weight_decay, grad_scale, step, _ptr(scalars) or None)
-    with _on(stream, plan.tensors["params"][0], scalars) as s:
-        _check(load_library().fp8q_adamw(plan.descriptors, len(plan.tensors["params"]), plan.grad_dtype, plan.state_dtype,
-                                         ctypes.byref(hyper), s), "fp8q_adamw")
+    s = _here(plan.tensors["params"][0], scalars)
+    _check(load_library().fp8q_adamw(plan.descriptors, len(plan.tensors["params"]), plan.grad_dtype, plan.state_dtype,
+                                     ctypes.byref(hyper), s), "fp8q_adamw")
 
 
 quantize_act_1x128 = fp8q_quantize_act_1x128
