@@ -162,7 +162,9 @@ def _here(*tensors) -> int:
 def _on(stream):
     """`stream` (a torch stream or a handle) as the current one, so that what is allocated inside
     belongs to the stream that writes it."""
-    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
 
 
 def _out(t, dtype, name: str, shape, like: torch.Tensor):

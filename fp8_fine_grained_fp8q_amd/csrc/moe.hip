@@ -311,10 +311,13 @@ __global__ __launch_bounds__(256) void moe_sum_kernel(const void *__restrict__ d
                                                       const int32_t *__restrict__ token_row, int k, int64_t cap,
                                                       void *__restrict__ dx) {
   const int64_t t = blockIdx.x / segs;
-  const int64_t c = static_cast<int64_t>(blockIdx.x % segs) * 256 + threadIdx.x;
+  // Threads past the row's end sum its first chunk and store nothing: no lane leaves before the
+  // loop, which reads `row` from all of them.
+  const int64_t own = static_cast<int64_t>(blockIdx.x % segs) * 256 + threadIdx.x;
+  const bool in = own < H / 8;
+  const int64_t c = in ? own : 0;
   int32_t row;
   uint64_t todo = token_rows(token_row, t, k, cap, row);
-  if (c >= H / 8) return;
   auto next = [&]() -> int64_t {
     const int64_t r = __builtin_amdgcn_readlane(row, __ffsll(static_cast<unsigned long long>(todo)) - 1);
     todo &= todo - 1;
@@ -334,7 +337,7 @@ __global__ __launch_bounds__(256) void moe_sum_kernel(const void *__restrict__ d
   while (__popcll(todo) >= 4) add(std::integral_constant<int, 4>{});
   if (__popcll(todo) >= 2) add(std::integral_constant<int, 2>{});
   if (todo != 0) add(std::integral_constant<int, 1>{});
-  store8<kOutF32>(dx, t * H + 8 * c, acc);
+  if (in) store8<kOutF32>(dx, t * H + 8 * c, acc);
 }
 
 // The whole sort of at most kSmallSort entries in one launch (a lone routing chunk: the routing

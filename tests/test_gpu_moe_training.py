@@ -177,12 +177,12 @@ def test_side_stream_argument():
     ref = kept(step(d, parameters(9)))
     torch.cuda.synchronize()
     side = torch.cuda.Stream()
-    for stream in (side, side.cuda_stream):
+    for stream in (side, side.cuda_stream, 0):
         par = parameters(9)
         torch.cuda.synchronize()
         got = step(d, par, stream=stream)
-        side.synchronize()
-        same(got, ref, "side stream")
+        torch.cuda.synchronize()
+        same(got, ref, f"stream {stream}")
 
 
 def test_two_threads():
