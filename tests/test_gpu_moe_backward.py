@@ -48,10 +48,12 @@ def within(got, ref, tol, what):
 
 
 # ------------------------------------------------------------------ sort, and its gradient
-# one wave's chunk and several, k = 1 and 64, one expert and 1024, nothing local, short capacity
+# one wave's chunk and several, k = 1 and 64, one expert and 1024, nothing local, short capacity; one
+# routing chunk, a few that count for themselves, and more that share the counts
 SORTS = [(1, 1, 1, 0, 8, 1, None), (300, 8, 20, 16, 264, 64, None), (77, 1, 5, 0, 2056, 64, None),
          (40, 64, 128, 0, 8, 128, None), (700, 8, 1024, 0, 24, 1500, None), (64, 6, 1, 9, 128, 8, None),
-         (200, 4, 16, 0, 4104, 16, 333), (50, 2, 8, 0, 64, 8, 0)]
+         (200, 4, 16, 0, 4104, 16, 333), (50, 2, 8, 0, 64, 8, 0),
+         (2100, 8, 1024, 0, 8, 1024, None), (2200, 8, 64, 0, 16, 80, None), (2200, 8, 64, 0, 16, 1, 9000)]
 
 
 @pytest.mark.parametrize("dtype", TYPES)
@@ -310,6 +312,26 @@ def test_grouped_weight_gradient(counts, P, Q, slack, out_dtype):
             total = np.abs(oq.dequant_act(h[0], h[1])) @ np.abs(oq.dequant_act(h[2], h[3])).T
             tol = np.minimum(tol, (130 + -(-c // 128)) * 2.0 ** -24 * (1 + 1e-4) * total)
         within(f64(got[g]), ref, tol + HALF[out_dtype] * np.abs(ref), f"expert {g}")
+
+
+@pytest.mark.parametrize("out_dtype", TYPES)
+def test_runs_of_tiles(out_dtype):
+    """Many experts with few tokens, where a workgroup takes several tiles in a row (the last run
+    of a row shorter): the same bits as each expert alone, tile by tile."""
+    counts = [100, 0, 200, 300, 1, 128, 129, 31, 257, 33] * 4
+    G, P, Q, M = len(counts), 1280, 1408, sum(counts)
+    dy, _ = values((M, P), torch.bfloat16, 1, 1e-3)
+    x, _ = values((M, Q), torch.bfloat16, 2)
+    off = dev(offsets_of(counts))
+    a, sa = fq.fp8q_quantize_act_grouped(dy, off, rows=False)[2:]
+    b, sb = fq.fp8q_quantize_act_grouped(x, off, rows=False)[2:]
+    got = fq.fp8q_grouped_gemm_rowscaled(a, sa, b, sb, off, M, out_dtype=out_dtype)
+    at = 0
+    for g, c in enumerate(counts):
+        one = dev(offsets_of([c]))
+        ops = [fq.fp8q_quantize_act_grouped(t[at:at + c].contiguous(), one, rows=False)[2:] for t in (dy, x)]
+        at += c
+        assert torch.equal(fq.fp8q_grouped_gemm_rowscaled(*ops[0], *ops[1], one, c, out_dtype=out_dtype)[0], got[g]), g
 
 
 def test_grouped_weight_gradient_without_rows():
