@@ -6,10 +6,12 @@
 //                sa[b][p] * sb[b][q] * sum_{k in tile b} e4m3(aq[p][k]) * e4m3(bq[q][k])
 //
 // The contraction runs over the expert's tokens, in the tiles of 128 that
-// quant_act_grouped_kernel writes (one FP32 scale per tile and channel).  A tile's sum starts
-// from zero in the matrix core; its result is scaled and added to an FP32 accumulator, acc =
-// (P * sa) * sb + acc: two vector operations per element and token tile, as both scales vary
-// inside a lane.
+// quant_act_grouped_kernel writes (one FP32 scale per tile and channel).  A tile's sum P starts
+// from zero in the matrix core, which also forms the products of the scales, S = sa * sb, by an
+// FP32 instruction of depth 1: each is one rounded product, and acc = P * S + acc is one vector
+// operation per element and token tile, where both scales vary inside a lane and two were
+// needed, (P * sa) * sb + acc (FP32 output 500 -> 488 us and 860 -> 838 us for the two sizes
+// below).  S under 2^-126 loses bits: such terms are below 448^2 * 128 * 2^-126 = 3e-31.
 //
 // BF16 output takes the FP8 matrix instructions.  Their sums of 64 products are off by 1.4e-5
 // (2-norm, normal data, any of the shapes), far below BF16's rounding but above FP32's: FP32
@@ -18,12 +20,11 @@
 //
 // Two regimes, measured on one MI355X (product alone, behind its quantizers):
 //  * few tokens per expert: the gradient's bytes.  32 experts of 4096 x 7168 over 8192 rows: FP32
-//    870 us (4.3 TB/s of 3.76 GB), BF16 534 us.  Stores alone take 650 and 366 us, loads and
+//    840-870 us (4.4 TB/s of 3.76 GB), BF16 510 us.  Stores alone take 650 and 366 us, loads and
 //    products alone about 700 and 450; the two overlap only in part.
-//  * many: the matrix cores and the vector units.  4 experts of 7168 x 2048 over 16384 rows: BF16
-//    output 310 us (1.55 PFLOP/s), FP32 520 us.  Beside the FP8 instructions the vector unit
-//    issues once in 8 cycles (without them, in 4 to 5), so the two operations per element
-//    take half as long again as the products; the time is near the sum of the two.
+//  * many: 4 experts of 7168 x 2048 over 16384 rows: FP32 output 490 us, the BF16 instructions
+//    (435 us without the copies), BF16 output 300 us (1.6 PFLOP/s): 225 us without the copies, 260
+//    with every copy a hit in the L2.
 //
 // A workgroup of 8 waves computes 128 x 128 tiles of one expert, 32 x 64 per wave in 32x32 blocks,
 // two workgroups per CU, so that one's loads and stores run beside the other's products.
@@ -43,6 +44,7 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef float v16f __attribute__((ext_vector_type(16)));
+typedef float v32f __attribute__((ext_vector_type(32)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 #define FP8Q_LDS __attribute__((address_space(3)))
 
@@ -108,15 +110,13 @@ __device__ __forceinline__ void read_chunks(v4i (&a)[2], v4i (&b)[2][2], uint32_
       : "v"(pa0), "v"(pa1), "v"(pb0), "v"(pb1), "n"(kAt), "n"(kAt + kPanel), "n"(kAt + kPanel + 4096)
       : "memory");
 }
-// The scales of the lane's 16 rows and 2 columns.
+// The scales of row l32 and of column 2 l32 + half of the wave.
 template <int kAt>
-__device__ __forceinline__ void read_scales(v4f (&sr)[4], f32x2 &sc, uint32_t pr, uint32_t pc) {
-  asm volatile(
-      "ds_read_b128 %0, %5 offset:%7\n\tds_read_b128 %1, %5 offset:%8\n\tds_read_b128 %2, %5 offset:%9\n\t"
-      "ds_read_b128 %3, %5 offset:%10\n\tds_read_b64 %4, %6 offset:%11\n\ts_waitcnt lgkmcnt(0)"
-      : "=&v"(sr[0]), "=&v"(sr[1]), "=&v"(sr[2]), "=&v"(sr[3]), "=&v"(sc)
-      : "v"(pr), "v"(pc), "n"(kAt), "n"(kAt + 32), "n"(kAt + 64), "n"(kAt + 96), "n"(kAt + kTile * 4)
-      : "memory");
+__device__ __forceinline__ void read_scales(float &sr, float &sc, uint32_t pr, uint32_t pc) {
+  asm volatile("ds_read_b32 %0, %2 offset:%4\n\tds_read_b32 %1, %3 offset:%5\n\ts_waitcnt lgkmcnt(0)"
+               : "=&v"(sr), "=&v"(sc)
+               : "v"(pr), "v"(pc), "n"(kAt), "n"(kAt + kTile * 4)
+               : "memory");
 }
 
 template <int N>
@@ -210,8 +210,8 @@ __device__ __forceinline__ void wgrad_run(const uint8_t *__restrict__ aq, const 
     at_a[m] = pos + wm * 4096;
     at_b[m] = pos + wn * 8192;
   }
-  const uint32_t at_sr = lds_address(st) + kScaleAt + (wm * 32 + 4 * half) * 4;
-  const uint32_t at_sc = lds_address(st) + kScaleAt + (wn * 64 + 2 * l32) * 4;
+  const uint32_t at_sr = lds_address(st) + kScaleAt + (wm * 32 + l32) * 4;
+  const uint32_t at_sc = lds_address(st) + kScaleAt + (wn * 64 + 2 * l32 + half) * 4;
   // Waits for the LDS reads and then for the other waves.  Not __syncthreads(), whose fence would
   // wait for the copies and stores in flight.
   auto meet = [&]() {
@@ -279,13 +279,13 @@ __device__ __forceinline__ void wgrad_run(const uint8_t *__restrict__ aq, const 
                                                                     0, 0, 0, 0, 0);
       }
     }
-    f32x2 sc;
-    v4f sr[4];
+    float sr, sc;
     read_scales<kCur>(sr, sc, at_sr, at_sc);
+    const v32f scale = __builtin_amdgcn_mfma_f32_32x32x1f32(sr, sc, v32f{}, 0, 0, 0);
 #pragma unroll
     for (int n = 0; n < 2; ++n)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) acc[n][i] = __builtin_fmaf(part[n][i] * sr[i >> 2][i & 3], sc[n], acc[n][i]);
+      for (int i = 0; i < 16; ++i) acc[n][i] = __builtin_fmaf(part[n][i], scale[16 * n + i], acc[n][i]);
     if (ends) {
       if (more) {
         meet();  // every wave has read this stage too: its buffer takes the stage after the next
