@@ -22,12 +22,13 @@
 //  * few tokens per expert: the gradient's bytes.  32 experts of 4096 x 7168 over 8192 rows: FP32
 //    840-870 us (4.4 TB/s of 3.76 GB), BF16 510 us.  Stores alone take 650 and 366 us, loads and
 //    products alone about 700 and 450; the two overlap only in part.
-//  * many: 4 experts of 7168 x 2048 over 16384 rows: FP32 output 490 us, the BF16 instructions
-//    (435 us without the copies), BF16 output 300 us (1.6 PFLOP/s): 225 us without the copies, 260
-//    with every copy a hit in the L2.
+//  * many: the matrix cores.  4 experts of 7168 x 2048 over 16384 rows: FP32 output 490 us, the BF16
+//    instructions (435 us without the copies); BF16 output 250 us (1.9 PFLOP/s) by the wide
+//    kernel below, 300 us by this one.
 //
-// A workgroup of 8 waves computes 128 x 128 tiles of one expert, 32 x 64 per wave in 32x32 blocks,
-// two workgroups per CU, so that one's loads and stores run beside the other's products.
+// The kernel for few tokens and for FP32: a workgroup of 8 waves computes 128 x 128 tiles of one
+// expert, 32 x 64 per wave in 32x32 blocks, two workgroups per CU, so that one's loads and stores
+// run beside the other's products.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -124,6 +125,35 @@ __device__ __forceinline__ void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
+// Expert g's tiles of 128 tokens: the first one, their number and the tokens of the last one.  Valid
+// offsets never reach past the last tile; others are kept inside the operands.
+__device__ __forceinline__ void expert_tiles(const int32_t *offsets, int G, int64_t M, int64_t all_tiles, int g,
+                                             int &first, int &tiles, int &rest) {
+  int64_t first64;
+  tiles_of_expert(offsets, G, M, g, first64, tiles, rest);
+  const int64_t room = all_tiles - first64;
+  tiles = room <= 0 ? 0 : (tiles < room ? tiles : static_cast<int>(room));
+  first = tiles > 0 ? static_cast<int>(first64) : 0;
+}
+
+// The tile row p and the run of tile columns r of expert g that this workgroup computes, of tp
+// rows and `runs` runs; false for workgroups past an expert's last run.  Workgroups are dealt
+// round-robin to the 8 XCDs.  Each XCD gets a contiguous eighth of every expert's runs, four rows
+// of tiles at a time, column by column: neighbouring workgroups share operands in their L2 and
+// write neighbouring parts of the same rows, and experts of different sizes load all XCDs alike
+// (whole experts per XCD: 4 uneven experts over 16384 rows 350 us instead of 314 us).
+__device__ __forceinline__ bool place(int tp, int runs, int &g, int &p, int &r) {
+  const int per = (tp * runs + 7) / 8;
+  const int xcd = blockIdx.x % 8, idx = blockIdx.x / 8;
+  g = idx / per;
+  const int in_g = xcd * per + idx % per;
+  if (in_g >= tp * runs) return false;
+  const int span = 4 * runs, first = in_g / span * 4, high = tp - first < 4 ? tp - first : 4, in_s = in_g % span;
+  p = first + in_s % high;
+  r = in_s / high;
+  return true;
+}
+
 // C tiles (p0, q) for the run of 128-column tiles q0 .. q0 + 128 (count - 1) of expert g.
 template <bool kOutF32>
 __device__ __forceinline__ void wgrad_run(const uint8_t *__restrict__ aq, const float *__restrict__ sa,
@@ -136,13 +166,8 @@ __device__ __forceinline__ void wgrad_run(const uint8_t *__restrict__ aq, const 
   const int wm = wave >> 1, wn = wave & 1;
   const int l32 = lane & 31, half = lane >> 5;
 
-  int64_t first64;
-  int tiles, rest;
-  tiles_of_expert(offsets, G, M, g, first64, tiles, rest);
-  // valid offsets never reach past the last tile; others are kept inside the operands
-  const int64_t room = all_tiles - first64;
-  tiles = room <= 0 ? 0 : (tiles < room ? tiles : static_cast<int>(room));
-  const int first = tiles > 0 ? static_cast<int>(first64) : 0;
+  int first, tiles, rest;
+  expert_tiles(offsets, G, M, all_tiles, g, first, tiles, rest);
   const int last = (rest + 31) / 32;
 
   // Copies: an operand's 16 KB stage is contiguous in memory.  1 KB block b = 8 i + wave of it
@@ -313,20 +338,255 @@ __global__ __launch_bounds__(64 * kWaves, 4) void wgrad_kernel(
     const float *__restrict__ sb, const int32_t *__restrict__ offsets, int G, int64_t M, int64_t all_tiles, int P,
     int Q, int run, void *__restrict__ c) {
   __shared__ __attribute__((aligned(1024))) uint8_t stages[2 * kStage];
-  // Workgroups are dealt round-robin to the 8 XCDs.  Each XCD gets a contiguous eighth of every
-  // expert's runs, four rows of tiles at a time, column by column: neighbouring workgroups share
-  // operands in their L2 and write neighbouring parts of the same rows, and experts of different sizes load
-  // all XCDs alike (whole experts per XCD: 4 uneven experts over 16384 rows 350 us instead of
-  // 314 us).  Workgroups past an expert's last run exit.
-  const int tp = P / kTile, tq = Q / kTile, runs = (tq + run - 1) / run;
-  const int per = (tp * runs + 7) / 8;
-  const int xcd = blockIdx.x % 8, idx = blockIdx.x / 8;
-  const int g = idx / per, in_g = xcd * per + idx % per;
-  if (in_g >= tp * runs) return;
-  const int span = 4 * runs, first = in_g / span * 4, high = tp - first < 4 ? tp - first : 4, in_s = in_g % span;
-  const int p = first + in_s % high, q = in_s / high * run;
+  const int tp = P / kTile, tq = Q / kTile;
+  int g, p, r;
+  if (!place(tp, (tq + run - 1) / run, g, p, r)) return;
+  const int q = r * run;
   wgrad_run<kOutF32>(aq, sa, bq, sb, offsets, G, M, all_tiles, P, Q, g, static_cast<int64_t>(p) * kTile,
                      static_cast<int64_t>(q) * kTile, tq - q < run ? tq - q : run, c, (FP8Q_LDS uint8_t *)stages);
+}
+
+// ---------------------------------------------------------------------------------------
+// The kernel for many tokens and BF16 output: tiles of 256 x 128, 64 x 64 per wave (4 x 2 waves), one
+// workgroup per CU.  The two waves of a SIMD (w and w + 4) take turns: one multiplies a token tile
+// from registers while the other scales and adds half of its last one and reads the next from LDS.
+// Against the 128 x 128 tiles a quarter less is copied and a third less read from LDS per product, and the
+// matrix core does not wait for either: 4 experts of 7168 x 2048 over 16384 rows 300 -> 250 us.  A
+// token tile takes 0.71 us on codes of zeros, of which the matrix core works 0.53, and 1.0 us on
+// random ones, where power limits the clock; a tile's start and end 4 us.  Three things it needed:
+// no branch and no address arithmetic between the barriers (310 us with them), the copies
+// behind the matrix instructions and not behind the reads, and no instruction that waits for
+// a matrix result right before another matrix instruction (265 -> 250 us).
+// ---------------------------------------------------------------------------------------
+constexpr int kWideRows = 256;
+constexpr int kWideScaleAt = kWideRows * 128 + kPanel;  // then the rows' scales and the columns'
+constexpr int kWideStage = kWideScaleAt + 8 * 256;  // waves 6 and 7 copy what 4 and 5 copy, behind it
+constexpr int kRing = 3;  // stages in LDS: one read, two in flight
+
+// A wave's operands of a stage and the scales of its row `lane` and of columns 2 l32, 2 l32 + 1.
+// a[f][m], b[n][m]: chunk 2 m + half of row 32 f + l32 and column block n.
+__device__ __forceinline__ void read_stage(v4i (&a)[2][4], v4i (&b)[2][4], float &sr, f32x2 &sc, const uint32_t (&pa)[4],
+                                           const uint32_t (&pb)[4], uint32_t pr, uint32_t pc) {
+  asm volatile(
+      "ds_read_b32 %16, %26\n\tds_read_b64 %17, %27\n\t"
+      "ds_read_b128 %0, %18\n\tds_read_b128 %8, %22\n\tds_read_b128 %1, %19\n\tds_read_b128 %9, %23\n\t"
+      "ds_read_b128 %4, %18 offset:4096\n\tds_read_b128 %5, %19 offset:4096\n\t"
+      "ds_read_b128 %2, %20\n\tds_read_b128 %10, %24\n\tds_read_b128 %3, %21\n\tds_read_b128 %11, %25\n\t"
+      "ds_read_b128 %6, %20 offset:4096\n\tds_read_b128 %7, %21 offset:4096\n\t"
+      "ds_read_b128 %12, %22 offset:4096\n\tds_read_b128 %13, %23 offset:4096\n\t"
+      "ds_read_b128 %14, %24 offset:4096\n\tds_read_b128 %15, %25 offset:4096\n\ts_waitcnt lgkmcnt(0)"
+      : "=&v"(a[0][0]), "=&v"(a[0][1]), "=&v"(a[0][2]), "=&v"(a[0][3]), "=&v"(a[1][0]), "=&v"(a[1][1]),
+        "=&v"(a[1][2]), "=&v"(a[1][3]), "=&v"(b[0][0]), "=&v"(b[0][1]), "=&v"(b[0][2]), "=&v"(b[0][3]),
+        "=&v"(b[1][0]), "=&v"(b[1][1]), "=&v"(b[1][2]), "=&v"(b[1][3]), "=&v"(sr), "=&v"(sc)
+      : "v"(pa[0]), "v"(pa[1]), "v"(pa[2]), "v"(pa[3]), "v"(pb[0]), "v"(pb[1]), "v"(pb[2]), "v"(pb[3]), "v"(pr), "v"(pc)
+      : "memory");
+}
+
+__device__ __forceinline__ void wgrad_wide_run(const uint8_t *__restrict__ aq, const float *__restrict__ sa,
+                                               const uint8_t *__restrict__ bq, const float *__restrict__ sb,
+                                               const int32_t *__restrict__ offsets, int G, int64_t M, int64_t all_tiles,
+                                               int64_t P, int64_t Q, int g, int64_t p0, int64_t q0,
+                                               uint16_t *__restrict__ c, FP8Q_LDS uint8_t *st) {
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  const int l32 = lane & 31, half = lane >> 5;
+  const bool lead = wave < 4;
+
+  int first, tiles, rest;
+  expert_tiles(offsets, G, M, all_tiles, g, first, tiles, rest);
+
+  // Copies, as in wgrad_run: wave w moves 1 KB block 8 i + w of either operand.  parts: 64-row parts of
+  // the tile that C has; the last tile of a P of 128 modulo 256 copies its rows twice and stores
+  // them once.
+  const int line = 4 * (wave & 1) + (lane >> 4);
+  const int at = 16 * (wave >> 1) + line + 8 * ((lane >> 3) & 1), chunk = ((lane & 7) ^ line) * 16;
+  const int off_a = at * 128 + chunk, off_b = (at & 31) * 256 + (at >> 5) * 128 + chunk;
+  const int parts = P - p0 < kWideRows ? 2 : 4;
+  const uint8_t *from_a = aq + (static_cast<int64_t>(first) * P + p0) * 128;
+  const uint8_t *from_b = bq + (static_cast<int64_t>(first) * Q + q0) * 128;
+  const float *from_s = wave < 4 ? sa + static_cast<int64_t>(first) * P + p0 + (wave & (parts - 1)) * 64
+                                 : sb + static_cast<int64_t>(first) * Q + q0 + (wave & 1) * 64;
+  const int64_t step_a = P * 128, step_b = Q * 128, step_s = wave < 4 ? P : Q;
+  int copied = 0;                           // stages
+  FP8Q_LDS uint8_t *to = st + wave * 1024;  // where the next one goes
+  // Copy i of 7 of the next stage.  Past the last stage the copies go through empty resources (zeros,
+  // no traffic), so that every wave always has the same number in flight.
+  auto copy = [&](int i) {
+    const bool some = copied < tiles;
+    if (i < 4)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer_of(from_a, some ? parts * 8192 : 0), (FP8Q_LDS void *)(to + i * 8192),
+                                               16, off_a, (i & (parts - 1)) * 8192, 0, 0);
+    else if (i < 6)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer_of(from_b, some ? kPanel : 0), (FP8Q_LDS void *)(to + i * 8192), 16,
+                                               off_b, (i - 4) * 8192, 0, 0);
+    else
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer_of(from_s, some ? 256 : 0),
+                                               (FP8Q_LDS void *)(to + kWideScaleAt - wave * 768), 4, lane * 4, 0, 0, 0);
+  };
+  auto turn = [&]() {
+    ++copied;
+    from_a += step_a;
+    from_b += step_b;
+    from_s += step_s;
+    to = to == st + wave * 1024 + (kRing - 1) * kWideStage ? st + wave * 1024 : to + kWideStage;
+  };
+  auto copy_stage = [&]() {
+#pragma unroll
+    for (int i = 0; i < 7; ++i) copy(i);
+  };
+
+  // Element i of block (f, n) is row 32 f + 8 (i / 4) + 4 half + i % 4, column 2 l32 + n of the wave.
+  v16f acc[2][2], part[2][2];
+  auto clear = [&](v16f (&x)[2][2]) {
+#pragma unroll
+    for (int f = 0; f < 2; ++f)
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[f][n][i] = 0.0f;
+  };
+  const bool mine = wm < parts;  // this wave's rows are in C
+  const int64_t c0 = (static_cast<int64_t>(g) * P + p0 + wm * 64) * Q + q0 + wn * 64;
+  const int ld = static_cast<int>(Q) * 2, off_c = 4 * half * ld + 4 * l32;
+  auto store = [&]() {
+    if (!mine) return;
+    const __amdgpu_buffer_rsrc_t rc = buffer_of(c + c0, 64 * ld);
+#pragma unroll
+    for (int f = 0; f < 2; ++f)
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        __builtin_amdgcn_raw_buffer_store_b32(pack2_bf16(acc[f][0][i], acc[f][1][i]), rc, off_c,
+                                              (32 * f + 8 * (i >> 2) + (i & 3)) * ld, 2);
+  };
+  clear(acc);
+  clear(part);
+  if (tiles == 0) {
+    store();
+    return;
+  }
+
+  // LDS address, in the first stage, of the lane's row's chunk `half`; chunk 2 m + half is at ^ 32 m.
+  const uint32_t at_0 = lds_address(st) + chunk_pos(l32, half);
+  uint32_t at_sr = lds_address(st) + kWideScaleAt + (wm * 64 + lane) * 4;
+  uint32_t at_sc = lds_address(st) + kWideScaleAt + (kWideRows + wn * 64 + 2 * l32) * 4;
+  auto barrier = [&]() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // Phases end at a barrier.  The lead waves 0-3 run one ahead: in phase 2 t they read stage t, in phase
+  // 2 t + 1 they multiply it, while the others read it.  Stage t is last read in phase 2 t + 1 and its
+  // place free from phase 2 t + 2 on, where the others multiply it and copy stage t + 3; the lead
+  // waves, which multiply it in phase 2 t + 1, copy stage t + 2 there.  A wave waits at the end of its
+  // products for all but the copies that it just issued: the lead waves' of stage t + 1 have then
+  // landed at the end of phase 2 t + 1, the others' of stage t + 2 at the end of phase 2 t + 2, both before
+  // those stages are first read (phases 2 t + 2 and 2 t + 4).
+  copy_stage();
+  turn();
+  copy_stage();
+  if (lead) {
+    wait_loads<7>();
+    barrier();
+  } else {
+    turn();
+    copy_stage();
+    wait_loads<14>();
+    barrier();
+    wait_loads<7>();
+    barrier();
+  }
+  // A column block's sums are scaled and added beside the products of the other one, block 1's
+  // beside the next token tile's.
+  int cur = 0;                   // the stage's place in LDS
+  v32f scale = {};               // those of part[.][1], later of part[.][0]
+  auto add = [&](int n, int from, int to) {
+#pragma unroll
+    for (int i = from; i < to; ++i)
+      acc[i / 16][n][i % 16] = __builtin_fmaf(part[i / 16][n][i % 16], scale[i], acc[i / 16][n][i % 16]);
+  };
+  auto multiply = [&](v4i (&a)[2][4], v4i (&b)[2][4], int n, int f, int h, const v16f &sum) {
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(join(a[f][2 * h], a[f][2 * h + 1]),
+                                                           join(b[n][2 * h], b[n][2 * h + 1]), sum, 0, 0, 0, 0, 0, 0);
+  };
+  for (int t = 0; t < tiles; ++t) {
+    turn();
+    add(1, 0, 32);
+    asm volatile("" : "+v"(acc[0][1]), "+v"(acc[1][1]));
+    v4i a[2][4], b[2][4];
+    float sr;
+    f32x2 sc;
+    const uint32_t a0 = at_0 + (cur + wm * 8192), b0 = at_0 + (cur + kWideRows * 128 + wn * 8192);
+    const uint32_t pa[4] = {a0, a0 ^ 32, a0 ^ 64, a0 ^ 96}, pb[4] = {b0, b0 ^ 32, b0 ^ 64, b0 ^ 96};
+    read_stage(a, b, sr, sc, pa, pb, at_sr + cur, at_sc + cur);
+    cur = cur == (kRing - 1) * kWideStage ? 0 : cur + kWideStage;
+    barrier();
+    const v16f zero = {};
+    v16f sum[2];
+    auto pin = []() { __builtin_amdgcn_sched_barrier(0); };
+    auto pinned = [](auto &x) {
+      asm volatile("" : "+v"(x));
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    sum[0] = multiply(a, b, 0, 0, 0, zero);
+    pinned(sum[0]);
+    copy(0);
+    copy(1);
+    pin();
+    sum[0] = multiply(a, b, 0, 0, 1, sum[0]);
+    pinned(sum[0]);
+    copy(2);
+    copy(3);
+    pin();
+    sum[1] = multiply(a, b, 0, 1, 0, zero);
+    pinned(sum[1]);
+    copy(4);
+    copy(5);
+    pin();
+    sum[1] = multiply(a, b, 0, 1, 1, sum[1]);
+    pinned(sum[1]);
+    part[0][0] = sum[0];
+    part[1][0] = sum[1];
+    scale = __builtin_amdgcn_mfma_f32_32x32x1f32(sr, sc.x, v32f{}, 0, 0, 0);
+    pinned(scale);
+    sum[0] = multiply(a, b, 1, 0, 0, zero);
+    pinned(sum[0]);
+    copy(6);
+    pin();
+    sum[0] = multiply(a, b, 1, 0, 1, sum[0]);
+    pinned(sum[0]);
+    add(0, 0, 8);
+    pin();
+    sum[1] = multiply(a, b, 1, 1, 0, zero);
+    pinned(sum[1]);
+    add(0, 8, 20);
+    pin();
+    sum[1] = multiply(a, b, 1, 1, 1, sum[1]);
+    pinned(sum[1]);
+    add(0, 20, 32);
+    pin();
+    scale = __builtin_amdgcn_mfma_f32_32x32x1f32(sr, sc.y, v32f{}, 0, 0, 0);
+    pinned(scale);
+    part[0][1] = sum[0];
+    part[1][1] = sum[1];
+    wait_loads<7>();
+    barrier();
+  }
+  if (lead) barrier();
+  wait_loads<0>();
+  add(1, 0, 32);
+  store();
+}
+
+__global__ __launch_bounds__(64 * kWaves, 2) void wgrad_wide_kernel(
+    const uint8_t *__restrict__ aq, const float *__restrict__ sa, const uint8_t *__restrict__ bq,
+    const float *__restrict__ sb, const int32_t *__restrict__ offsets, int G, int64_t M, int64_t all_tiles, int P,
+    int Q, uint16_t *__restrict__ c) {
+  __shared__ __attribute__((aligned(1024))) uint8_t stages[kRing * kWideStage];
+  int g, p, q;
+  if (!place((P + kWideRows - 1) / kWideRows, Q / kTile, g, p, q)) return;
+  wgrad_wide_run(aq, sa, bq, sb, offsets, G, M, all_tiles, P, Q, g, static_cast<int64_t>(p) * kWideRows,
+                 static_cast<int64_t>(q) * kTile, c, (FP8Q_LDS uint8_t *)stages);
 }
 
 hipError_t launch_grouped_gemm_rowscaled(const uint8_t *aq, const float *sa, const uint8_t *bq, const float *sb,
@@ -338,8 +598,21 @@ hipError_t launch_grouped_gemm_rowscaled(const uint8_t *aq, const float *sa, con
   // experts over 8192 rows: 3 tiles instead of one, FP32
   // 940 -> 870 us, BF16 622 -> 534 us; 4 experts over 16384 rows, where a tile is
   // 32 token tiles: one instead of 3, BF16 345 -> 310 us.
-  const int64_t tiles = G * (P / kTile) * (Q / kTile), slots = 2 * device_cu_count();
   const int64_t depth = M / (128 * G) + 1;  // about the token tiles of an expert
+  // BF16 output of experts with 8 token tiles or more, if that makes a 256 x 128 tile for every CU:
+  // 4 experts of 7168 x 2048 with 4, 8 and 12 token tiles take 59, 88 and 111 us by wide tiles, 56, 97
+  // and 130 by the others; 2048 x 2048, half as many tiles as CUs, 20 and 19.  P = 128 would leave half
+  // of each wide tile empty (16 experts of 128 x 8192 with 32 token tiles 160 and 107 us).
+  const int64_t wide = G * ((P + kWideRows - 1) / kWideRows) * (Q / kTile);
+  if (!out_f32 && depth > 8 && P > kTile && wide >= device_cu_count()) {
+    const int64_t grid = 8 * G * ((wide / G + 7) / 8);
+    if (grid > 0x7fffffff) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(wgrad_wide_kernel, dim3(static_cast<uint32_t>(grid)), dim3(64 * kWaves), 0, stream, aq, sa, bq, sb,
+                       offsets, static_cast<int>(G), M, M / 128 + G, static_cast<int>(P), static_cast<int>(Q),
+                       static_cast<uint16_t *>(c));
+    return hipGetLastError();
+  }
+  const int64_t tiles = G * (P / kTile) * (Q / kTile), slots = 2 * device_cu_count();
   const int64_t want = (8 + depth - 1) / depth, most = tiles / (4 * slots);
   int64_t run = want < most ? want : most;
   run = run < 1 ? 1 : (run > Q / kTile ? Q / kTile : run);

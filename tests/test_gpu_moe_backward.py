@@ -334,6 +334,43 @@ def test_runs_of_tiles(out_dtype):
         assert torch.equal(fq.fp8q_grouped_gemm_rowscaled(*ops[0], *ops[1], one, c, out_dtype=out_dtype)[0], got[g]), g
 
 
+@pytest.mark.parametrize("counts,P,Q,slack", [([1500, 900], 8320, 512, 0),
+                                              ([1, 0, 129, 259, 385, 64, 4000, 5000], 384, 2048, 7),
+                                              ([0, 0, 5120, 0], 512, 4096, 100)])
+def test_wide_tiles(counts, P, Q, slack):
+    """BF16 gradients of experts with many tokens, computed in tiles of 256 x 128 (the last one of a P
+    of 128 modulo 256 half empty): experts without tokens and of one to 40 token tiles, the same
+    bits as each expert alone in the small tiles, rows and tokens behind them not touched."""
+    G, M = len(counts), sum(counts) + slack
+    dy, _ = values((M, P), torch.bfloat16, 3, 1e-3)
+    x, _ = values((M, Q), torch.bfloat16, 4)
+    off = dev(offsets_of(counts))
+    a, sa = fq.fp8q_quantize_act_grouped(dy, off, rows=False)[2:]
+    b, sb = fq.fp8q_quantize_act_grouped(x, off, rows=False)[2:]
+    w = sum(-(-c // 128) for c in counts)
+    a[w:], b[w:], sa[w:], sb[w:] = 0x7F, 0x7F, float("nan"), float("nan")
+    all_c = torch.full((G + 2, P, Q), 7.0, dtype=torch.bfloat16, device="cuda")
+    got = fq.fp8q_grouped_gemm_rowscaled(a, sa, b, sb, off, M, out=all_c[1:G + 1])
+    torch.cuda.synchronize()
+    assert bool((all_c[0] == 7.0).all()) and bool((all_c[-1] == 7.0).all())
+    rows = list(range(0, 40)) + list(range(P - 150, P - 110)) + list(range(P - 20, P))
+    at = row = 0
+    for g, c in enumerate(counts):
+        tiles = slice(at, at + -(-c // 128))
+        at, row = tiles.stop, row + c
+        if c == 0:
+            assert bool((got[g] == 0).all())
+            continue
+        one = dev(offsets_of([c]))
+        ops = [fq.fp8q_quantize_act_grouped(t[row - c:row].contiguous(), one, rows=False)[2:] for t in (dy, x)]
+        assert torch.equal(fq.fp8q_grouped_gemm_rowscaled(*ops[0], *ops[1], one, c, out_dtype=torch.bfloat16)[0], got[g]), g
+        h = [host(t) for t in (a[tiles][:, rows], sa[tiles][:, rows], b[tiles], sb[tiles])]
+        h[0], h[2] = (np.ascontiguousarray(q.transpose(1, 0, 2).reshape(q.shape[1], -1)) for q in (h[0], h[2]))
+        ref = ob.wgrad(*h)
+        tol = og.tolerance(ob.row_norms_rowscaled(h[0], h[1]), ob.row_norms_rowscaled(h[2], h[3]))
+        within(f64(got[g][rows]), ref, tol + HALF[torch.bfloat16] * np.abs(ref), f"expert {g}")
+
+
 def test_grouped_weight_gradient_without_rows():
     off = torch.zeros(4, dtype=torch.int32, device="cuda")
     ops = [torch.zeros((3, 128, 128), dtype=torch.uint8, device="cuda"), torch.zeros((3, 128), device="cuda")] * 2
