@@ -22,13 +22,13 @@
 //  * few tokens per expert: the gradient's bytes.  32 experts of 4096 x 7168 over 8192 rows: FP32
 //    840-870 us (4.4 TB/s of 3.76 GB), BF16 510 us.  Stores alone take 650 and 366 us, loads and
 //    products alone about 700 and 450; the two overlap only in part.
-//  * many: the matrix cores.  4 experts of 7168 x 2048 over 16384 rows: FP32 output 490 us, the BF16
-//    instructions (435 us without the copies); BF16 output 250 us (1.9 PFLOP/s) by the wide
-//    kernel below, 300 us by this one.
+//  * many: the matrix cores and the instructions around theirs.  4 experts of 7168 x 2048 over 16384
+//    rows: BF16 250 us (1.9 PFLOP/s), FP32 447 us (1.1) by the wide kernel below; 300 and 505 us by the
+//    small tiles.
 //
-// The kernel for few tokens and for FP32: a workgroup of 8 waves computes 128 x 128 tiles of one
-// expert, 32 x 64 per wave in 32x32 blocks, two workgroups per CU, so that one's loads and stores
-// run beside the other's products.
+// The kernel for few tokens: a workgroup of 8 waves computes 128 x 128 tiles of one expert, 32 x 64
+// per wave in 32x32 blocks, two workgroups per CU, so that one's loads and stores run beside the
+// other's products.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -347,16 +347,18 @@ __global__ __launch_bounds__(64 * kWaves, 4) void wgrad_kernel(
 }
 
 // ---------------------------------------------------------------------------------------
-// The kernel for many tokens and BF16 output: tiles of 256 x 128, 64 x 64 per wave (4 x 2 waves), one
-// workgroup per CU.  The two waves of a SIMD (w and w + 4) take turns: one multiplies a token tile
-// from registers while the other scales and adds half of its last one and reads the next from LDS.
-// Against the 128 x 128 tiles a quarter less is copied and a third less read from LDS per product, and the
-// matrix core does not wait for either: 4 experts of 7168 x 2048 over 16384 rows 300 -> 250 us.  A
-// token tile takes 0.71 us on codes of zeros, of which the matrix core works 0.53, and 1.0 us on
-// random ones, where power limits the clock; a tile's start and end 4 us.  Three things it needed:
-// no branch and no address arithmetic between the barriers (310 us with them), the copies
-// behind the matrix instructions and not behind the reads, and no instruction that waits for
-// a matrix result right before another matrix instruction (265 -> 250 us).
+// The kernel for many tokens: tiles of 256 x 128, 64 x 64 per wave (4 x 2 waves), one workgroup per
+// CU.  The two waves of a SIMD (w and w + 4) take turns: one multiplies a token tile from registers
+// while the other scales and adds its last one and reads the next from LDS.  Against the 128 x 128
+// tiles a quarter less is copied, and a third less read from LDS and widened per product.
+//
+// 4 experts of 7168 x 2048 over 16384 rows: BF16 300 -> 250 us, FP32 505 -> 447 us.  BF16: a token
+// tile takes 0.71 us on codes of zeros, of which the matrix core works 0.53, and 1.0 us on random
+// ones, where power limits the clock; a tile's start and end 4 us.  FP32 (385 us on zeros) is bound
+// by the issue of the widening: 315 us without the products, 307 without the widening.  Three
+// things it needed: no branch and no address arithmetic between the barriers (310 us with them),
+// the copies behind the matrix instructions and not behind the reads, and no instruction that waits
+// for a matrix result right before another matrix instruction (265 -> 250 us).
 // ---------------------------------------------------------------------------------------
 constexpr int kWideRows = 256;
 constexpr int kWideScaleAt = kWideRows * 128 + kPanel;  // then the rows' scales and the columns'
@@ -382,11 +384,12 @@ __device__ __forceinline__ void read_stage(v4i (&a)[2][4], v4i (&b)[2][4], float
       : "memory");
 }
 
+template <bool kOutF32>
 __device__ __forceinline__ void wgrad_wide_run(const uint8_t *__restrict__ aq, const float *__restrict__ sa,
                                                const uint8_t *__restrict__ bq, const float *__restrict__ sb,
                                                const int32_t *__restrict__ offsets, int G, int64_t M, int64_t all_tiles,
                                                int64_t P, int64_t Q, int g, int64_t p0, int64_t q0,
-                                               uint16_t *__restrict__ c, FP8Q_LDS uint8_t *st) {
+                                               void *__restrict__ c, FP8Q_LDS uint8_t *st) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 1, wn = wave & 1;
@@ -448,16 +451,22 @@ __device__ __forceinline__ void wgrad_wide_run(const uint8_t *__restrict__ aq, c
   };
   const bool mine = wm < parts;  // this wave's rows are in C
   const int64_t c0 = (static_cast<int64_t>(g) * P + p0 + wm * 64) * Q + q0 + wn * 64;
-  const int ld = static_cast<int>(Q) * 2, off_c = 4 * half * ld + 4 * l32;
+  constexpr int kSize = kOutF32 ? 4 : 2, kStream = 2;  // bytes of an element; the streaming-store flag
+  const int ld = static_cast<int>(Q) * kSize, off_c = 4 * half * ld + 2 * l32 * kSize;
   auto store = [&]() {
     if (!mine) return;
-    const __amdgpu_buffer_rsrc_t rc = buffer_of(c + c0, 64 * ld);
+    const __amdgpu_buffer_rsrc_t rc = buffer_of(static_cast<uint8_t *>(c) + c0 * kSize, 64 * ld);
 #pragma unroll
     for (int f = 0; f < 2; ++f)
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        __builtin_amdgcn_raw_buffer_store_b32(pack2_bf16(acc[f][0][i], acc[f][1][i]), rc, off_c,
-                                              (32 * f + 8 * (i >> 2) + (i & 3)) * ld, 2);
+      for (int i = 0; i < 16; ++i) {
+        const int row = (32 * f + 8 * (i >> 2) + (i & 3)) * ld;
+        if (kOutF32)
+          __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(acc[f][0][i]), __float_as_uint(acc[f][1][i])}, rc,
+                                                off_c, row, kStream);
+        else
+          __builtin_amdgcn_raw_buffer_store_b32(pack2_bf16(acc[f][0][i], acc[f][1][i]), rc, off_c, row, kStream);
+      }
   };
   clear(acc);
   clear(part);
@@ -496,23 +505,27 @@ __device__ __forceinline__ void wgrad_wide_run(const uint8_t *__restrict__ aq, c
     wait_loads<7>();
     barrier();
   }
-  // A column block's sums are scaled and added beside the products of the other one, block 1's
-  // beside the next token tile's.
-  int cur = 0;                   // the stage's place in LDS
-  v32f scale = {};               // those of part[.][1], later of part[.][0]
-  auto add = [&](int n, int from, int to) {
+  // Column block n's sums, part[.][n], are scaled and added in the next reading phase, with BF16 output
+  // block 0's beside block 1's products.
+  int cur = 0;           // the stage's place in LDS
+  v32f scale[2] = {};    // of column block n; BF16 output keeps one at a time, in scale[1]
+  auto add = [&](int n, const v32f &by, int from, int to) {
 #pragma unroll
     for (int i = from; i < to; ++i)
-      acc[i / 16][n][i % 16] = __builtin_fmaf(part[i / 16][n][i % 16], scale[i], acc[i / 16][n][i % 16]);
+      acc[i / 16][n][i % 16] = __builtin_fmaf(part[i / 16][n][i % 16], by[i], acc[i / 16][n][i % 16]);
   };
-  auto multiply = [&](v4i (&a)[2][4], v4i (&b)[2][4], int n, int f, int h, const v16f &sum) {
-    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(join(a[f][2 * h], a[f][2 * h + 1]),
-                                                           join(b[n][2 * h], b[n][2 * h + 1]), sum, 0, 0, 0, 0, 0, 0);
+  auto scales = [&](float sr, float sc) { return __builtin_amdgcn_mfma_f32_32x32x1f32(sr, sc, v32f{}, 0, 0, 0); };
+  // The order of a phase as written: the value is taken as changed here.
+  auto pin = []() { __builtin_amdgcn_sched_barrier(0); };
+  auto pinned = [](auto &x) {
+    asm volatile("" : "+v"(x));
+    __builtin_amdgcn_sched_barrier(0);
   };
   for (int t = 0; t < tiles; ++t) {
     turn();
-    add(1, 0, 32);
-    asm volatile("" : "+v"(acc[0][1]), "+v"(acc[1][1]));
+    if (kOutF32) add(0, scale[0], 0, 32);
+    add(1, scale[1], 0, 32);
+    asm volatile("" : "+v"(acc[0][0]), "+v"(acc[1][0]), "+v"(acc[0][1]), "+v"(acc[1][1]));
     v4i a[2][4], b[2][4];
     float sr;
     f32x2 sc;
@@ -520,73 +533,99 @@ __device__ __forceinline__ void wgrad_wide_run(const uint8_t *__restrict__ aq, c
     const uint32_t pa[4] = {a0, a0 ^ 32, a0 ^ 64, a0 ^ 96}, pb[4] = {b0, b0 ^ 32, b0 ^ 64, b0 ^ 96};
     read_stage(a, b, sr, sc, pa, pb, at_sr + cur, at_sc + cur);
     cur = cur == (kRing - 1) * kWideStage ? 0 : cur + kWideStage;
-    barrier();
     const v16f zero = {};
-    v16f sum[2];
-    auto pin = []() { __builtin_amdgcn_sched_barrier(0); };
-    auto pinned = [](auto &x) {
-      asm volatile("" : "+v"(x));
-      __builtin_amdgcn_sched_barrier(0);
-    };
-    sum[0] = multiply(a, b, 0, 0, 0, zero);
-    pinned(sum[0]);
-    copy(0);
-    copy(1);
-    pin();
-    sum[0] = multiply(a, b, 0, 0, 1, sum[0]);
-    pinned(sum[0]);
-    copy(2);
-    copy(3);
-    pin();
-    sum[1] = multiply(a, b, 0, 1, 0, zero);
-    pinned(sum[1]);
-    copy(4);
-    copy(5);
-    pin();
-    sum[1] = multiply(a, b, 0, 1, 1, sum[1]);
-    pinned(sum[1]);
-    part[0][0] = sum[0];
-    part[1][0] = sum[1];
-    scale = __builtin_amdgcn_mfma_f32_32x32x1f32(sr, sc.x, v32f{}, 0, 0, 0);
-    pinned(scale);
-    sum[0] = multiply(a, b, 1, 0, 0, zero);
-    pinned(sum[0]);
-    copy(6);
-    pin();
-    sum[0] = multiply(a, b, 1, 0, 1, sum[0]);
-    pinned(sum[0]);
-    add(0, 0, 8);
-    pin();
-    sum[1] = multiply(a, b, 1, 1, 0, zero);
-    pinned(sum[1]);
-    add(0, 8, 20);
-    pin();
-    sum[1] = multiply(a, b, 1, 1, 1, sum[1]);
-    pinned(sum[1]);
-    add(0, 20, 32);
-    pin();
-    scale = __builtin_amdgcn_mfma_f32_32x32x1f32(sr, sc.y, v32f{}, 0, 0, 0);
-    pinned(scale);
-    part[0][1] = sum[0];
-    part[1][1] = sum[1];
+    if constexpr (kOutF32) {
+      // Steps of 16 tokens: four products each, and behind every one the widening of a quarter of
+      // the next step's operands.
+      bf16x8 wide[2][4];  // of two steps: row blocks 0 and 1, column blocks 0 and 1
+      auto widen = [&](int step, int k) {
+        const v4i &x = k < 2 ? a[k][step >> 1] : b[k - 2][step >> 1];
+        const int r = 2 * (step & 1);
+        wide[step & 1][k] = widen8(x[r], x[r + 1]);
+      };
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        widen(0, k);
+        pinned(wide[0][k]);
+      }
+      barrier();
+#pragma unroll
+      for (int step = 0; step < 8; ++step)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int f = k >> 1, n = k & 1;
+          part[f][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wide[step & 1][f], wide[step & 1][2 + n],
+                                                               step == 0 ? zero : part[f][n], 0, 0, 0);
+          pinned(part[f][n]);
+          if (step < 7) {
+            widen(step + 1, k);
+            pinned(wide[(step + 1) & 1][k]);
+            if (k == 0) copy(step);
+            pin();
+          }
+        }
+      scale[0] = scales(sr, sc.x);
+      pinned(scale[0]);
+      scale[1] = scales(sr, sc.y);
+      pinned(scale[1]);
+    } else {
+      barrier();
+      auto multiply = [&](int n, int f, int h, const v16f &sum) {
+        part[f][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(join(a[f][2 * h], a[f][2 * h + 1]),
+                                                                     join(b[n][2 * h], b[n][2 * h + 1]), sum, 0, 0, 0, 0,
+                                                                     0, 0);
+        pinned(part[f][n]);
+      };
+      multiply(0, 0, 0, zero);
+      copy(0);
+      copy(1);
+      pin();
+      multiply(0, 0, 1, part[0][0]);
+      copy(2);
+      copy(3);
+      pin();
+      multiply(0, 1, 0, zero);
+      copy(4);
+      copy(5);
+      pin();
+      multiply(0, 1, 1, part[1][0]);
+      scale[1] = scales(sr, sc.x);
+      pinned(scale[1]);
+      multiply(1, 0, 0, zero);
+      copy(6);
+      pin();
+      multiply(1, 0, 1, part[0][1]);
+      add(0, scale[1], 0, 8);
+      pin();
+      multiply(1, 1, 0, zero);
+      add(0, scale[1], 8, 20);
+      pin();
+      multiply(1, 1, 1, part[1][1]);
+      add(0, scale[1], 20, 32);
+      pin();
+      scale[1] = scales(sr, sc.y);
+      pinned(scale[1]);
+    }
     wait_loads<7>();
     barrier();
   }
   if (lead) barrier();
   wait_loads<0>();
-  add(1, 0, 32);
+  if (kOutF32) add(0, scale[0], 0, 32);
+  add(1, scale[1], 0, 32);
   store();
 }
 
+template <bool kOutF32>
 __global__ __launch_bounds__(64 * kWaves, 2) void wgrad_wide_kernel(
     const uint8_t *__restrict__ aq, const float *__restrict__ sa, const uint8_t *__restrict__ bq,
     const float *__restrict__ sb, const int32_t *__restrict__ offsets, int G, int64_t M, int64_t all_tiles, int P,
-    int Q, uint16_t *__restrict__ c) {
+    int Q, void *__restrict__ c) {
   __shared__ __attribute__((aligned(1024))) uint8_t stages[kRing * kWideStage];
   int g, p, q;
   if (!place((P + kWideRows - 1) / kWideRows, Q / kTile, g, p, q)) return;
-  wgrad_wide_run(aq, sa, bq, sb, offsets, G, M, all_tiles, P, Q, g, static_cast<int64_t>(p) * kWideRows,
-                 static_cast<int64_t>(q) * kTile, c, (FP8Q_LDS uint8_t *)stages);
+  wgrad_wide_run<kOutF32>(aq, sa, bq, sb, offsets, G, M, all_tiles, P, Q, g, static_cast<int64_t>(p) * kWideRows,
+                          static_cast<int64_t>(q) * kTile, c, (FP8Q_LDS uint8_t *)stages);
 }
 
 hipError_t launch_grouped_gemm_rowscaled(const uint8_t *aq, const float *sa, const uint8_t *bq, const float *sb,
@@ -599,17 +638,21 @@ hipError_t launch_grouped_gemm_rowscaled(const uint8_t *aq, const float *sa, con
   // 940 -> 870 us, BF16 622 -> 534 us; 4 experts over 16384 rows, where a tile is
   // 32 token tiles: one instead of 3, BF16 345 -> 310 us.
   const int64_t depth = M / (128 * G) + 1;  // about the token tiles of an expert
-  // BF16 output of experts with 8 token tiles or more, if that makes a 256 x 128 tile for every CU:
-  // 4 experts of 7168 x 2048 with 4, 8 and 12 token tiles take 59, 88 and 111 us by wide tiles, 56, 97
-  // and 130 by the others; 2048 x 2048, half as many tiles as CUs, 20 and 19.  P = 128 would leave half
-  // of each wide tile empty (16 experts of 128 x 8192 with 32 token tiles 160 and 107 us).
+  // Wide tiles for experts of 8 token tiles or more, with FP32 output 12, if that makes one for every
+  // CU.  4 experts of 7168 x 2048 with 4, 8 and 12 token tiles, BF16: 59, 88 and 111 us by wide tiles,
+  // 56, 97 and 130 by the others; 32 of 4096 x 7168 with 8 and 12, FP32: 2349 and 3090 us, 2197
+  // and 3054; 4 of 7168 x 2048 with 12, FP32: 204 and 212.  One expert of 2048 x 2048, half as many wide
+  // tiles as CUs, BF16: 20 and 19.  P = 128 would leave half of each wide tile empty (16 experts
+  // of 128 x 8192 with 32 token tiles, BF16, 160 and 107 us).
   const int64_t wide = G * ((P + kWideRows - 1) / kWideRows) * (Q / kTile);
-  if (!out_f32 && depth > 8 && P > kTile && wide >= device_cu_count()) {
+  if (depth > (out_f32 ? 12 : 8) && P > kTile && wide >= device_cu_count()) {
     const int64_t grid = 8 * G * ((wide / G + 7) / 8);
     if (grid > 0x7fffffff) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(wgrad_wide_kernel, dim3(static_cast<uint32_t>(grid)), dim3(64 * kWaves), 0, stream, aq, sa, bq, sb,
-                       offsets, static_cast<int>(G), M, M / 128 + G, static_cast<int>(P), static_cast<int>(Q),
-                       static_cast<uint16_t *>(c));
+    auto go = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(grid)), dim3(64 * kWaves), 0, stream, aq, sa, bq, sb, offsets,
+                         static_cast<int>(G), M, M / 128 + G, static_cast<int>(P), static_cast<int>(Q), c);
+    };
+    out_f32 ? go(wgrad_wide_kernel<true>) : go(wgrad_wide_kernel<false>);
     return hipGetLastError();
   }
   const int64_t tiles = G * (P / kTile) * (Q / kTile), slots = 2 * device_cu_count();

@@ -334,11 +334,14 @@ def test_runs_of_tiles(out_dtype):
         assert torch.equal(fq.fp8q_grouped_gemm_rowscaled(*ops[0], *ops[1], one, c, out_dtype=out_dtype)[0], got[g]), g
 
 
+@pytest.mark.parametrize("out_dtype", TYPES)
 @pytest.mark.parametrize("counts,P,Q,slack", [([1500, 900], 8320, 512, 0),
                                               ([1, 0, 129, 259, 385, 64, 4000, 5000], 384, 2048, 7),
-                                              ([0, 0, 5120, 0], 512, 4096, 100)])
-def test_wide_tiles(counts, P, Q, slack):
-    """BF16 gradients of experts with many tokens, computed in tiles of 256 x 128 (the last one of a P
+                                              ([0, 0, 5120, 0], 512, 4096, 100), ([2900, 900], 8320, 512, 0),
+                                              ([1, 0, 129, 259, 385, 64, 6000, 8000], 384, 2048, 7),
+                                              ([0, 0, 7000, 0], 512, 4096, 100)])
+def test_wide_tiles(counts, P, Q, slack, out_dtype):
+    """Gradients of experts with many tokens, computed in tiles of 256 x 128 (the last one of a P
     of 128 modulo 256 half empty): experts without tokens and of one to 40 token tiles, the same
     bits as each expert alone in the small tiles, rows and tokens behind them not touched."""
     G, M = len(counts), sum(counts) + slack
@@ -349,7 +352,7 @@ def test_wide_tiles(counts, P, Q, slack):
     b, sb = fq.fp8q_quantize_act_grouped(x, off, rows=False)[2:]
     w = sum(-(-c // 128) for c in counts)
     a[w:], b[w:], sa[w:], sb[w:] = 0x7F, 0x7F, float("nan"), float("nan")
-    all_c = torch.full((G + 2, P, Q), 7.0, dtype=torch.bfloat16, device="cuda")
+    all_c = torch.full((G + 2, P, Q), 7.0, dtype=out_dtype, device="cuda")
     got = fq.fp8q_grouped_gemm_rowscaled(a, sa, b, sb, off, M, out=all_c[1:G + 1])
     torch.cuda.synchronize()
     assert bool((all_c[0] == 7.0).all()) and bool((all_c[-1] == 7.0).all())
@@ -363,12 +366,16 @@ def test_wide_tiles(counts, P, Q, slack):
             continue
         one = dev(offsets_of([c]))
         ops = [fq.fp8q_quantize_act_grouped(t[row - c:row].contiguous(), one, rows=False)[2:] for t in (dy, x)]
-        assert torch.equal(fq.fp8q_grouped_gemm_rowscaled(*ops[0], *ops[1], one, c, out_dtype=torch.bfloat16)[0], got[g]), g
+        assert torch.equal(fq.fp8q_grouped_gemm_rowscaled(*ops[0], *ops[1], one, c, out_dtype=out_dtype)[0], got[g]), g
         h = [host(t) for t in (a[tiles][:, rows], sa[tiles][:, rows], b[tiles], sb[tiles])]
         h[0], h[2] = (np.ascontiguousarray(q.transpose(1, 0, 2).reshape(q.shape[1], -1)) for q in (h[0], h[2]))
         ref = ob.wgrad(*h)
         tol = og.tolerance(ob.row_norms_rowscaled(h[0], h[1]), ob.row_norms_rowscaled(h[2], h[3]))
-        within(f64(got[g][rows]), ref, tol + HALF[torch.bfloat16] * np.abs(ref), f"expert {g}")
+        if out_dtype == torch.float32:
+            # 128 additions in a tile, two scalings, one addition per tile
+            total = np.abs(oq.dequant_act(h[0], h[1])) @ np.abs(oq.dequant_act(h[2], h[3])).T
+            tol = np.minimum(tol, (130 + -(-c // 128)) * 2.0 ** -24 * (1 + 1e-4) * total)
+        within(f64(got[g][rows]), ref, tol + HALF[out_dtype] * np.abs(ref), f"expert {g}")
 
 
 def test_grouped_weight_gradient_without_rows():
