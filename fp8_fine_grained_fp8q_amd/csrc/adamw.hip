@@ -31,7 +31,7 @@
 
 namespace fp8q {
 
-constexpr int64_t kPerBlock = 2048;
+constexpr int64_t kPerBlock = kAdamwPerGroup;
 
 // The descriptors of a launch: as many as its 4 KB of kernel arguments hold.
 struct AdamE4M3 {
@@ -233,7 +233,7 @@ hipError_t launch_batches(const fp8q_adamw_tensor *tensors, int64_t count, bool 
     for (; i < count && table.count < AdamTable<kE4M3>::kMax; ++i) {
       const int64_t b = (tensors[i].n + kPerBlock - 1) / kPerBlock;
       if (b == 0) continue;
-      if (blocks + b > 0x7fffffff) break;  // the caller has checked that one tensor fits
+      if (!grid_fits(blocks + b, 256)) break;  // the caller has checked that one tensor fits
       table.t[table.count] = descriptor(tensors[i], table.t);
       table.first[table.count++] = static_cast<uint32_t>(blocks);
       blocks += b;

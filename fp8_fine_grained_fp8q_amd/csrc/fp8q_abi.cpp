@@ -238,7 +238,7 @@ fp8q_status fp8q_moe_sort(const int32_t *topk_ids, int64_t T, int64_t k, int64_t
                           int32_t *row_token, void *stream) {
   if (bad_dtype(dtype)) return FP8Q_ERR_DTYPE;
   if (bad_rows(T, k, capacity, H) || E < 1 || E > 1024 || e_begin < 0 || bad_dim(e_begin)) return FP8Q_ERR_SHAPE;
-  if (too_many(T, (H + 1023) / 1024) || T * ((H + 1023) / 1024) >= kMaxDim) return FP8Q_ERR_SHAPE;
+  if (!fp8q::grid_fits(fp8q::moe_sort_groups(T, k, dtype == FP8Q_OUT_F32, H), 256)) return FP8Q_ERR_SHAPE;
   if (!offsets || (T > 0 && (!topk_ids || !token_row)) || (T > 0 && H > 0 && !x) ||
       (capacity > 0 && ((H > 0 && !xs) || !row_token)))
     return FP8Q_ERR_NULL;
@@ -255,7 +255,7 @@ fp8q_status fp8q_moe_sort_backward(const void *dxs, int32_t in_dtype, int64_t ca
                                    void *stream) {
   if (bad_dtype(in_dtype) || bad_dtype(out_dtype)) return FP8Q_ERR_DTYPE;
   if (bad_rows(T, k, capacity, H)) return FP8Q_ERR_SHAPE;
-  if (too_many(T, (H + 1023) / 1024) || T * ((H + 1023) / 1024) >= kMaxDim) return FP8Q_ERR_SHAPE;
+  if (!fp8q::grid_fits(T * ((H + 2047) / 2048), 256)) return FP8Q_ERR_SHAPE;  // 2048 columns of a token each
   if (T == 0 || H == 0) return FP8Q_OK;
   if (!token_row || !dx || (capacity > 0 && !dxs)) return FP8Q_ERR_NULL;
   if (misaligned(token_row, 4) || misaligned(dx) || misaligned(dxs)) return FP8Q_ERR_ALIGN;
@@ -270,6 +270,7 @@ fp8q_status fp8q_moe_combine_backward(const void *dy, int32_t dy_dtype, const vo
                                       void *stream) {
   if (bad_dtype(dy_dtype) || bad_dtype(dtype)) return FP8Q_ERR_DTYPE;
   if (bad_rows(T, k, capacity, N)) return FP8Q_ERR_SHAPE;
+  if (!fp8q::grid_fits((T * k + 3) / 4, 256)) return FP8Q_ERR_SHAPE;  // a wave per slot
   if (T == 0) return FP8Q_OK;
   if (!token_row || !topk_weights || !dw || (N > 0 && (!dy || (capacity > 0 && (!expert_out || !dout)))))
     return FP8Q_ERR_NULL;
@@ -286,7 +287,7 @@ fp8q_status fp8q_swiglu_backward(const uint16_t *gu_bf16, const void *dh, int32_
                                  uint16_t *dgu_bf16, uint16_t *h_bf16, void *stream) {
   if (bad_dtype(dh_dtype)) return FP8Q_ERR_DTYPE;
   if (bad_dim(M) || bad_dim(I) || I % 8 != 0 || too_many(M, 2 * I)) return FP8Q_ERR_SHAPE;
-  if (M * (I / 8) > int64_t(256) * 0x7fffffff) return FP8Q_ERR_SHAPE;  // workgroups of 256 threads
+  if (!fp8q::grid_fits((M * (I / 8) + 255) / 256, 256)) return FP8Q_ERR_SHAPE;  // eight elements of h per thread
   if (M == 0 || I == 0) return FP8Q_OK;
   if (!gu_bf16 || !dh || !dgu_bf16) return FP8Q_ERR_NULL;
   if (misaligned(gu_bf16) || misaligned(dh) || misaligned(dgu_bf16) || misaligned(h_bf16)) return FP8Q_ERR_ALIGN;
@@ -299,7 +300,8 @@ fp8q_status fp8q_quantize_act_grouped(const uint16_t *x_bf16, const int32_t *off
                                       int64_t K, uint8_t *xq, float *sa, uint8_t *xqt, float *sat, void *stream) {
   if (G < 1 || bad_dim(G) || bad_dim(M_tot) || bad_dim(K) || K % 128 != 0 || too_many(M_tot, K))
     return FP8Q_ERR_SHAPE;
-  if (too_many(M_tot / 128 + G, K) || (M_tot / 128 + G) * (K / 64) >= kMaxDim) return FP8Q_ERR_SHAPE;
+  // 128 channels of a tile per workgroup, or 64 without the rows' codes
+  if (!fp8q::grid_fits((M_tot / 128 + G) * (K / (xq ? 128 : 64)), 256)) return FP8Q_ERR_SHAPE;
   if (M_tot == 0 || K == 0) return FP8Q_OK;
   if (!x_bf16 || !offsets || !xqt || !sat || !xq != !sa) return FP8Q_ERR_NULL;
   if (misaligned(x_bf16) || misaligned(offsets, 4) || misaligned(xq) || misaligned(sa) || misaligned(xqt) ||
@@ -318,7 +320,9 @@ fp8q_status fp8q_grouped_gemm_rowscaled(const uint8_t *aq, const float *sa, cons
     return FP8Q_ERR_SHAPE;
   if (P > kMaxGemmK || Q > kMaxGemmK) return FP8Q_ERR_SHAPE;  // 32-bit offsets within a tile's rows
   if (too_many(G, P) || too_many(G * P, Q)) return FP8Q_ERR_SHAPE;
-  if (G * ((P / 128) * (Q / 128) + 7) >= kMaxDim || M_tot / 128 + G >= kMaxDim) return FP8Q_ERR_SHAPE;
+  if (M_tot / 128 + G >= kMaxDim) return FP8Q_ERR_SHAPE;
+  // a workgroup per 128 x 128 tile of C, an expert's rounded up to eight of them
+  if (!fp8q::grid_fits(8 * G * (((P / 128) * (Q / 128) + 7) / 8), 512)) return FP8Q_ERR_SHAPE;
   if (P == 0 || Q == 0) return FP8Q_OK;
   if (!c || !offsets || (M_tot > 0 && (!aq || !sa || !bq || !sb))) return FP8Q_ERR_NULL;
   if (misaligned(aq) || misaligned(sa) || misaligned(bq) || misaligned(sb) || misaligned(offsets, 4) || misaligned(c))
@@ -343,7 +347,8 @@ fp8q_status fp8q_adamw(const fp8q_adamw_tensor *tensors, int64_t count, int32_t 
   bool work = false;
   for (int64_t i = 0; i < count; ++i) {
     const fp8q_adamw_tensor &t = tensors[i];
-    if (t.n < 0 || t.n >= (int64_t(1) << 40)) return FP8Q_ERR_SHAPE;
+    if (t.n < 0 || !fp8q::grid_fits(t.n / fp8q::kAdamwPerGroup + (t.n % fp8q::kAdamwPerGroup != 0), 256))
+      return FP8Q_ERR_SHAPE;
     if (t.n == 0) continue;
     if (!t.p || !t.grad || !t.m || !t.v || (e4m3 && (!t.m_scale || !t.v_scale))) return FP8Q_ERR_NULL;
     if (misaligned(t.p) || misaligned(t.grad) || misaligned(t.m) || misaligned(t.v) || misaligned(t.p_bf16) ||

@@ -9,6 +9,9 @@
 
 namespace fp8q {
 
+// HIP supports fewer than 2^32 threads per dimension of a grid.
+inline bool grid_fits(int64_t groups, int64_t threads) { return groups < (int64_t(1) << 32) / threads; }
+
 // Compute units of the current device (cached per device; 256 if the query fails).
 int device_cu_count();
 
@@ -64,6 +67,9 @@ hipError_t launch_moe_dispatch(const int32_t *ids, int64_t T, int64_t k, int64_t
 hipError_t launch_moe_combine(const void *out, bool in_f32, int64_t cap, int64_t N, const int32_t *token_row,
                               const float *w, int64_t T, int64_t k, void *y, bool out_f32, hipStream_t stream);
 
+// Workgroups of 256 threads of the copy in launch_moe_sort (the routing's fit for every T * k < 2^31).
+int64_t moe_sort_groups(int64_t T, int64_t k, bool f32, int64_t H);
+
 // The dispatch's routing with values in place of codes: xs[token_row[t][s]] = x[t], rows of H
 // BF16 or FP32 values.
 hipError_t launch_moe_sort(const int32_t *ids, int64_t T, int64_t k, int64_t e_begin, int64_t E, const void *x,
@@ -93,6 +99,8 @@ hipError_t launch_quant_act_grouped(const uint16_t *x, const int32_t *offsets, i
 hipError_t launch_grouped_gemm_rowscaled(const uint8_t *aq, const float *sa, const uint8_t *bq, const float *sb,
                                          const int32_t *offsets, int64_t G, int64_t M, int64_t P, int64_t Q,
                                           void *c, bool out_f32, hipStream_t stream);
+
+constexpr int64_t kAdamwPerGroup = 2048;  // elements of a workgroup of 256 threads
 
 // One AdamW step over `count` tensors (host array).
 hipError_t launch_adamw(const fp8q_adamw_tensor *tensors, int64_t count, bool grad_f32, bool e4m3,

@@ -539,7 +539,6 @@ hipError_t launch_quant_act_grouped(const uint16_t *x, const int32_t *offsets, i
                                     uint8_t *xq, float *sa, uint8_t *xqt, float *sat,
                                     hipStream_t stream) {
   const int64_t tiles = M / 128 + G;
-  if (tiles * (K / 64) > 0x7fffffff) return hipErrorInvalidValue;
   const dim3 block(256);
   if (xq != nullptr)
     hipLaunchKernelGGL(quant_act_grouped_kernel, dim3(static_cast<uint32_t>(tiles * (K / 128))), block, 0, stream, x,

@@ -50,7 +50,6 @@ __global__ __launch_bounds__(256) void swiglu_backward_kernel(const uint16_t *__
 hipError_t launch_swiglu_backward(const uint16_t *gu, const void *dh, bool dh_f32, int64_t M, int64_t I, uint16_t *dgu,
                                   uint16_t *h, hipStream_t stream) {
   const int64_t chunks = M * (I / 8), blocks = (chunks + 255) / 256;
-  if (blocks > 0x7fffffff) return hipErrorInvalidValue;
   const dim3 grid(static_cast<uint32_t>(blocks)), block(256);
   const uint64_t n = static_cast<uint64_t>(chunks);
   const uint32_t per_row = static_cast<uint32_t>(I / 8);

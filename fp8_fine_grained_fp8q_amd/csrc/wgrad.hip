@@ -647,7 +647,6 @@ hipError_t launch_grouped_gemm_rowscaled(const uint8_t *aq, const float *sa, con
   const int64_t wide = G * ((P + kWideRows - 1) / kWideRows) * (Q / kTile);
   if (depth > (out_f32 ? 12 : 8) && P > kTile && wide >= device_cu_count()) {
     const int64_t grid = 8 * G * ((wide / G + 7) / 8);
-    if (grid > 0x7fffffff) return hipErrorInvalidValue;
     auto go = [&](auto kernel) {
       hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(grid)), dim3(64 * kWaves), 0, stream, aq, sa, bq, sb, offsets,
                          static_cast<int>(G), M, M / 128 + G, static_cast<int>(P), static_cast<int>(Q), c);
@@ -660,7 +659,6 @@ hipError_t launch_grouped_gemm_rowscaled(const uint8_t *aq, const float *sa, con
   int64_t run = want < most ? want : most;
   run = run < 1 ? 1 : (run > Q / kTile ? Q / kTile : run);
   const int64_t grid = 8 * G * (((P / kTile) * ((Q / kTile + run - 1) / run) + 7) / 8);
-  if (grid > 0x7fffffff) return hipErrorInvalidValue;
   auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(grid)), dim3(64 * kWaves), 0, stream, aq, sa, bq, sb, offsets,
                        static_cast<int>(G), M, M / 128 + G, static_cast<int>(P), static_cast<int>(Q), static_cast<int>(run), c);

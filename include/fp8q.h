@@ -317,7 +317,8 @@ fp8q_status fp8q_moe_combine(const void *expert_out, int32_t in_dtype, int64_t c
  *   topk_ids, T, k, e_begin, E, capacity, offsets, token_row, row_token : as fp8q_moe_dispatch
  *   x  : [T][H] BF16 or FP32 per dtype;  xs : [capacity][H] of the same type (out); rows from
  *        min(offsets[E], capacity) on are left as they were
- * Requires H % 8 == 0 and T * ceil(H / 1024) < 2^31.  With T == 0 only `offsets` is written.
+ * Requires H % 8 == 0 and T * ceil(H / 8192) < 2^24 (BF16 rows of more than 4096 columns; FP32: of
+ * half as many; T * ceil(H / 2048) for shorter ones, FP32 1024).  With T == 0 only `offsets` is written.
  * Errors: FP8Q_ERR_DTYPE, otherwise as fp8q_moe_dispatch.
  */
 fp8q_status fp8q_moe_sort(const int32_t *topk_ids, int64_t T, int64_t k, int64_t e_begin, int64_t E, const void *x,
@@ -328,7 +329,8 @@ fp8q_status fp8q_moe_sort(const int32_t *topk_ids, int64_t T, int64_t k, int64_t
  * Gradient of the sort with respect to the tokens:
  *   dx[t][c] = sum over slots s with 0 <= token_row[t][s] < capacity of dxs[token_row[t][s]][c],
  * FP32 additions in slot order, rounded once to out_dtype (0 for a token without a row).
- *   dxs : [capacity][H] in in_dtype;  dx : [T][H] in out_dtype (out).  Requires H % 8 == 0.
+ *   dxs : [capacity][H] in in_dtype;  dx : [T][H] in out_dtype (out).  Requires H % 8 == 0 and
+ *   T * ceil(H / 2048) < 2^24.
  * Errors: as fp8q_moe_combine.
  */
 fp8q_status fp8q_moe_sort_backward(const void *dxs, int32_t in_dtype, int64_t capacity, int64_t H,
@@ -344,7 +346,7 @@ fp8q_status fp8q_moe_sort_backward(const void *dxs, int32_t in_dtype, int64_t ca
  * dispatch and the sort give such maps): a row that several slots shared would get one of
  * their gradients.
  *   dy : [T][N] in dy_dtype;  expert_out, dout : [capacity][N] in dtype;  dw : [T][k] FP32.
- * Requires N % 8 == 0.  Errors: as fp8q_moe_combine.
+ * Requires N % 8 == 0 and T * k <= 2^26 - 4.  Errors: as fp8q_moe_combine.
  */
 fp8q_status fp8q_moe_combine_backward(const void *dy, int32_t dy_dtype, const void *expert_out, int32_t dtype,
                                       int64_t capacity, int64_t N, const int32_t *token_row,
@@ -358,7 +360,7 @@ fp8q_status fp8q_moe_combine_backward(const void *dy, int32_t dy_dtype, const vo
  *   dgu_bf16 : [M][2I] (out), the layout of gu
  *   h_bf16 : [M][I] (out) or NULL: h again, rounded to BF16, for the weight gradient of the
  *            down projection
- * Requires I % 8 == 0, M >= 0.  M == 0 or I == 0 is a no-op.
+ * Requires I % 8 == 0, M >= 0 and M * I <= 2^35 - 2048.  M == 0 or I == 0 is a no-op.
  * Errors: FP8Q_ERR_DTYPE, FP8Q_ERR_SHAPE, FP8Q_ERR_NULL, FP8Q_ERR_ALIGN, FP8Q_ERR_DEVICE,
  * FP8Q_ERR_LAUNCH.
  */
@@ -379,7 +381,7 @@ fp8q_status fp8q_swiglu_backward(const uint16_t *gu_bf16, const void *dh, int32_
  *   xqt    : [B][K][128] E4M3 codes (out): xqt[b][k][i] is channel k of token i of tile b
  *   sat    : [B][K] FP32 scales (out)
  * What lies behind the last expert's last tile, and rows of no expert, are left as they were.
- * Requires G >= 1, K % 128 == 0, B * K / 64 < 2^31.  M_tot == 0 or K == 0 is a no-op.
+ * Requires G >= 1, K % 128 == 0, B * K < 2^31 (2^30 without xq and sa).  M_tot == 0 or K == 0 is a no-op.
  * Errors: FP8Q_ERR_SHAPE, FP8Q_ERR_NULL (also one of xq and sa without the other),
  * FP8Q_ERR_ALIGN, FP8Q_ERR_DEVICE, FP8Q_ERR_LAUNCH.
  */
@@ -398,8 +400,9 @@ fp8q_status fp8q_quantize_act_grouped(const uint16_t *x_bf16, const int32_t *off
  *   aq [B][P][128], sa [B][P] and bq [B][Q][128], sb [B][Q], B = M_tot / 128 + G : from
  *   fp8q_quantize_act_grouped with these offsets, G and M_tot (dW: aq of dY, bq of X)
  *   c [G][P][Q], BF16 or FP32 per out_dtype (out)
- * Requires G >= 1, P % 128 == 0, Q % 128 == 0, P and Q <= 2^22, M_tot >= 0.  With M_tot == 0 the operands are not
- * read (they may be NULL) and C is zeros.  P == 0 or Q == 0 is a no-op.
+ * Requires G >= 1, P % 128 == 0, Q % 128 == 0, P and Q <= 2^22, M_tot >= 0 and fewer than 2^23
+ * tiles of 128 x 128 in C (each expert's number rounded up to 8).  With M_tot == 0 the operands are
+ * not read (they may be NULL) and C is zeros.  P == 0 or Q == 0 is a no-op.
  * Errors: FP8Q_ERR_DTYPE, FP8Q_ERR_SHAPE, FP8Q_ERR_NULL, FP8Q_ERR_ALIGN, FP8Q_ERR_DEVICE,
  * FP8Q_ERR_LAUNCH.
  */
@@ -430,7 +433,7 @@ fp8q_status fp8q_grouped_gemm_rowscaled(const uint8_t *aq, const float *sa, cons
  *           grad_scale, so that a captured step can be replayed with new values.
  * Launches: one per 76 nonempty tensors (58 with E4M3 states).  Gradients are finite (else unspecified, and an E4M3
  * tile shares the damage).  Errors: FP8Q_ERR_DTYPE, FP8Q_ERR_VALUE, FP8Q_ERR_SHAPE (n < 0 or
- * n >= 2^40), FP8Q_ERR_NULL, FP8Q_ERR_ALIGN (scales and scalars 4-byte, the rest 16-byte),
+ * n > 2^35 - 2048), FP8Q_ERR_NULL, FP8Q_ERR_ALIGN (scales and scalars 4-byte, the rest 16-byte),
  * FP8Q_ERR_DEVICE, FP8Q_ERR_LAUNCH.
  */
 enum { FP8Q_STATE_F32 = 0, FP8Q_STATE_E4M3 = 1 };
