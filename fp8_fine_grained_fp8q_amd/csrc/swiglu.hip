@@ -4,7 +4,9 @@
 //
 // With s = 1 / (1 + e^-g):  du = dh * g s,  dg = dh * u * s (1 + g (1 - s)),  h = g s u.
 // s and 1 - s are both formed from e^-|g| (no overflow for any g, no cancellation in 1 - s)
-// with the hardware reciprocal (one ulp), all in FP32 with one rounding at the end.
+// with the hardware reciprocal (one ulp), all in FP32 with one rounding at the end.  Products are
+// ordered so that none overflows in between: g u first would make inf * 0 of a large u beside a
+// closed gate.
 //
 // Bound by HBM: 4 bytes of gu and 2 or 4 of dh in, 4 bytes of dgu out per element of h, and
 // 2 more for h itself, which the down projection's weight gradient contracts with and the
@@ -38,9 +40,12 @@ __global__ __launch_bounds__(256) void swiglu_backward_kernel(const uint16_t *__
     const float r = __builtin_amdgcn_rcpf(1.0f + t);
     const float s = (g[e] >= 0.0f ? 1.0f : t) * r;  // sigma(g)
     const float c = (g[e] >= 0.0f ? t : 1.0f) * r;  // 1 - sigma(g)
-    hv[e] = g[e] * u[e] * s;
-    du[e] = d[e] * (g[e] * s);
-    dg[e] = d[e] * u[e] * (s * __builtin_fmaf(g[e], c, 1.0f));
+    const float silu = g[e] * s, slope = s * __builtin_fmaf(g[e], c, 1.0f);  // |slope| < 1.1
+    hv[e] = silu * u[e];
+    du[e] = silu * d[e];
+    // the larger of d and u meets the slope first, halved: no overflow but the result's own
+    const bool less = fabsf(d[e]) < fabsf(u[e]);
+    dg[e] = (0.5f * slope) * (less ? u[e] : d[e]) * (less ? d[e] : u[e]) * 2.0f;
   }
   store8<false>(dgu, at_g, dg);
   store8<false>(dgu, at_u, du);

@@ -355,7 +355,9 @@ fp8q_status fp8q_moe_combine_backward(const void *dy, int32_t dy_dtype, const vo
 
 /*
  * Gradient of h = SiLU(g) * u (fp8q_swiglu_quantize_act_1x128 before its quantizer):
- *   du = dh * SiLU(g),  dg = dh * u * s (1 + g (1 - s)) with s = 1 / (1 + e^-g), FP32, rounded once.
+ *   du = dh * SiLU(g),  dg = dh * u * s (1 + g (1 - s)) with s = 1 / (1 + e^-g), FP32, rounded once;
+ *   no product in between overflows.  s has few bits left where it is below 2^-126 (gates below
+ *   -87) and is 0 below -104.
  *   gu_bf16 : [M][2I] (g = columns 0..I-1, u the rest);  dh : [M][I] BF16 or FP32 per dh_dtype
  *   dgu_bf16 : [M][2I] (out), the layout of gu
  *   h_bf16 : [M][I] (out) or NULL: h again, rounded to BF16, for the weight gradient of the
