@@ -599,17 +599,28 @@ __global__ __launch_bounds__(256) void swiglu_quant_act_1x128_kernel(const uint1
       const uint32_t gw[4] = {vg[k][i].x, vg[k][i].y, vg[k][i].z, vg[k][i].w};
       const uint32_t uw[4] = {vu[k][i].x, vu[k][i].y, vu[k][i].z, vu[k][i].w};
       float h[8];
-      float m = 0.0f;
+      // sigma(g) = 1 / (1 + e^-g) for g >= 0 and e^g / (1 + e^g) for g < 0: e^-|g| never overflows
+      auto values = [&](auto product) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float g = (e & 1) ? bf16_hi(gw[e >> 1]) : bf16_lo(gw[e >> 1]);
-        const float u = (e & 1) ? bf16_hi(uw[e >> 1]) : bf16_lo(uw[e >> 1]);
-        // sigma(g) = 1 / (1 + e^-g) for g >= 0 and e^g / (1 + e^g) for g < 0: e^-|g| never
-        // overflows
-        const float t = expf(-fabsf(g));
-        h[e] = g * u * ((g >= 0.0f ? 1.0f : t) * __builtin_amdgcn_rcpf(1.0f + t));
-        m = fmaxf(m, fabsf(h[e]));
+        for (int e = 0; e < 8; ++e) {
+          const float g = (e & 1) ? bf16_hi(gw[e >> 1]) : bf16_lo(gw[e >> 1]);
+          const float u = (e & 1) ? bf16_hi(uw[e >> 1]) : bf16_lo(uw[e >> 1]);
+          const float t = expf(-fabsf(g));
+          h[e] = product(g, u, (g >= 0.0f ? 1.0f : t) * __builtin_amdgcn_rcpf(1.0f + t));
+        }
+      };
+      values([](float g, float u, float sigma) { return g * u * sigma; });
+      // the bits of |h| order like the values, NaN above inf
+      uint32_t top = 0u;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(fabsf(h[e])));
+      if (top >= 0x7f800000u) {  // g u can overflow where h does not
+        values([](float g, float u, float sigma) { return g * sigma * u; });
+        top = 0u;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(fabsf(h[e])));
       }
+      const float m = __uint_as_float(top);
       const float s = row16_max(m) / kE4M3Max;
       const int64_t row = row0 + 4 * i + grp;
       const uint2 q = quant8f<false>(h, GroupDiv(s));

@@ -1,6 +1,6 @@
 """The SwiGLU gradient over BF16's whole range: every product of a gate, a value and a gradient from
 0 to the largest finite ones.  A factor that is nearly zero and two large ones give what their
-product is, not inf * 0, and nothing overflows that is finite."""
+product is, not inf * 0, and nothing overflows that is finite.  The forward quantizer's h likewise."""
 import itertools
 
 import numpy as np
@@ -52,3 +52,26 @@ def test_extremes(dtype):
         err = np.abs(x[inside] - ref[inside])
         worst = np.argmax(err - tol[inside])
         assert np.all(err <= tol[inside]), f"{what}: {x[inside][worst]} for {ref[inside][worst]}"
+
+
+def test_forward_of_a_closed_gate():
+    """Tiles in which the product of gate and value passes FP32 where h does not: h of 0 beside ordinary
+    ones, and h of a half-closed gate, whose codes are those of h."""
+    g = torch.full((4, 128), 1.5)
+    u = torch.linspace(-2, 2, 128).repeat(4, 1)
+    g[0, 3], u[0, 3] = -1e20, 1e20                       # h = 0
+    g[1, :], u[1, :] = -3e38, torch.linspace(1e38, 3e38, 128)
+    g[2, 7], u[2, 7] = -50.0, 3e37                       # h = -2.9e17 where g u is past FP32
+    gu = torch.cat([g, u], 1).to(torch.bfloat16).cuda()
+    xq, sa = fq.fp8q_swiglu_quantize_act_1x128(gu)
+    torch.cuda.synchronize()
+    x = gu.double().cpu().numpy()
+    with np.errstate(over="ignore"):
+        h = x[:, :128] * x[:, 128:] / (1 + np.exp(-x[:, :128]))
+    scale = sa[0].double().cpu().numpy()
+    # a few ulps of the largest h over 448
+    assert np.all(np.abs(scale * 448 - np.abs(h).max(1)) <= 2.0 ** -20 * np.abs(h).max(1)), scale
+    got = xq.view(torch.float8_e4m3fn).double().cpu().numpy() * scale[:, None]
+    # half a step of E4M3, normal or subnormal, beside h's own ulps
+    tol = (2.0 ** -4 + 2.0 ** -20) * np.abs(h) + 2.0 ** -10 * scale[:, None]
+    assert np.all(np.abs(got - h) <= tol)
