@@ -2,6 +2,7 @@
 // Every check runs before the first HIP call, so a bad call never touches the device.
 #include "fp8q.h"
 
+#include <float.h>
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdlib.h>
@@ -38,6 +39,10 @@ bool debug_checks() {
 }
 
 bool bad_dtype(int32_t d) { return d != FP8Q_OUT_BF16 && d != FP8Q_OUT_F32; }
+
+// The kernels take their numbers in FP32: a finite one that stays finite there, and nonzero if it is.
+bool f32_number(double v) { return fabs(v) <= FLT_MAX && (v == 0 || static_cast<float>(v) != 0.0f); }
+bool f32_beta(double v) { return v >= 0 && static_cast<float>(v) < 1.0f; }
 
 // Shared checks of the token maps [T][k] and of rows of `width` columns.
 bool bad_rows(int64_t T, int64_t k, int64_t capacity, int64_t width) {
@@ -341,8 +346,11 @@ fp8q_status fp8q_adamw(const fp8q_adamw_tensor *tensors, int64_t count, int32_t 
   const fp8q_adamw_hyper &h = *hyper;
   const double numbers[] = {h.lr, h.beta1, h.beta2, h.eps, h.weight_decay, h.grad_scale};
   for (double v : numbers)
-    if (!isfinite(v)) return FP8Q_ERR_VALUE;
-  if (h.beta1 < 0 || h.beta1 >= 1 || h.beta2 < 0 || h.beta2 >= 1 || h.eps < 0 || h.step < 1) return FP8Q_ERR_VALUE;
+    if (!f32_number(v)) return FP8Q_ERR_VALUE;
+  if (!f32_beta(h.beta1) || !f32_beta(h.beta2) || h.eps < 0 || h.step < 1) return FP8Q_ERR_VALUE;
+  if (!h.scalars && (!(fabs(1.0 - h.lr * h.weight_decay) <= FLT_MAX) ||
+                     !(fabs(h.lr / (1.0 - pow(h.beta1, static_cast<double>(h.step)))) <= FLT_MAX)))
+    return FP8Q_ERR_VALUE;
   const bool e4m3 = state_dtype == FP8Q_STATE_E4M3;
   bool work = false;
   for (int64_t i = 0; i < count; ++i) {
@@ -372,7 +380,7 @@ const char *fp8q_status_string(fp8q_status status) {
     case FP8Q_ERR_DEVICE: return "no usable HIP device";
     case FP8Q_ERR_LAUNCH: return "kernel launch failed";
     case FP8Q_ERR_OFFSETS: return "grouped GEMM offsets invalid (offsets[0] != 0, decreasing, or offsets[G] != M_tot)";
-    case FP8Q_ERR_VALUE: return "hyperparameter out of range (not finite, beta outside [0, 1), eps < 0 or step < 1)";
+    case FP8Q_ERR_VALUE: return "hyperparameter out of range (not a finite FP32 number, beta outside [0, 1), eps < 0, step < 1, or lr / (1 - beta1^step) or lr * weight_decay past FP32)";
     default: return "unknown status";
   }
 }

@@ -430,9 +430,11 @@ fp8q_status fp8q_grouped_gemm_rowscaled(const uint8_t *aq, const float *sa, cons
  *     p_bf16 : [n] BF16 (out), the new p rounded to nearest even, or NULL
  *     n >= 0 elements, any number (n == 0: skipped)
  *   hyper : HOST struct, read during the call only.  Requires 0 <= beta < 1, eps >= 0, step >= 1,
- *           every number finite.  `scalars`, if not NULL, is a DEVICE float[4] = {lr,
+ *           and numbers that FP32 holds: each finite there, nonzero if it is nonzero, and beta
+ *           below 1 after rounding; also 1 - lr weight_decay and lr / (1 - beta1^t).  With eps = 0 an
+ *           element whose v is 0 gets m / 0.  `scalars`, if not NULL, is a DEVICE float[4] = {lr,
  *           1 - beta1^t, 1 - beta2^t, grad_scale} read by the kernels in place of lr, step and
- *           grad_scale, so that a captured step can be replayed with new values.
+ *           grad_scale (not checked), so that a captured step can be replayed with new values.
  * Launches: one per 76 nonempty tensors (58 with E4M3 states).  Gradients are finite (else unspecified, and an E4M3
  * tile shares the damage).  Errors: FP8Q_ERR_DTYPE, FP8Q_ERR_VALUE, FP8Q_ERR_SHAPE (n < 0 or
  * n > 2^35 - 2048), FP8Q_ERR_NULL, FP8Q_ERR_ALIGN (scales and scalars 4-byte, the rest 16-byte),
