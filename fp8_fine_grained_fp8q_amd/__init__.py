@@ -618,13 +618,28 @@ def fp8q_grouped_gemm_rowscaled(aq, sa, bq, sb, offsets, m_tot: int, out_dtype=t
 
 
 class AdamwPlan:
-    """The tensors of an AdamW step, checked once (fp8q_adamw_plan makes it).  It holds them, so
-    their memory stays theirs as long as the plan lives; replacing a tensor's storage
-    (`tensor.data = ...`, `resize_`) needs a new plan."""
+    """The tensors of an AdamW step, their types, sizes and memory checked once (fp8q_adamw_plan makes
+    it).  It holds the tensors.  A step checks that each still has its memory and that a gradient
+    which was its parameter's `.grad` still is, and raises ValueError otherwise: `tensor.data = ...`,
+    a resized storage and zero_grad(set_to_none=True) need a new plan.  A captured step does
+    not check when it is replayed."""
 
     def __init__(self, tensors, descriptors, grad_dtype, state_dtype, device):
         self.tensors, self.descriptors = tensors, descriptors
         self.grad_dtype, self.state_dtype, self.device = grad_dtype, state_dtype, device
+        self.every = [t for each in tensors.values() for t in each]
+        self.addresses = list(map(torch.Tensor.data_ptr, self.every))
+        self.followed = [(p, g) for p, g in zip(tensors["params"], tensors["grads"]) if p.is_leaf and p.grad is g]
+
+    def check(self):
+        """Raises ValueError if a tensor's memory or a parameter's gradient is another one than the plan's.
+        (0.04 us a tensor: 9 us for 64 parameters with FP32 states.)"""
+        if list(map(torch.Tensor.data_ptr, self.every)) != self.addresses:
+            raise ValueError("a tensor of the plan has other memory than when the plan was made; make a new plan")
+        for p, g in self.followed:
+            if p.grad is not g:
+                raise ValueError("a parameter's .grad is not the plan's gradient any more; make a new plan, or keep the "
+                                 "gradients (zero_grad(set_to_none=False))")
 
 
 def fp8q_adamw_plan(params, grads, m, v, m_scales=None, v_scales=None, copies=None) -> AdamwPlan:
@@ -677,7 +692,8 @@ def fp8q_adamw_plan(params, grads, m, v, m_scales=None, v_scales=None, copies=No
 
 def fp8q_adamw(plan: AdamwPlan, lr: float, betas=(0.9, 0.95), eps: float = 1e-8, weight_decay: float = 0.0, step: int = 1,
                grad_scale: float = 1.0, scalars: torch.Tensor | None = None, stream=None) -> None:
-    """One AdamW step over the plan's tensors, in place.  `step` counts from 1.  `scalars`: a device
+    """One AdamW step over the plan's tensors, in place; ValueError if one of them has other memory or
+    another gradient than when the plan was made.  `step` counts from 1.  `scalars`: a device
     float32 [4] holding {lr, 1 - beta1^step, 1 - beta2^step, grad_scale}, read by the kernels in
     place of those arguments (a captured step is replayed with new values in it)."""
     if stream is not None:
@@ -689,6 +705,7 @@ def fp8q_adamw(plan: AdamwPlan, lr: float, betas=(0.9, 0.95), eps: float = 1e-8,
         _need(scalars, torch.float32, "scalars", (4,))
     if plan.device is None:
         return
+    plan.check()
     hyper = _AdamwHyper(lr, betas[0], betas[1], eps, weight_decay, grad_scale, step, _ptr(scalars) or None)
     s = _here(plan.tensors["params"][0], scalars)
     _check(load_library().fp8q_adamw(plan.descriptors, len(plan.tensors["params"]), plan.grad_dtype, plan.state_dtype,
