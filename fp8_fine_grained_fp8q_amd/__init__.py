@@ -649,6 +649,8 @@ def fp8q_adamw_plan(params, grads, m, v, m_scales=None, v_scales=None, copies=No
     bf16, written with the new parameters, or None.  All memory disjoint."""
     lists = {"params": params, "grads": grads, "m": m, "v": v, "m_scales": m_scales, "v_scales": v_scales,
              "copies": copies}
+    if any(lists[k] is None for k in ("params", "grads", "m", "v")):
+        raise ValueError("params, grads, m and v are needed")
     lists = {k: list(x) for k, x in lists.items() if x is not None}
     count = len(lists["params"])
     if any(len(x) != count for x in lists.values()):
@@ -656,9 +658,9 @@ def fp8q_adamw_plan(params, grads, m, v, m_scales=None, v_scales=None, copies=No
     e4m3 = "m_scales" in lists
     if e4m3 != ("v_scales" in lists):
         raise ValueError("m_scales and v_scales go together")
-    grad = lists["grads"][0].dtype if count else torch.float32
+    grad = getattr(lists["grads"][0], "dtype", None) if count else torch.float32  # None: a parameter's .grad may be
     if grad not in (torch.bfloat16, torch.float32):
-        raise ValueError("grads must be bfloat16 or float32")
+        raise ValueError("grads must be bfloat16 or float32 tensors")
     state = torch.uint8 if e4m3 else torch.float32
     types = {"params": torch.float32, "grads": grad, "m": state, "v": state, "m_scales": torch.float32,
              "v_scales": torch.float32, "copies": torch.bfloat16}

@@ -50,3 +50,12 @@ def test_gradients_of_their_own_do_not_follow():
     made, p, *_ = plan(own_grads=False)
     p[2].grad = torch.zeros(300)
     made.check()
+
+
+def test_missing_lists_and_gradients():
+    z = [torch.zeros(4)]
+    for lists in ((None, z, z, z), (z, None, z, z), (z, z, None, z), (z, z, z, None)):
+        with pytest.raises(ValueError, match="are needed"):
+            fq.fp8q_adamw_plan(*lists)
+    with pytest.raises(ValueError, match="bfloat16 or float32"):
+        fq.fp8q_adamw_plan(z, [None], z, z)       # a parameter without a gradient
