@@ -136,15 +136,21 @@ __device__ __forceinline__ void expert_tiles(const int32_t *offsets, int G, int6
   first = tiles > 0 ? static_cast<int>(first64) : 0;
 }
 
-// The tile row p and the run of tile columns r of expert g that this workgroup computes, of tp
-// rows and `runs` runs; false for workgroups past an expert's last run.  Workgroups are dealt
-// round-robin to the 8 XCDs.  Each XCD gets a contiguous eighth of every expert's runs, four rows
+// The rows that are routed, offsets[G] of the M that there is room for.
+__device__ __forceinline__ int routed_rows(const int32_t *offsets, int G, int64_t M) {
+  const int n = offsets[G];
+  return n < 0 ? 0 : (n > M ? static_cast<int>(M) : n);
+}
+
+// The tile row p and the run of tile columns r of expert g that unit `unit` computes, of tp
+// rows and `runs` runs; false for units past an expert's last run.  Workgroups are dealt
+// round-robin to the 8 XCDs, and a grid of several units per workgroup is a multiple of 8.  Each XCD gets a contiguous eighth of every expert's runs, four rows
 // of tiles at a time, column by column: neighbouring workgroups share operands in their L2 and
 // write neighbouring parts of the same rows, and experts of different sizes load all XCDs alike
 // (whole experts per XCD: 4 uneven experts over 16384 rows 350 us instead of 314 us).
-__device__ __forceinline__ bool place(int tp, int runs, int &g, int &p, int &r) {
+__device__ __forceinline__ bool place(uint32_t unit, int tp, int runs, int &g, int &p, int &r) {
   const int per = (tp * runs + 7) / 8;
-  const int xcd = blockIdx.x % 8, idx = blockIdx.x / 8;
+  const int xcd = static_cast<int>(unit % 8), idx = static_cast<int>(unit / 8);
   g = idx / per;
   const int in_g = xcd * per + idx % per;
   if (in_g >= tp * runs) return false;
@@ -332,15 +338,17 @@ __device__ __forceinline__ void wgrad_run(const uint8_t *__restrict__ aq, const 
   }
 }
 
+// Leaves if the routed rows make `deepest` token tiles of an expert or more on average (0: never).
 template <bool kOutF32>
 __global__ __launch_bounds__(64 * kWaves, 4) void wgrad_kernel(
     const uint8_t *__restrict__ aq, const float *__restrict__ sa, const uint8_t *__restrict__ bq,
     const float *__restrict__ sb, const int32_t *__restrict__ offsets, int G, int64_t M, int64_t all_tiles, int P,
-    int Q, int run, void *__restrict__ c) {
+    int Q, int run, int deepest, void *__restrict__ c) {
   __shared__ __attribute__((aligned(1024))) uint8_t stages[2 * kStage];
+  if (deepest > 0 && routed_rows(offsets, G, M) >= deepest * (int64_t(kTile) * G)) return;
   const int tp = P / kTile, tq = Q / kTile;
   int g, p, r;
-  if (!place(tp, (tq + run - 1) / run, g, p, r)) return;
+  if (!place(blockIdx.x, tp, (tq + run - 1) / run, g, p, r)) return;
   const int q = r * run;
   wgrad_run<kOutF32>(aq, sa, bq, sb, offsets, G, M, all_tiles, P, Q, g, static_cast<int64_t>(p) * kTile,
                      static_cast<int64_t>(q) * kTile, tq - q < run ? tq - q : run, c, (FP8Q_LDS uint8_t *)stages);
@@ -616,54 +624,68 @@ __device__ __forceinline__ void wgrad_wide_run(const uint8_t *__restrict__ aq, c
   store();
 }
 
+// Leaves if the routed rows make fewer than `deepest` token tiles of an expert on average.  A workgroup
+// takes every gridDim.x-th tile, so that few of them have to leave.
 template <bool kOutF32>
 __global__ __launch_bounds__(64 * kWaves, 2) void wgrad_wide_kernel(
     const uint8_t *__restrict__ aq, const float *__restrict__ sa, const uint8_t *__restrict__ bq,
     const float *__restrict__ sb, const int32_t *__restrict__ offsets, int G, int64_t M, int64_t all_tiles, int P,
-    int Q, void *__restrict__ c) {
+    int Q, int deepest, void *__restrict__ c) {
   __shared__ __attribute__((aligned(1024))) uint8_t stages[kRing * kWideStage];
-  int g, p, q;
-  if (!place((P + kWideRows - 1) / kWideRows, Q / kTile, g, p, q)) return;
-  wgrad_wide_run<kOutF32>(aq, sa, bq, sb, offsets, G, M, all_tiles, P, Q, g, static_cast<int64_t>(p) * kWideRows,
-                          static_cast<int64_t>(q) * kTile, c, (FP8Q_LDS uint8_t *)stages);
+  if (routed_rows(offsets, G, M) < deepest * (int64_t(kTile) * G)) return;
+  const int tp = (P + kWideRows - 1) / kWideRows, tq = Q / kTile, units = 8 * G * ((tp * tq + 7) / 8);
+  for (int u = blockIdx.x; u < units; u += gridDim.x) {
+    int g, p, q;
+    if (!place(u, tp, tq, g, p, q)) continue;
+    // its last barrier is behind every wave's last read, and a wave's copies are all done
+    wgrad_wide_run<kOutF32>(aq, sa, bq, sb, offsets, G, M, all_tiles, P, Q, g, static_cast<int64_t>(p) * kWideRows,
+                            static_cast<int64_t>(q) * kTile, c, (FP8Q_LDS uint8_t *)stages);
+  }
 }
 
 hipError_t launch_grouped_gemm_rowscaled(const uint8_t *aq, const float *sa, const uint8_t *bq, const float *sb,
                                          const int32_t *offsets, int64_t G, int64_t M, int64_t P, int64_t Q,
                                          void *c, bool out_f32, hipStream_t stream) {
-  // Tiles per workgroup, one after the other in a row of tiles: with few tokens per expert the
-  // start of a workgroup (its expert's offsets, the first copies) costs as much as a tile, so a
-  // workgroup takes about 8 token tiles' work as long as four workgroups per slot remain.  32
-  // experts over 8192 rows: 3 tiles instead of one, FP32
-  // 940 -> 870 us, BF16 622 -> 534 us; 4 experts over 16384 rows, where a tile is
-  // 32 token tiles: one instead of 3, BF16 345 -> 310 us.
-  const int64_t depth = M / (128 * G) + 1;  // about the token tiles of an expert
-  // Wide tiles for experts of 8 token tiles or more, with FP32 output 12, if that makes one for every
-  // CU.  4 experts of 7168 x 2048 with 4, 8 and 12 token tiles, BF16: 59, 88 and 111 us by wide tiles,
+  const int64_t cus = device_cu_count(), tp = P / kTile, tq = Q / kTile, tile = kTile * G;
+  // Wide tiles for experts of 8 token tiles or more on average, with FP32 output 12, if that makes one for
+  // every CU.  4 experts of 7168 x 2048 with 4, 8 and 12 token tiles, BF16: 59, 88 and 111 us by wide tiles,
   // 56, 97 and 130 by the others; 32 of 4096 x 7168 with 8 and 12, FP32: 2349 and 3090 us, 2197
   // and 3054; 4 of 7168 x 2048 with 12, FP32: 204 and 212.  One expert of 2048 x 2048, half as many wide
   // tiles as CUs, BF16: 20 and 19.  P = 128 would leave half of each wide tile empty (16 experts
   // of 128 x 8192 with 32 token tiles, BF16, 160 and 107 us).
-  const int64_t wide = G * ((P + kWideRows - 1) / kWideRows) * (Q / kTile);
-  if (depth > (out_f32 ? 12 : 8) && P > kTile && wide >= device_cu_count()) {
-    const int64_t grid = 8 * G * ((wide / G + 7) / 8);
-    auto go = [&](auto kernel) {
-      hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(grid)), dim3(64 * kWaves), 0, stream, aq, sa, bq, sb, offsets,
-                         static_cast<int>(G), M, M / 128 + G, static_cast<int>(P), static_cast<int>(Q), c);
-    };
-    out_f32 ? go(wgrad_wide_kernel<true>) : go(wgrad_wide_kernel<false>);
-    return hipGetLastError();
-  }
-  const int64_t tiles = G * (P / kTile) * (Q / kTile), slots = 2 * device_cu_count();
-  const int64_t want = (8 + depth - 1) / depth, most = tiles / (4 * slots);
-  int64_t run = want < most ? want : most;
-  run = run < 1 ? 1 : (run > Q / kTile ? Q / kTile : run);
-  const int64_t grid = 8 * G * (((P / kTile) * ((Q / kTile + run - 1) / run) + 7) / 8);
-  auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(grid)), dim3(64 * kWaves), 0, stream, aq, sa, bq, sb, offsets,
-                       static_cast<int>(G), M, M / 128 + G, static_cast<int>(P), static_cast<int>(Q), static_cast<int>(run), c);
+  // M only bounds the rows, and how many are routed is known on the device: the value sort's default
+  // capacity has room for every expert to be local.  So where M allows wide tiles both kernels are
+  // launched, and the one that the offsets do not call for leaves at once (about 5 us).  8192 tokens x 8
+  // slots, 32 of 256 experts of 4096 x 7168 local, 8192 of 65536 rows routed: FP32 1060 -> 850 us, BF16
+  // 680 -> 510 against wide tiles by M.
+  const int64_t wide = (P + kWideRows - 1) / kWideRows * tq;
+  const int deepest = out_f32 ? 12 : 8;
+  const bool maybe_wide = M >= deepest * tile && P > kTile && G * wide >= cus;
+  // Tiles that a workgroup computes one after the other in a row of them: with few tokens per expert the
+  // start of a workgroup (its expert's offsets, the first copies) costs as much as a tile.  Four, or two
+  // for experts of half a token tile, as long as four workgroups per slot (two on a CU) remain.  32
+  // experts of 7168 x 2048, BF16, by 1, 2, 4 and 8 tiles: 32 rows each 202, 151, 171 and 176 us, 128 rows
+  // 243, 188, 180 and 177, 256 rows 306, 256, 251 and 245, 600 rows 476, 444, 427 and 458; FP32 less, 256
+  // rows 453, 433, 413 and 419.
+  int64_t run = G * tp * tq / (8 * cus);
+  const int64_t longest = M < tile / 2 ? 2 : 4;
+  run = run < 1 ? 1 : (run > longest ? longest : run);
+  run = run > tq ? tq : run;
+  auto small = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(8 * G * ((tp * ((tq + run - 1) / run) + 7) / 8))),
+                       dim3(64 * kWaves), 0, stream, aq, sa, bq, sb, offsets, static_cast<int>(G), M, M / kTile + G,
+                       static_cast<int>(P), static_cast<int>(Q), static_cast<int>(run), maybe_wide ? deepest : 0, c);
   };
-  out_f32 ? go(wgrad_kernel<true>) : go(wgrad_kernel<false>);
+  out_f32 ? small(wgrad_kernel<true>) : small(wgrad_kernel<false>);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !maybe_wide) return e;
+  const int64_t units = 8 * G * ((wide + 7) / 8);
+  auto large = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(units < 4 * cus ? units : 4 * cus)), dim3(64 * kWaves), 0, stream,
+                       aq, sa, bq, sb, offsets, static_cast<int>(G), M, M / kTile + G, static_cast<int>(P),
+                       static_cast<int>(Q), deepest, c);
+  };
+  out_f32 ? large(wgrad_wide_kernel<true>) : large(wgrad_wide_kernel<false>);
   return hipGetLastError();
 }
 

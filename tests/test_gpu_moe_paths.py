@@ -133,9 +133,9 @@ def offsets_of(counts):
     return dev(np.concatenate([[0], np.cumsum(counts)]).astype(np.int32))
 
 
-# experts of no, one, two and three token tiles; a row of tiles of 17 columns, so that the last run of 4 or
-# 8 is shorter
-RUNS = {"3 to 8 tiles in a row": ([0, 100, 128, 129, 256, 300, 384, 1] * 8, 2048, 2176),
+# experts of no, one, two and three token tiles; a row of 17 tiles, so that the last run of four or two is
+# shorter
+RUNS = {"up to three token tiles each": ([0, 100, 128, 129, 256, 300, 384, 1] * 8, 2048, 2176),
         "about 100 tokens each": ([0, 100, 128, 129, 40, 300, 3, 1] * 8, 2048, 2176),
         "one token each": ([1, 0, 1, 2] * 20, 1920, 2176)}
 
