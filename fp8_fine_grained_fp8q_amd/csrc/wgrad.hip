@@ -11,7 +11,8 @@
 // FP32 instruction of depth 1: each is one rounded product, and acc = P * S + acc is one vector
 // operation per element and token tile, where both scales vary inside a lane and two were
 // needed, (P * sa) * sb + acc (FP32 output 500 -> 488 us and 860 -> 838 us for the two sizes
-// below).  S under 2^-126 loses bits: such terms are below 448^2 * 128 * 2^-126 = 3e-31.
+// below).  S can pass FP32's range at either end where its term does not; waves watch the scales
+// they meet and form such blocks again without it (wide_range_block; the watching costs 1 to 2 %).
 //
 // BF16 output takes the FP8 matrix instructions.  Their sums of 64 products are off by 1.4e-5
 // (2-norm, normal data, any of the shapes), far below BF16's rounding but above FP32's: FP32
@@ -136,6 +137,84 @@ __device__ __forceinline__ void expert_tiles(const int32_t *offsets, int G, int6
   first = tiles > 0 ? static_cast<int>(first64) : 0;
 }
 
+// The largest and the smallest nonzero scales of rows and of columns that a lane has seen, as bits (which
+// order like the values; 0 less one wraps round past all of them).
+struct ScaleRange {
+  uint32_t top_r = 0u, low_r = ~0u, top_c = 0u, low_c = ~0u;
+  template <typename... Columns>
+  __device__ __forceinline__ void see(float sr, Columns... sc) {
+    top_r = max(top_r, __float_as_uint(sr));
+    low_r = min(low_r, __float_as_uint(sr) - 1u);
+    ((top_c = max(top_c, __float_as_uint(sc)), low_c = min(low_c, __float_as_uint(sc) - 1u)), ...);
+  }
+  // Whether a product of a row's and a column's scale, of all lanes, may not be a normal FP32 number.
+  // None if every scale is in [2^-63, 2^63].
+  __device__ __forceinline__ bool wide() const {
+    constexpr uint32_t kTop = (127u + 63u) << 23, kLow = ((127u - 63u) << 23) - 1u;
+    if (__ballot(max(top_r, top_c) > kTop || min(low_r, low_c) < kLow) == 0) return false;
+    uint32_t tr = top_r, lr = low_r, tc = top_c, lc = low_c;
+#pragma unroll 1
+    for (int m = 32; m >= 1; m >>= 1) {
+      tr = max(tr, static_cast<uint32_t>(__shfl_xor(static_cast<int>(tr), m)));
+      lr = min(lr, static_cast<uint32_t>(__shfl_xor(static_cast<int>(lr), m)));
+      tc = max(tc, static_cast<uint32_t>(__shfl_xor(static_cast<int>(tc), m)));
+      lc = min(lc, static_cast<uint32_t>(__shfl_xor(static_cast<int>(lc), m)));
+    }
+    if (lr == ~0u || lc == ~0u) return false;  // all zeros
+    // the largest below 2^(e + 1), e the sum of two exponents; the smallest at least 2^e (subnormal: 2^-149)
+    auto exponent = [](uint32_t bits) { return static_cast<int>(bits >> 23) - 127; };
+    auto least = [&](uint32_t less_one) { return less_one < 0x7fffffu ? -149 : exponent(less_one + 1u); };
+    return __builtin_amdgcn_readfirstlane(exponent(tr) + exponent(tc) > 125 || least(lr) + least(lc) < -126) != 0;
+  }
+};
+
+// Rows row .. row + 31 and columns col, col + 2 .. col + 62 of an expert's gradient, laid out as the wave's
+// blocks, without the product of the scales: the smaller one multiplies a tile's sum, the larger
+// one the result, so that nothing overflows that the term does not, and what underflows is below
+// 2^-149 times the larger scale.  For scales that ScaleRange finds wide, which ordinary tensors do
+// not have: straight from memory, two to nine times slower.
+template <bool kOutF32>
+__device__ __forceinline__ void wide_range_block(const uint8_t *aq, const float *sa, const uint8_t *bq, const float *sb,
+                                                 int64_t P, int64_t Q, int first, int tiles, int64_t row, int64_t col,
+                                                 v16f &acc) {
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));  // keeps the addresses from being formed long before
+  const int l32 = lane & 31, half = lane >> 5;
+  row += static_cast<int64_t>(first) * P;
+  col += static_cast<int64_t>(first) * Q + 2 * l32;
+  const uint8_t *a = aq + (row + l32) * 128 + 16 * half, *b = bq + col * 128 + 16 * half;
+  sa += row + 4 * half;
+  sb += col;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
+#pragma unroll 1
+  for (int t = 0; t < tiles; ++t, a += P * 128, b += Q * 128, sa += P, sb += Q) {
+    v16f part = {};
+    if constexpr (kOutF32) {
+#pragma unroll 1
+      for (int m = 0; m < 4; ++m) {
+        const v4i x = *reinterpret_cast<const v4i *>(a + 32 * m), y = *reinterpret_cast<const v4i *>(b + 32 * m);
+#pragma unroll
+        for (int r = 0; r < 4; r += 2)
+          part = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen8(x[r], x[r + 1]), widen8(y[r], y[r + 1]), part, 0, 0, 0);
+      }
+    } else {
+#pragma unroll 1
+      for (int m = 0; m < 4; m += 2) {
+        const v4i *x = reinterpret_cast<const v4i *>(a + 32 * m), *y = reinterpret_cast<const v4i *>(b + 32 * m);
+        part = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(join(x[0], x[2]), join(y[0], y[2]), part, 0, 0, 0, 0, 0, 0);
+      }
+    }
+    const float sc = *sb;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if (i % 4 == 0) __builtin_amdgcn_sched_barrier(0);  // few of the rows' scales at a time
+      const float sr = sa[8 * (i >> 2) + (i & 3)];
+      acc[i] = __builtin_fmaf(part[i] * fminf(sr, sc), fmaxf(sr, sc), acc[i]);
+    }
+  }
+}
+
 // The rows that are routed, offsets[G] of the M that there is room for.
 __device__ __forceinline__ int routed_rows(const int32_t *offsets, int G, int64_t M) {
   const int n = offsets[G];
@@ -202,7 +281,9 @@ __device__ __forceinline__ void wgrad_run(const uint8_t *__restrict__ aq, const 
 
   // Element i of block n is row 8 (i / 4) + 4 half + i % 4, column 2 l32 + n of the wave.
   v16f acc[2];
+  ScaleRange range;
   auto clear = [&]() {
+    range = ScaleRange();
 #pragma unroll
     for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -259,6 +340,7 @@ __device__ __forceinline__ void wgrad_run(const uint8_t *__restrict__ aq, const 
   int j = 0, s = 0;          // the stage being multiplied
   bool ahead = false;        // the next stage's copies are issued already
   int stores = 0;            // 2: a tile ended a stage ago; 1: two stages ago
+  uint32_t redo = 0;         // the run's tiles (at most 4) whose scales' products FP32 does not hold
   auto stage = [&](auto parity) {
     constexpr int kCur = decltype(parity)::value * kStage;  // the stage's place in LDS
     FP8Q_LDS uint8_t *cur = st + kCur, *next = st + (kStage - kCur);
@@ -312,6 +394,7 @@ __device__ __forceinline__ void wgrad_run(const uint8_t *__restrict__ aq, const 
     }
     float sr, sc;
     read_scales<kCur>(sr, sc, at_sr, at_sc);
+    range.see(sr, sc);
     const v32f scale = __builtin_amdgcn_mfma_f32_32x32x1f32(sr, sc, v32f{}, 0, 0, 0);
 #pragma unroll
     for (int n = 0; n < 2; ++n)
@@ -325,6 +408,7 @@ __device__ __forceinline__ void wgrad_run(const uint8_t *__restrict__ aq, const 
           ahead = true;
         }
       }
+      redo |= range.wide() ? 1u << j : 0u;
       store(j);
       clear();
       stores = 2;
@@ -335,6 +419,15 @@ __device__ __forceinline__ void wgrad_run(const uint8_t *__restrict__ aq, const 
   };
   load(0, 0, st);
   while (stage(std::integral_constant<int, 0>{}) && stage(std::integral_constant<int, 1>{})) {
+  }
+  if (redo == 0) return;
+  wait_loads<0>();  // the tiles' first stores
+  for (j = 0; j < count; ++j) {
+    if ((redo >> j & 1u) == 0) continue;
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+      wide_range_block<kOutF32>(aq, sa, bq, sb, P, Q, first, tiles, p0 + wm * 32, q0 + j * kTile + wn * 64 + n, acc[n]);
+    store(j);
   }
 }
 
@@ -515,6 +608,7 @@ __device__ __forceinline__ void wgrad_wide_run(const uint8_t *__restrict__ aq, c
   }
   // Column block n's sums, part[.][n], are scaled and added in the next reading phase, with BF16 output
   // block 0's beside block 1's products.
+  ScaleRange range;
   int cur = 0;           // the stage's place in LDS
   v32f scale[2] = {};    // of column block n; BF16 output keeps one at a time, in scale[1]
   auto add = [&](int n, const v32f &by, int from, int to) {
@@ -569,6 +663,7 @@ __device__ __forceinline__ void wgrad_wide_run(const uint8_t *__restrict__ aq, c
             widen(step + 1, k);
             pinned(wide[(step + 1) & 1][k]);
             if (k == 0) copy(step);
+            if (step == 0 && k == 1) range.see(sr, sc.x, sc.y);
             pin();
           }
         }
@@ -591,6 +686,7 @@ __device__ __forceinline__ void wgrad_wide_run(const uint8_t *__restrict__ aq, c
       multiply(0, 0, 1, part[0][0]);
       copy(2);
       copy(3);
+      range.see(sr, sc.x, sc.y);
       pin();
       multiply(0, 1, 0, zero);
       copy(4);
@@ -621,6 +717,12 @@ __device__ __forceinline__ void wgrad_wide_run(const uint8_t *__restrict__ aq, c
   wait_loads<0>();
   if (kOutF32) add(0, scale[0], 0, 32);
   add(1, scale[1], 0, 32);
+  if (mine && range.wide()) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      wide_range_block<kOutF32>(aq, sa, bq, sb, P, Q, first, tiles, p0 + wm * 64 + 32 * (k >> 1), q0 + wn * 64 + (k & 1),
+                                acc[k >> 1][k & 1]);
+  }
   store();
 }
 

@@ -395,8 +395,10 @@ fp8q_status fp8q_quantize_act_grouped(const uint16_t *x_bf16, const int32_t *off
  *   C[g][p][q] = sum over expert g's token tiles b of
  *                sa[b][p] * sb[b][q] * sum_i decode(aq[b][p][i]) decode(bq[b][q][i])
  * with FP32 promotion at every tile of 128 tokens, tiles ascending: the scales' product is
- * rounded to FP32 (its range is FP32's too), then multiplied with the tile's sum and added in one
- * operation.  Zeros for an expert without rows.  With BF16 output a tile's sum comes from the FP8 matrix instructions (off by
+ * rounded to FP32, then multiplied with the tile's sum and added in one operation.  In blocks of C with
+ * such products outside FP32's normal range (at most 64 x 64 of C; two to nine times slower) the
+ * smaller scale multiplies the tile's sum and the larger one the result instead.  Zeros for an
+ * expert without rows.  With BF16 output a tile's sum comes from the FP8 matrix instructions (off by
  * about 1.4e-5 of the sum's norm); with FP32 output the codes are widened to BF16, exactly, and
  * multiplied by the BF16 instructions, whose sums are good to FP32.
  *   aq [B][P][128], sa [B][P] and bq [B][Q][128], sb [B][Q], B = M_tot / 128 + G : from
