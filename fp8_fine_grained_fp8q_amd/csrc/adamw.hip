@@ -61,7 +61,7 @@ struct AdamTable {
 
 struct AdamHyper {
   float b1, c1, b2, c2;  // beta and 1 - beta
-  float eps, wd, lr;
+  float eps, wd;
   float decay, step, root;  // 1 - lr wd, lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
   float grad_scale;
   const float *scalars;  // device {lr, 1 - b1^t, 1 - b2^t, grad_scale} in place of the host's, or null
@@ -260,7 +260,6 @@ hipError_t launch_adamw(const fp8q_adamw_tensor *tensors, int64_t count, bool gr
   hy.c2 = static_cast<float>(1.0 - h.beta2);
   hy.eps = static_cast<float>(h.eps);
   hy.wd = static_cast<float>(h.weight_decay);
-  hy.lr = static_cast<float>(h.lr);
   hy.decay = static_cast<float>(1.0 - h.lr * h.weight_decay);
   hy.step = static_cast<float>(h.lr / (1.0 - pow(h.beta1, static_cast<double>(h.step))));
   hy.root = static_cast<float>(1.0 / sqrt(1.0 - pow(h.beta2, static_cast<double>(h.step))));
