@@ -12,7 +12,8 @@
 // operation per element and token tile, where both scales vary inside a lane and two were
 // needed, (P * sa) * sb + acc (FP32 output 500 -> 488 us and 860 -> 838 us for the two sizes
 // below).  S can pass FP32's range at either end where its term does not; waves watch the scales
-// they meet and form such blocks again without it (wide_range_block; the watching costs 1 to 2 %).
+// they meet and form such blocks again without it (ScaleRange, wide_products, wide_range_block; the
+// watching costs 1 to 2 % of the cycles).
 //
 // BF16 output takes the FP8 matrix instructions.  Their sums of 64 products are off by 1.4e-5
 // (2-norm, normal data, any of the shapes), far below BF16's rounding but above FP32's: FP32
@@ -137,41 +138,57 @@ __device__ __forceinline__ void expert_tiles(const int32_t *offsets, int G, int6
   first = tiles > 0 ? static_cast<int>(first64) : 0;
 }
 
-// The largest and the smallest nonzero scales of rows and of columns that a lane has seen, as bits (which
-// order like the values; 0 less one wraps round past all of them).
+// The largest and smallest scales that a lane has met in a tile of C, as bits (which order like the values).
+// If all are in [2^-63, 2^63] every product of two is a normal FP32 number.
 struct ScaleRange {
-  uint32_t top_r = 0u, low_r = ~0u, top_c = 0u, low_c = ~0u;
-  template <typename... Columns>
-  __device__ __forceinline__ void see(float sr, Columns... sc) {
-    top_r = max(top_r, __float_as_uint(sr));
-    low_r = min(low_r, __float_as_uint(sr) - 1u);
-    ((top_c = max(top_c, __float_as_uint(sc)), low_c = min(low_c, __float_as_uint(sc) - 1u)), ...);
+  uint32_t top = 0u, low = ~0u;
+  __device__ __forceinline__ void see(float a, float b) {
+    top = max(top, max(__float_as_uint(a), __float_as_uint(b)));
+    low = min(low, min(__float_as_uint(a), __float_as_uint(b)));
   }
-  // Whether a product of a row's and a column's scale, of all lanes, may not be a normal FP32 number.
-  // None if every scale is in [2^-63, 2^63].
+  // of all lanes; also true for a scale of 0
   __device__ __forceinline__ bool wide() const {
-    constexpr uint32_t kTop = (127u + 63u) << 23, kLow = ((127u - 63u) << 23) - 1u;
-    if (__ballot(max(top_r, top_c) > kTop || min(low_r, low_c) < kLow) == 0) return false;
-    uint32_t tr = top_r, lr = low_r, tc = top_c, lc = low_c;
-#pragma unroll 1
-    for (int m = 32; m >= 1; m >>= 1) {
-      tr = max(tr, static_cast<uint32_t>(__shfl_xor(static_cast<int>(tr), m)));
-      lr = min(lr, static_cast<uint32_t>(__shfl_xor(static_cast<int>(lr), m)));
-      tc = max(tc, static_cast<uint32_t>(__shfl_xor(static_cast<int>(tc), m)));
-      lc = min(lc, static_cast<uint32_t>(__shfl_xor(static_cast<int>(lc), m)));
-    }
-    if (lr == ~0u || lc == ~0u) return false;  // all zeros
-    // the largest below 2^(e + 1), e the sum of two exponents; the smallest at least 2^e (subnormal: 2^-149)
-    auto exponent = [](uint32_t bits) { return static_cast<int>(bits >> 23) - 127; };
-    auto least = [&](uint32_t less_one) { return less_one < 0x7fffffu ? -149 : exponent(less_one + 1u); };
-    return __builtin_amdgcn_readfirstlane(exponent(tr) + exponent(tc) > 125 || least(lr) + least(lc) < -126) != 0;
+    return __ballot(top > ((127u + 63u) << 23) || low < ((127u - 63u) << 23)) != 0;
   }
 };
+
+// Whether a product of one of kRows rows' scales and one of 64 columns' may not be a normal FP32 number, zeros
+// aside: from the exponents of the largest and of the smallest of either, over all of an expert's tiles.
+// For tiles with a scale of 0 or outside ScaleRange, of which it costs a tenth.
+template <int kRows>
+__device__ __forceinline__ bool wide_products(const float *sa, const float *sb, int64_t P, int64_t Q, int first, int tiles,
+                                              int64_t row, int64_t col) {
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));  // keeps the addresses from being formed long before
+  sa += static_cast<int64_t>(first) * P + row + (lane & (kRows - 1));
+  sb += static_cast<int64_t>(first) * Q + col + lane;
+  uint32_t tr = 0u, lr = ~0u, tc = 0u, lc = ~0u;  // the smallest ones less one: 0 wraps round past all others
+#pragma unroll 4
+  for (int t = 0; t < tiles; ++t, sa += P, sb += Q) {
+    const uint32_t r = __float_as_uint(*sa), c = __float_as_uint(*sb);
+    tr = max(tr, r);
+    lr = min(lr, r - 1u);
+    tc = max(tc, c);
+    lc = min(lc, c - 1u);
+  }
+#pragma unroll 1
+  for (int m = 32; m >= 1; m >>= 1) {
+    tr = max(tr, static_cast<uint32_t>(__shfl_xor(static_cast<int>(tr), m)));
+    lr = min(lr, static_cast<uint32_t>(__shfl_xor(static_cast<int>(lr), m)));
+    tc = max(tc, static_cast<uint32_t>(__shfl_xor(static_cast<int>(tc), m)));
+    lc = min(lc, static_cast<uint32_t>(__shfl_xor(static_cast<int>(lc), m)));
+  }
+  if (lr == ~0u || lc == ~0u) return false;  // all zeros
+  // the largest is below 2^(e + 1), e the sum of two exponents, the smallest at least 2^e (subnormal: 2^-149)
+  auto exponent = [](uint32_t bits) { return static_cast<int>(bits >> 23) - 127; };
+  auto least = [&](uint32_t less_one) { return less_one < 0x7fffffu ? -149 : exponent(less_one + 1u); };
+  return __builtin_amdgcn_readfirstlane(exponent(tr) + exponent(tc) > 125 || least(lr) + least(lc) < -126) != 0;
+}
 
 // Rows row .. row + 31 and columns col, col + 2 .. col + 62 of an expert's gradient, laid out as the wave's
 // blocks, without the product of the scales: the smaller one multiplies a tile's sum, the larger
 // one the result, so that nothing overflows that the term does not, and what underflows is below
-// 2^-149 times the larger scale.  For scales that ScaleRange finds wide, which ordinary tensors do
+// 2^-149 times the larger scale.  For scales that wide_products finds, which ordinary tensors do
 // not have: straight from memory, two to nine times slower.
 template <bool kOutF32>
 __device__ __forceinline__ void wide_range_block(const uint8_t *aq, const float *sa, const uint8_t *bq, const float *sb,
@@ -340,7 +357,7 @@ __device__ __forceinline__ void wgrad_run(const uint8_t *__restrict__ aq, const 
   int j = 0, s = 0;          // the stage being multiplied
   bool ahead = false;        // the next stage's copies are issued already
   int stores = 0;            // 2: a tile ended a stage ago; 1: two stages ago
-  uint32_t redo = 0;         // the run's tiles (at most 4) whose scales' products FP32 does not hold
+  uint32_t redo = 0;         // the run's tiles (at most 4) with scales outside the range, or of 0
   auto stage = [&](auto parity) {
     constexpr int kCur = decltype(parity)::value * kStage;  // the stage's place in LDS
     FP8Q_LDS uint8_t *cur = st + kCur, *next = st + (kStage - kCur);
@@ -423,10 +440,11 @@ __device__ __forceinline__ void wgrad_run(const uint8_t *__restrict__ aq, const 
   if (redo == 0) return;
   wait_loads<0>();  // the tiles' first stores
   for (j = 0; j < count; ++j) {
-    if ((redo >> j & 1u) == 0) continue;
+    const int64_t row = p0 + wm * 32, col = q0 + j * kTile + wn * 64;
+    if ((redo >> j & 1u) == 0 || !wide_products<32>(sa, sb, P, Q, first, tiles, row, col)) continue;
 #pragma unroll
     for (int n = 0; n < 2; ++n)
-      wide_range_block<kOutF32>(aq, sa, bq, sb, P, Q, first, tiles, p0 + wm * 32, q0 + j * kTile + wn * 64 + n, acc[n]);
+      wide_range_block<kOutF32>(aq, sa, bq, sb, P, Q, first, tiles, row, col + n, acc[n]);
     store(j);
   }
 }
@@ -663,7 +681,7 @@ __device__ __forceinline__ void wgrad_wide_run(const uint8_t *__restrict__ aq, c
             widen(step + 1, k);
             pinned(wide[(step + 1) & 1][k]);
             if (k == 0) copy(step);
-            if (step == 0 && k == 1) range.see(sr, sc.x, sc.y);
+            if (step == 0 && k == 1) range.see(sr, half ? sc.y : sc.x);
             pin();
           }
         }
@@ -686,7 +704,6 @@ __device__ __forceinline__ void wgrad_wide_run(const uint8_t *__restrict__ aq, c
       multiply(0, 0, 1, part[0][0]);
       copy(2);
       copy(3);
-      range.see(sr, sc.x, sc.y);
       pin();
       multiply(0, 1, 0, zero);
       copy(4);
@@ -705,6 +722,7 @@ __device__ __forceinline__ void wgrad_wide_run(const uint8_t *__restrict__ aq, c
       add(0, scale[1], 8, 20);
       pin();
       multiply(1, 1, 1, part[1][1]);
+      range.see(sr, half ? sc.y : sc.x);
       add(0, scale[1], 20, 32);
       pin();
       scale[1] = scales(sr, sc.y);
@@ -717,11 +735,11 @@ __device__ __forceinline__ void wgrad_wide_run(const uint8_t *__restrict__ aq, c
   wait_loads<0>();
   if (kOutF32) add(0, scale[0], 0, 32);
   add(1, scale[1], 0, 32);
-  if (mine && range.wide()) {
+  const int64_t row = p0 + wm * 64, col = q0 + wn * 64;
+  if (mine && range.wide() && wide_products<64>(sa, sb, P, Q, first, tiles, row, col)) {
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      wide_range_block<kOutF32>(aq, sa, bq, sb, P, Q, first, tiles, p0 + wm * 64 + 32 * (k >> 1), q0 + wn * 64 + (k & 1),
-                                acc[k >> 1][k & 1]);
+      wide_range_block<kOutF32>(aq, sa, bq, sb, P, Q, first, tiles, row + 32 * (k >> 1), col + (k & 1), acc[k >> 1][k & 1]);
   }
   store();
 }

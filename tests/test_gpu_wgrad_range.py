@@ -77,3 +77,20 @@ def test_scales_of_any_size(counts, P, Q, out_dtype):
         assert bool(torch.isinf(out[over]).all())
         err = (out - ref).abs()[~over] - tol[~over]
         assert bool((err <= 0).all()), f"expert {g}: {int((err > 0).sum())} of {err.numel()} out of tolerance"
+
+
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("counts,P,Q", SIZES)
+def test_scales_far_from_one_with_ordinary_products(counts, P, Q, out_dtype):
+    """One operand 2^70 times larger, the other as much smaller, and channels of zeros: the products of the
+    scales are what they were, and so is every bit of the gradient."""
+    G, M = len(counts), sum(counts)
+    off = dev(np.concatenate([[0], np.cumsum(counts)]).astype(np.int32))
+    tiles = M // 128 + G
+    (a, sa), (b, sb) = operand(tiles, P, 3), operand(tiles, Q, 4)
+    for q, s, at in ((a, sa, P // 3), (b, sb, Q // 2)):
+        q[:, at], s[:, at] = 0, 0
+        q[0, at + 1], s[0, at + 1] = 0, 0
+    got = [fq.fp8q_grouped_gemm_rowscaled(a, sa * x, b, sb / x, off, M, out_dtype=out_dtype) for x in (1.0, 2.0 ** 70, 2.0 ** -75)]
+    assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
+    assert not bool(got[0][:, P // 3].any()) and not bool(got[0][:, :, Q // 2].any())
