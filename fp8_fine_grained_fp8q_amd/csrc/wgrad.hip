@@ -411,8 +411,9 @@ __device__ __forceinline__ void wgrad_run(const uint8_t *__restrict__ aq, const 
     }
     float sr, sc;
     read_scales<kCur>(sr, sc, at_sr, at_sc);
-    range.see(sr, sc);
     const v32f scale = __builtin_amdgcn_mfma_f32_32x32x1f32(sr, sc, v32f{}, 0, 0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    range.see(sr, sc);
 #pragma unroll
     for (int n = 0; n < 2; ++n)
 #pragma unroll
