@@ -374,8 +374,8 @@ __global__ __launch_bounds__(256) void moe_sum_kernel(const void *__restrict__ d
 // kernel and the copy would be two).  Every workgroup holds all local expert indices in LDS and
 // finds its token's rows by counting, row = the entries of an earlier expert, or of the same
 // one and earlier in order: one ballot per 64 entries and slot.  The last workgroup counts the
-// offsets.  64 tokens x 8 slots x 7168 BF16 columns: 14.3 -> 11.6 us a call
-// from Python, of which the kernel is 6.1.
+// offsets.  64 tokens x 8 slots x 7168 BF16 columns: 2.7 us less a call than by two launches; the
+// kernel takes 6.0.
 constexpr int kSmallSort = 2 * static_cast<int>(kChunk) - 1;
 
 __global__ __launch_bounds__(256) void moe_sort_small_kernel(const int32_t *__restrict__ ids, int n, int k,

@@ -1,5 +1,5 @@
 // Weight gradients of MoE experts in E4M3, dW[g] = dY[g]^T X[g] for every local expert in one
-// launch, for gfx950 (the pages' unified E4M3 format in the backward pass; see the dense
+// call, for gfx950 (the pages' unified E4M3 format in the backward pass; see the dense
 // weight-gradient product in gemm.hip).
 //
 //   C[g][p][q] = sum over expert g's token tiles b of
@@ -20,13 +20,13 @@
 // output widens the codes to BF16, exactly, and takes the BF16 instructions (8e-9), at half
 // their rate.
 //
-// Two regimes, measured on one MI355X (product alone, behind its quantizers):
+// Two regimes, measured on one MI355X (product alone):
 //  * few tokens per expert: the gradient's bytes.  32 experts of 4096 x 7168 over 8192 rows: FP32
-//    840-870 us (4.4 TB/s of 3.76 GB), BF16 510 us.  Stores alone take 650 and 366 us, loads and
+//    850-870 us (4.4 TB/s of 3.76 GB), BF16 500-515 us.  Stores alone take 650 and 366 us, loads and
 //    products alone about 700 and 450; the two overlap only in part.
 //  * many: the matrix cores and the instructions around theirs.  4 experts of 7168 x 2048 over 16384
-//    rows: BF16 250 us (1.9 PFLOP/s), FP32 447 us (1.1) by the wide kernel below; 300 and 505 us by the
-//    small tiles.
+//    rows: BF16 245-250 us (1.9 PFLOP/s), FP32 435-450 us (1.1) by the wide kernel below; 289 and 483 us
+//    by the small tiles.
 //
 // The kernel for few tokens: a workgroup of 8 waves computes 128 x 128 tiles of one expert, 32 x 64
 // per wave in 32x32 blocks, two workgroups per CU, so that one's loads and stores run beside the
@@ -243,7 +243,8 @@ __device__ __forceinline__ int routed_rows(const int32_t *offsets, int G, int64_
 // round-robin to the 8 XCDs, and a grid of several units per workgroup is a multiple of 8.  Each XCD gets a contiguous eighth of every expert's runs, four rows
 // of tiles at a time, column by column: neighbouring workgroups share operands in their L2 and
 // write neighbouring parts of the same rows, and experts of different sizes load all XCDs alike
-// (whole experts per XCD: 4 uneven experts over 16384 rows 350 us instead of 314 us).
+// (whole experts per XCD: 8 uneven experts of 7168 x 2048 over 16384 rows FP32 548 us instead of 496,
+// BF16 294 instead of 277).
 __device__ __forceinline__ bool place(uint32_t unit, int tp, int runs, int &g, int &p, int &r) {
   const int per = (tp * runs + 7) / 8;
   const int xcd = static_cast<int>(unit % 8), idx = static_cast<int>(unit / 8);
@@ -472,13 +473,14 @@ __global__ __launch_bounds__(64 * kWaves, 4) void wgrad_kernel(
 // while the other scales and adds its last one and reads the next from LDS.  Against the 128 x 128
 // tiles a quarter less is copied, and a third less read from LDS and widened per product.
 //
-// 4 experts of 7168 x 2048 over 16384 rows: BF16 300 -> 250 us, FP32 505 -> 447 us.  BF16: a token
-// tile takes 0.71 us on codes of zeros, of which the matrix core works 0.53, and 1.0 us on random
-// ones, where power limits the clock; a tile's start and end 4 us.  FP32 (385 us on zeros) is bound
-// by the issue of the widening: 315 us without the products, 307 without the widening.  Three
-// things it needed: no branch and no address arithmetic between the barriers (310 us with them),
-// the copies behind the matrix instructions and not behind the reads, and no instruction that waits
-// for a matrix result right before another matrix instruction (265 -> 250 us).
+// 4 experts of 7168 x 2048 over 16384 rows: BF16 289 -> 242 us, FP32 483 -> 432 us.  BF16 takes 456
+// to 467 thousand cycles.  The matrix cores work in 62 to 64 % of them; the vector instructions, 79 per wave and token
+// tile and 64 of them the promotion, issue once per 8 cycles beside FP8 products and fill up to 80 %;
+// a tile's start and end are 4 us of 36.  On codes of zeros it takes 196 us: the clock is higher then.  FP32 is bound by the issue
+// of the widening: 315 us without the products, 307 without the widening.  Three things it needed: no
+// branch and no address arithmetic between the barriers (BF16 310 us with them), the copies behind the
+// matrix instructions and not behind the reads, and no instruction that waits for a matrix result
+// right before another matrix instruction (265 -> 250 us).
 // ---------------------------------------------------------------------------------------
 constexpr int kWideRows = 256;
 constexpr int kWideScaleAt = kWideRows * 128 + kPanel;  // then the rows' scales and the columns'
@@ -769,11 +771,11 @@ hipError_t launch_grouped_gemm_rowscaled(const uint8_t *aq, const float *sa, con
                                          void *c, bool out_f32, hipStream_t stream) {
   const int64_t cus = device_cu_count(), tp = P / kTile, tq = Q / kTile, tile = kTile * G;
   // Wide tiles for experts of 8 token tiles or more on average, with FP32 output 12, if that makes one for
-  // every CU.  4 experts of 7168 x 2048 with 4, 8 and 12 token tiles, BF16: 59, 88 and 111 us by wide tiles,
-  // 56, 97 and 130 by the others; 32 of 4096 x 7168 with 8 and 12, FP32: 2349 and 3090 us, 2197
-  // and 3054; 4 of 7168 x 2048 with 12, FP32: 204 and 212.  One expert of 2048 x 2048, half as many wide
-  // tiles as CUs, BF16: 20 and 19.  P = 128 would leave half of each wide tile empty (16 experts
-  // of 128 x 8192 with 32 token tiles, BF16, 160 and 107 us).
+  // every CU.  4 experts of 7168 x 2048 with 4, 8 and 12 token tiles, BF16: 60, 88 and 113 us by wide tiles,
+  // 57, 92 and 125 by the others; with 12, FP32: 194 and 200; 32 of 4096 x 7168 with 8 and 12, FP32: 2380
+  // and 3210 us, 2195 and 3125.  One expert of 2048 x 2048, half as many wide tiles as CUs, with 32:
+  // BF16 29 and 30, FP32 53 and 46.  P = 128 would leave half of each wide tile empty (16 experts of
+  // 128 x 8192 with 32 token tiles, BF16, 166 and 111 us).
   // M only bounds the rows, and how many are routed is known on the device: the value sort's default
   // capacity has room for every expert to be local.  So where M allows wide tiles both kernels are
   // launched, and the one that the offsets do not call for leaves at once (about 5 us).  8192 tokens x 8

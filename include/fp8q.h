@@ -274,8 +274,8 @@ fp8q_status fp8q_quantize_per_tensor(const uint16_t *x_bf16, int64_t n, const fl
  *   token_row  : [T][k] out: the row of (t, s), or -1 if its expert is not local
  *   row_token  : [capacity] out: the token of each row < offsets[E]
  * Requires K % 128 == 0, 1 <= E <= 1024; with T == 0 only `offsets` is written (zeros).
- * Up to four launches (count, scan and rank over chunks of 1024 entries, then the copy);
- * token_row serves as the count pass's scratch.  Errors: FP8Q_ERR_SHAPE, FP8Q_ERR_NULL, FP8Q_ERR_ALIGN (index arrays 4-byte, the
+ * Two launches (rank, then the copy) for up to 17407 entries T*k, four beyond (count, scan and rank over
+ * chunks of 1024 entries, then the copy); token_row serves as the count pass's scratch.  Errors: FP8Q_ERR_SHAPE, FP8Q_ERR_NULL, FP8Q_ERR_ALIGN (index arrays 4-byte, the
  * rest 16-byte), FP8Q_ERR_DEVICE, FP8Q_ERR_LAUNCH.
  */
 fp8q_status fp8q_moe_dispatch(const int32_t *topk_ids, int64_t T, int64_t k, int64_t e_begin, int64_t E,
@@ -391,7 +391,8 @@ fp8q_status fp8q_quantize_act_grouped(const uint16_t *x_bf16, const int32_t *off
                                       int64_t K, uint8_t *xq, float *sa, uint8_t *xqt, float *sat, void *stream);
 
 /*
- * The experts' weight gradients dW[g] = dY[g]^T X[g], every expert in one launch:
+ * The experts' weight gradients dW[g] = dY[g]^T X[g], every expert in one call (one launch, or two of which
+ * one leaves at once: which depends on the rows that `offsets` routes, not on M_tot alone):
  *   C[g][p][q] = sum over expert g's token tiles b of
  *                sa[b][p] * sb[b][q] * sum_i decode(aq[b][p][i]) decode(bq[b][q][i])
  * with FP32 promotion at every tile of 128 tokens, tiles ascending: the scales' product is
