@@ -28,6 +28,12 @@ Training step of an MoE layer (the forward pass with values beside the codes, an
     plan = fp8q_adamw_plan(params, grads, m, v)                  # states in FP32 or in E4M3
     fp8q_adamw(plan, lr=2e-4, step=1)
 
+Around the experts:
+    y, mean, rstd = fp8q_layer_norm(x, weight, bias)             # center=False: RMS norm
+    dx, dweight, dbias = fp8q_layer_norm_backward(dy, x, weight, mean, rstd, want_bias=True)
+    topk_ids, topk_w, counts, loss, slope = fp8q_moe_route(logits, k, bias, balance=1e-4)
+    dlogits = fp8q_moe_route_backward(logits, topk_ids, topk_w, dw, slope, dloss)
+
 Layouts: xq uint8 [M, K]; sa float32 [K/128, M]; wq uint8 [G, N, K]; sb float32
 [G, N/128, K/128]; C row-major [M, N].
 """
@@ -48,15 +54,18 @@ FP8Q_OUT_BF16 = 0
 FP8Q_OUT_F32 = 1
 FP8Q_STATE_F32 = 0
 FP8Q_STATE_E4M3 = 1
-ABI_VERSION = 8
+FP8Q_SCORE_SOFTMAX = 0
+FP8Q_SCORE_SIGMOID = 1
+ABI_VERSION = 9
 
 EXPORTED = ("fp8q_quantize_act_1x128", "fp8q_quantize_w_128x128", "fp8q_gemm_blockscaled",
             "fp8q_grouped_gemm_blockscaled", "fp8q_quantize_w_128x128_t", "fp8q_quantize_act_dual",
             "fp8q_gemm_rowscaled", "fp8q_swiglu_quantize_act_1x128", "fp8q_quantize_per_tensor",
             "fp8q_quantize_act_w", "fp8q_moe_dispatch", "fp8q_moe_combine", "fp8q_moe_sort",
             "fp8q_moe_sort_backward", "fp8q_moe_combine_backward", "fp8q_swiglu_backward",
-            "fp8q_quantize_act_grouped", "fp8q_grouped_gemm_rowscaled", "fp8q_adamw", "fp8q_status_string",
-            "fp8q_abi_version")
+            "fp8q_quantize_act_grouped", "fp8q_grouped_gemm_rowscaled", "fp8q_adamw", "fp8q_layer_norm",
+            "fp8q_layer_norm_backward", "fp8q_layer_norm_backward_workspace", "fp8q_moe_route",
+            "fp8q_moe_route_workspace", "fp8q_moe_route_backward", "fp8q_status_string", "fp8q_abi_version")
 
 
 class Fp8qError(RuntimeError):
@@ -109,8 +118,15 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.fp8q_quantize_act_grouped.argtypes = [vp, vp, i64, i64, i64, vp, vp, vp, vp, vp]
     lib.fp8q_grouped_gemm_rowscaled.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i64, vp, i32, vp]
     lib.fp8q_adamw.argtypes = [ctypes.POINTER(_AdamwTensor), i64, i32, i32, ctypes.POINTER(_AdamwHyper), vp]
+    f64 = ctypes.c_double
+    lib.fp8q_layer_norm.argtypes = [vp, i32, vp, vp, i64, i64, f64, i32, vp, i32, vp, vp, vp]
+    lib.fp8q_layer_norm_backward.argtypes = [vp, i32, vp, i32, vp, vp, vp, i64, i64, vp, i32, vp, vp, vp, vp]
+    lib.fp8q_layer_norm_backward_workspace.argtypes = [i64, i64]
+    lib.fp8q_moe_route.argtypes = [vp, i32, i64, i64, i64, i64, vp, vp, i32, i32, f64, f64, vp, vp, vp, vp, vp, vp, vp]
+    lib.fp8q_moe_route_workspace.argtypes = [i64, i64, i64]
+    lib.fp8q_moe_route_backward.argtypes = [vp, i32, i64, i64, i64, i64, vp, vp, vp, vp, vp, i32, i32, f64, vp, i32, vp]
     for name in EXPORTED:
-        getattr(lib, name).restype = i32
+        getattr(lib, name).restype = i64 if name.endswith("_workspace") else i32
     lib.fp8q_status_string.argtypes = [i32]
     lib.fp8q_status_string.restype = ctypes.c_char_p
     lib.fp8q_abi_version.argtypes = []
@@ -714,6 +730,149 @@ def fp8q_adamw(plan: AdamwPlan, lr: float, betas=(0.9, 0.95), eps: float = 1e-8,
                                      ctypes.byref(hyper), s), "fp8q_adamw")
 
 
+def _workspace(size, like: torch.Tensor):
+    """`size` bytes (or a status) of scratch memory on `like`'s device, of the current stream's allocator."""
+    if size < 0:
+        raise Fp8qError(int(size), "workspace")
+    return like.new_empty(size, dtype=torch.uint8)
+
+
+def fp8q_layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None, eps: float = 1e-5,
+                    center: bool = True, out_dtype=None, y: torch.Tensor | None = None, stream=None):
+    """Layer norm, or RMS norm with center=False, of every row: x bf16 or float32 [T, H], weight and bias
+    float32 [H] -> (y [T, H] in out_dtype (x's by default), mean float32 [T] or None, rstd float32 [T])."""
+    if stream is not None:
+        with _on(stream):
+            return fp8q_layer_norm(x, weight, bias, eps, center, out_dtype, y)
+    _need_rows(x, "x")
+    T, H = x.shape
+    _need(weight, torch.float32, "weight", (H,))
+    if bias is not None:
+        _need(bias, torch.float32, "bias", (H,))
+    s = _here(x, weight, bias, y)
+    y = _out(y, (out_dtype or x.dtype) if y is None else y.dtype, "y", x.shape, x)
+    mean = weight.new_empty(T) if center else None
+    rstd = weight.new_empty(T)
+    _check(load_library().fp8q_layer_norm(_ptr(x), _out_code(x.dtype), _ptr(weight), _ptr(bias), T, H, eps, bool(center),
+                                          _ptr(y), _out_code(y.dtype), _ptr(mean), _ptr(rstd), s), "fp8q_layer_norm")
+    return y, mean, rstd
+
+
+def fp8q_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, mean: torch.Tensor | None,
+                             rstd: torch.Tensor, want_bias: bool = False, out_dtype=None, dx: torch.Tensor | None = None,
+                             stream=None):
+    """Gradients of fp8q_layer_norm (mean None: RMS norm): dy and x bf16 or float32 [T, H] each, weight [H],
+    mean and rstd [T] float32 -> (dx [T, H] in out_dtype (x's by default), dweight float32 [H], dbias float32
+    [H] with want_bias, else None)."""
+    if stream is not None:
+        with _on(stream):
+            return fp8q_layer_norm_backward(dy, x, weight, mean, rstd, want_bias, out_dtype, dx)
+    _need_rows(x, "x")
+    T, H = x.shape
+    _need_rows(dy, "dy", rows=T)
+    if dy.shape[1] != H:
+        raise ValueError(f"dy must be [{T}, {H}], got {tuple(dy.shape)}")
+    _need(weight, torch.float32, "weight", (H,))
+    if mean is not None:
+        _need(mean, torch.float32, "mean", (T,))
+    _need(rstd, torch.float32, "rstd", (T,))
+    s = _here(dy, x, weight, mean, rstd, dx)
+    lib = load_library()
+    dx = _out(dx, (out_dtype or x.dtype) if dx is None else dx.dtype, "dx", x.shape, x)
+    dweight = torch.empty_like(weight)
+    dbias = torch.empty_like(weight) if want_bias else None
+    work = _workspace(lib.fp8q_layer_norm_backward_workspace(T, H), x)
+    _check(lib.fp8q_layer_norm_backward(_ptr(dy), _out_code(dy.dtype), _ptr(x), _out_code(x.dtype), _ptr(weight),
+                                        _ptr(mean), _ptr(rstd), T, H, _ptr(dx), _out_code(dx.dtype), _ptr(dweight),
+                                        _ptr(dbias), _ptr(work), s), "fp8q_layer_norm_backward")
+    return dx, dweight, dbias
+
+
+_SCORES = {"softmax": FP8Q_SCORE_SOFTMAX, "sigmoid": FP8Q_SCORE_SIGMOID}
+
+
+def _logits_shape(logits):
+    """(B, S, E) of the router's logits [S, E] or [B, S, E]."""
+    if not isinstance(logits, torch.Tensor) or (logits.dtype != torch.bfloat16 and logits.dtype != torch.float32):
+        raise ValueError("logits must be a bfloat16 or float32 tensor")
+    if not logits.is_cuda or not logits.is_contiguous() or logits.dim() not in (2, 3):
+        raise ValueError("logits must be a contiguous CUDA tensor [S, E] or [B, S, E]")
+    return (1, *logits.shape) if logits.dim() == 2 else tuple(logits.shape)
+
+
+def _score_code(score):
+    if score not in _SCORES:
+        raise ValueError(f"score must be 'softmax' or 'sigmoid', got {score!r}")
+    return _SCORES[score]
+
+
+def fp8q_moe_route(logits: torch.Tensor, k: int, bias: torch.Tensor | None = None, valid: torch.Tensor | None = None,
+                   score: str = "softmax", normalize: bool = True, scale: float = 1.0, balance: float = 0.0, stream=None):
+    """Top-k experts of every token: logits bf16 or float32 [S, E], or [B, S, E] of B sequences -> (topk_ids int32
+    [.., S, k], topk_weights float32 [.., S, k], counts int32 [.., E], loss float32 [1], slope float32
+    [.., E]).  Chosen by score + bias (float32 [E]); weights scale * score, normalized over the chosen ones;
+    loss = balance * the mean over the sequences of E sum_e (share of the slots)_e (mean of p_e), slope its
+    derivative by each p.  Tokens with valid (bool [.., S]) False get ids -1 and weights 0 and do not count."""
+    if stream is not None:
+        with _on(stream):
+            return fp8q_moe_route(logits, k, bias, valid, score, normalize, scale, balance)
+    B, S, E = _logits_shape(logits)
+    lead = logits.shape[:-1]
+    if bias is not None:
+        _need(bias, torch.float32, "bias", (E,))
+    if valid is not None:
+        _need(valid, torch.bool, "valid", lead)
+    code = _score_code(score)
+    s = _here(logits, bias, valid)
+    lib = load_library()
+    work = _workspace(lib.fp8q_moe_route_workspace(B, S, E), logits)
+    if not 1 <= k <= min(E, 64):
+        raise ValueError(f"k must be between 1 and min(E, 64), got {k}")
+    ids = logits.new_empty(*lead, k, dtype=torch.int32)
+    w = logits.new_empty(*lead, k, dtype=torch.float32)
+    counts = logits.new_empty(*lead[:-1], E, dtype=torch.int32)
+    slope = logits.new_empty(*lead[:-1], E, dtype=torch.float32)
+    loss = logits.new_empty(1, dtype=torch.float32)
+    _check(lib.fp8q_moe_route(_ptr(logits), _out_code(logits.dtype), B, S, E, k, _ptr(bias), _ptr(valid), code,
+                              bool(normalize), scale, balance, _ptr(ids), _ptr(w), _ptr(counts), _ptr(loss), _ptr(slope),
+                              _ptr(work), s), "fp8q_moe_route")
+    return ids, w, counts, loss, slope
+
+
+def fp8q_moe_route_backward(logits: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor, dw: torch.Tensor,
+                            slope: torch.Tensor, dloss: torch.Tensor | None = None, score: str = "softmax",
+                            normalize: bool = True, scale: float = 1.0, out_dtype=None,
+                            dlogits: torch.Tensor | None = None, stream=None):
+    """Gradient of fp8q_moe_route by the logits, from dw float32 like topk_w and dloss float32 [1] (None: 1);
+    topk_ids, topk_w and slope as fp8q_moe_route gave them, score, normalize and scale as it got them ->
+    dlogits like logits, in out_dtype (logits' by default).  Zeros for tokens with ids -1."""
+    if stream is not None:
+        with _on(stream):
+            return fp8q_moe_route_backward(logits, topk_ids, topk_w, dw, slope, dloss, score, normalize, scale, out_dtype,
+                                           dlogits)
+    B, S, E = _logits_shape(logits)
+    lead = logits.shape[:-1]
+    if not isinstance(topk_ids, torch.Tensor) or topk_ids.dim() != logits.dim():
+        raise ValueError("topk_ids must be [.., S, k] like the logits")
+    k = topk_ids.shape[-1]
+    _need(topk_ids, torch.int32, "topk_ids", (*lead, k))
+    _need(topk_w, torch.float32, "topk_w", (*lead, k))
+    _need(dw, torch.float32, "dw", (*lead, k))
+    _need(slope, torch.float32, "slope", (*lead[:-1], E))
+    if dloss is not None:
+        _need(dloss, torch.float32, "dloss")
+        if dloss.numel() != 1:
+            raise ValueError("dloss must hold one float32")
+    code = _score_code(score)
+    s = _here(logits, topk_ids, topk_w, dw, slope, dloss, dlogits)
+    dlogits = _out(dlogits, (out_dtype or logits.dtype) if dlogits is None else dlogits.dtype, "dlogits", logits.shape,
+                   logits)
+    _check(load_library().fp8q_moe_route_backward(
+        _ptr(logits), _out_code(logits.dtype), B, S, E, k, _ptr(topk_ids), _ptr(topk_w), _ptr(dw), _ptr(slope),
+        _ptr(dloss), code, bool(normalize), scale, _ptr(dlogits), _out_code(dlogits.dtype), s), "fp8q_moe_route_backward")
+    return dlogits
+
+
 quantize_act_1x128 = fp8q_quantize_act_1x128
 quantize_w_128x128 = fp8q_quantize_w_128x128
 gemm_blockscaled = fp8q_gemm_blockscaled
@@ -731,3 +890,7 @@ quantize_act_grouped = fp8q_quantize_act_grouped
 grouped_gemm_rowscaled = fp8q_grouped_gemm_rowscaled
 adamw_plan = fp8q_adamw_plan
 adamw = fp8q_adamw
+layer_norm = fp8q_layer_norm
+layer_norm_backward = fp8q_layer_norm_backward
+moe_route = fp8q_moe_route
+moe_route_backward = fp8q_moe_route_backward

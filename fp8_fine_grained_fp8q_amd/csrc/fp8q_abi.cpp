@@ -50,6 +50,12 @@ bool bad_rows(int64_t T, int64_t k, int64_t capacity, int64_t width) {
          T * k >= kMaxDim || too_many(capacity, width) || too_many(T, width);
 }
 
+// Shared checks of the router's logits [B][S][E] and of k.
+bool bad_route(int64_t B, int64_t S, int64_t E, int64_t k) {
+  return B < 1 || B > fp8q::kMaxSequences || bad_dim(S) || E < 1 || E > 1024 || k < 1 || k > fp8q::kMaxTopK || k > E ||
+         B * S * k >= kMaxDim;
+}
+
 // Shared checks of the two GEMM entry points (everything except the grouped extras).
 fp8q_status check_gemm(const uint8_t *xq, const float *sa, const uint8_t *wq, const float *sb,
                        int64_t M, int64_t N, int64_t K, void *c, int32_t out_dtype) {
@@ -370,6 +376,86 @@ fp8q_status fp8q_adamw(const fp8q_adamw_tensor *tensors, int64_t count, int32_t 
   return launched(fp8q::launch_adamw(tensors, count, grad_dtype == FP8Q_OUT_F32, e4m3, h, as_stream(stream)));
 }
 
+fp8q_status fp8q_layer_norm(const void *x, int32_t x_dtype, const float *weight, const float *bias, int64_t T, int64_t H,
+                            double eps, int32_t center, void *y, int32_t out_dtype, float *mean, float *rstd,
+                            void *stream) {
+  if (bad_dtype(x_dtype) || bad_dtype(out_dtype)) return FP8Q_ERR_DTYPE;
+  if (bad_dim(T) || H < 8 || H % 8 != 0 || H > fp8q::kMaxNormWidth) return FP8Q_ERR_SHAPE;
+  if (!f32_number(eps) || eps < 0) return FP8Q_ERR_VALUE;
+  if (T == 0) return FP8Q_OK;
+  if (!x || !weight || !y || !rstd || (center && !mean)) return FP8Q_ERR_NULL;
+  if (misaligned(x) || misaligned(weight) || misaligned(bias) || misaligned(y) || misaligned(mean, 4) ||
+      misaligned(rstd, 4))
+    return FP8Q_ERR_ALIGN;
+  if (device_ok() != FP8Q_OK) return FP8Q_ERR_DEVICE;
+  return launched(fp8q::launch_layer_norm(x, x_dtype == FP8Q_OUT_F32, weight, bias, T, H, static_cast<float>(eps),
+                                          center != 0, y, out_dtype == FP8Q_OUT_F32, mean, rstd, as_stream(stream)));
+}
+
+int64_t fp8q_layer_norm_backward_workspace(int64_t T, int64_t H) {
+  if (bad_dim(T) || H < 8 || H % 8 != 0 || H > fp8q::kMaxNormWidth) return FP8Q_ERR_SHAPE;
+  return 8 * H * fp8q::norm_backward_groups(T);
+}
+
+fp8q_status fp8q_layer_norm_backward(const void *dy, int32_t dy_dtype, const void *x, int32_t x_dtype,
+                                     const float *weight, const float *mean, const float *rstd, int64_t T, int64_t H,
+                                     void *dx, int32_t out_dtype, float *dweight, float *dbias, void *workspace,
+                                     void *stream) {
+  if (bad_dtype(dy_dtype) || bad_dtype(x_dtype) || bad_dtype(out_dtype)) return FP8Q_ERR_DTYPE;
+  if (bad_dim(T) || H < 8 || H % 8 != 0 || H > fp8q::kMaxNormWidth) return FP8Q_ERR_SHAPE;
+  if (!dweight || (T > 0 && (!dy || !x || !weight || !rstd || !dx || !workspace))) return FP8Q_ERR_NULL;
+  if (misaligned(dy) || misaligned(x) || misaligned(weight) || misaligned(mean, 4) || misaligned(rstd, 4) ||
+      misaligned(dx) || misaligned(dweight, 4) || misaligned(dbias, 4) || misaligned(workspace))
+    return FP8Q_ERR_ALIGN;
+  if (device_ok() != FP8Q_OK) return FP8Q_ERR_DEVICE;
+  return launched(fp8q::launch_layer_norm_backward(dy, dy_dtype == FP8Q_OUT_F32, x, x_dtype == FP8Q_OUT_F32, weight, mean,
+                                                   rstd, T, H, dx, out_dtype == FP8Q_OUT_F32, dweight, dbias,
+                                                   static_cast<float *>(workspace), as_stream(stream)));
+}
+
+int64_t fp8q_moe_route_workspace(int64_t B, int64_t S, int64_t E) {
+  if (bad_route(B, S, E, 1)) return FP8Q_ERR_SHAPE;
+  return fp8q::moe_route_workspace(B, S, E);
+}
+
+fp8q_status fp8q_moe_route(const void *logits, int32_t dtype, int64_t B, int64_t S, int64_t E, int64_t k,
+                           const float *bias, const uint8_t *valid, int32_t score, int32_t normalize, double scale,
+                           double balance, int32_t *topk_ids, float *topk_weights, int32_t *counts, float *loss,
+                           float *slope, void *workspace, void *stream) {
+  if (bad_dtype(dtype) || (score != FP8Q_SCORE_SOFTMAX && score != FP8Q_SCORE_SIGMOID)) return FP8Q_ERR_DTYPE;
+  if (bad_route(B, S, E, k)) return FP8Q_ERR_SHAPE;
+  if (!f32_number(scale) || scale <= 0 || !f32_number(1.0 / scale) || !f32_number(balance)) return FP8Q_ERR_VALUE;
+  if (!counts || !loss || !slope || !workspace || (S > 0 && (!logits || !topk_ids || !topk_weights)))
+    return FP8Q_ERR_NULL;
+  if (misaligned(logits) || misaligned(bias, 4) || misaligned(topk_ids, 4) || misaligned(topk_weights, 4) ||
+      misaligned(counts, 4) || misaligned(loss, 4) || misaligned(slope, 4) || misaligned(workspace))
+    return FP8Q_ERR_ALIGN;
+  if (device_ok() != FP8Q_OK) return FP8Q_ERR_DEVICE;
+  return launched(fp8q::launch_moe_route(logits, dtype == FP8Q_OUT_F32, B, S, E, k, bias, valid,
+                                         score == FP8Q_SCORE_SOFTMAX, normalize != 0, static_cast<float>(scale), balance,
+                                         topk_ids, topk_weights, counts, loss, slope, workspace, as_stream(stream)));
+}
+
+fp8q_status fp8q_moe_route_backward(const void *logits, int32_t dtype, int64_t B, int64_t S, int64_t E, int64_t k,
+                                    const int32_t *topk_ids, const float *topk_weights, const float *dw,
+                                    const float *slope, const float *dloss, int32_t score, int32_t normalize,
+                                    double scale, void *dlogits, int32_t out_dtype, void *stream) {
+  if (bad_dtype(dtype) || bad_dtype(out_dtype) || (score != FP8Q_SCORE_SOFTMAX && score != FP8Q_SCORE_SIGMOID))
+    return FP8Q_ERR_DTYPE;
+  if (bad_route(B, S, E, k)) return FP8Q_ERR_SHAPE;
+  if (!f32_number(scale) || scale <= 0 || !f32_number(1.0 / scale)) return FP8Q_ERR_VALUE;
+  if (S == 0) return FP8Q_OK;
+  if (!logits || !topk_ids || !topk_weights || !dw || !slope || !dlogits) return FP8Q_ERR_NULL;
+  if (misaligned(logits) || misaligned(topk_ids, 4) || misaligned(topk_weights, 4) || misaligned(dw, 4) ||
+      misaligned(slope, 4) || misaligned(dloss, 4) || misaligned(dlogits))
+    return FP8Q_ERR_ALIGN;
+  if (device_ok() != FP8Q_OK) return FP8Q_ERR_DEVICE;
+  return launched(fp8q::launch_moe_route_backward(logits, dtype == FP8Q_OUT_F32, B, S, E, k, topk_ids, topk_weights, dw,
+                                                  slope, dloss, score == FP8Q_SCORE_SOFTMAX, normalize != 0,
+                                                  static_cast<float>(scale), dlogits, out_dtype == FP8Q_OUT_F32,
+                                                  as_stream(stream)));
+}
+
 const char *fp8q_status_string(fp8q_status status) {
   switch (status) {
     case FP8Q_OK: return "ok";
@@ -380,7 +466,7 @@ const char *fp8q_status_string(fp8q_status status) {
     case FP8Q_ERR_DEVICE: return "no usable HIP device";
     case FP8Q_ERR_LAUNCH: return "kernel launch failed";
     case FP8Q_ERR_OFFSETS: return "grouped GEMM offsets invalid (offsets[0] != 0, decreasing, or offsets[G] != M_tot)";
-    case FP8Q_ERR_VALUE: return "hyperparameter out of range (not a finite FP32 number, beta outside [0, 1), eps < 0, step < 1, or lr / (1 - beta1^step) or lr * weight_decay past FP32)";
+    case FP8Q_ERR_VALUE: return "hyperparameter out of range (not a finite FP32 number, beta outside [0, 1), eps < 0, step < 1, scale <= 0, or lr / (1 - beta1^step) or lr * weight_decay past FP32)";
     default: return "unknown status";
   }
 }

@@ -106,4 +106,38 @@ constexpr int64_t kAdamwPerGroup = 2048;  // elements of a workgroup of 256 thre
 hipError_t launch_adamw(const fp8q_adamw_tensor *tensors, int64_t count, bool grad_f32, bool e4m3,
                         const fp8q_adamw_hyper &hyper, hipStream_t stream);
 
+constexpr int64_t kMaxNormWidth = 16384;  // columns: 1024 threads of 16
+constexpr int64_t kNormGroups = 256;      // the most workgroups that layer norm's gradient leaves sums of
+
+// Workgroups of launch_layer_norm_backward for T rows; its `part` holds 2 H floats for each (H without db).
+int64_t norm_backward_groups(int64_t T);
+
+// y = (x - mean) rstd w + b of rows of H values (center false: RMS norm, mean not written); b may be null.
+hipError_t launch_layer_norm(const void *x, bool x_f32, const float *w, const float *b, int64_t T, int64_t H, float eps,
+                             bool center, void *y, bool out_f32, float *mean, float *rstd, hipStream_t stream);
+
+// dx, dw and db (unless null) of launch_layer_norm; mean null: RMS norm.
+hipError_t launch_layer_norm_backward(const void *dy, bool dy_f32, const void *x, bool x_f32, const float *w,
+                                      const float *mean, const float *rstd, int64_t T, int64_t H, void *dx, bool out_f32,
+                                      float *dw, float *db, float *part, hipStream_t stream);
+
+constexpr int kMaxTopK = 64;
+constexpr int64_t kMaxSequences = 65535;  // the second dimension of a grid
+constexpr int64_t kRouteGroups = 256;     // the most workgroups per sequence of the router
+
+// Bytes of launch_moe_route's workspace (16-byte aligned).
+int64_t moe_route_workspace(int64_t B, int64_t S, int64_t E);
+
+// Top-k experts of B sequences of S tokens from their logits [B][S][E], gating weights, counts [B][E] and
+// the balance loss with its slope [B][E].
+hipError_t launch_moe_route(const void *logits, bool f32, int64_t B, int64_t S, int64_t E, int64_t k, const float *bias,
+                            const uint8_t *valid, bool softmax, bool normalize, float scale, double balance, int32_t *ids,
+                            float *w, int32_t *counts, float *loss, float *slope, void *workspace, hipStream_t stream);
+
+// Gradient of the weights (dw) and of the loss (dloss, 1 if null) by the logits.
+hipError_t launch_moe_route_backward(const void *logits, bool f32, int64_t B, int64_t S, int64_t E, int64_t k,
+                                     const int32_t *ids, const float *w, const float *dw, const float *slope,
+                                     const float *dloss, bool softmax, bool normalize, float scale, void *dlogits,
+                                     bool out_f32, hipStream_t stream);
+
 }  // namespace fp8q

@@ -65,7 +65,7 @@
 extern "C" {
 #endif
 
-#define FP8Q_ABI_VERSION 8
+#define FP8Q_ABI_VERSION 9
 
 typedef int32_t fp8q_status;
 
@@ -464,6 +464,97 @@ typedef struct {
 
 fp8q_status fp8q_adamw(const fp8q_adamw_tensor *tensors, int64_t count, int32_t grad_dtype, int32_t state_dtype,
                        const fp8q_adamw_hyper *hyper, void *stream);
+
+/*
+ * Around the experts of an MoE layer: the norm whose output the quantizers and the router read, the
+ * router itself, and their gradients.  The router's ids feed fp8q_moe_dispatch and fp8q_moe_sort, its
+ * weights fp8q_moe_combine; dw of fp8q_moe_combine_backward feeds its gradient.
+ */
+
+/*
+ * Layer norm (center != 0) or RMS norm (center == 0) of every row,
+ *   mean = sum x / H (RMS norm: 0),  rstd = 1 / sqrt(sum (x - mean)^2 / H + eps),
+ *   y = (x - mean) rstd weight + bias,
+ * sums in FP32, y rounded once.
+ *   x : [T][H] in x_dtype;  weight : [H] FP32;  bias : [H] FP32 or NULL
+ *   y : [T][H] in out_dtype (out);  rstd : [T] FP32 (out);  mean : [T] FP32 (out; center == 0: not written,
+ *       may be NULL)
+ * Requires H % 8 == 0, 8 <= H <= 16384, eps >= 0.  T == 0 is a no-op.  Values whose squares FP32 does not hold
+ * (above about 1e19) give y = 0.
+ * Errors: FP8Q_ERR_DTYPE, FP8Q_ERR_SHAPE, FP8Q_ERR_VALUE, FP8Q_ERR_NULL, FP8Q_ERR_ALIGN (mean and rstd 4-byte),
+ * FP8Q_ERR_DEVICE, FP8Q_ERR_LAUNCH.
+ */
+fp8q_status fp8q_layer_norm(const void *x, int32_t x_dtype, const float *weight, const float *bias, int64_t T, int64_t H,
+                            double eps, int32_t center, void *y, int32_t out_dtype, float *mean, float *rstd,
+                            void *stream);
+
+/*
+ * Gradients of fp8q_layer_norm, with h = (x - mean) rstd and g = dy weight:
+ *   dx = rstd (g - sum g / H - h sum g h / H)   (RMS norm: without sum g / H),
+ *   dweight = sum over rows of dy h,  dbias = sum over rows of dy.
+ * Sums in FP32 in an order that only the sizes decide (the same inputs give the same bits).
+ *   dy, x : [T][H] in dy_dtype, x_dtype;  mean, rstd : [T] as written by fp8q_layer_norm (mean NULL: RMS norm)
+ *   dx : [T][H] in out_dtype (out);  dweight : [H] FP32 (out);  dbias : [H] FP32 (out) or NULL
+ *   workspace : fp8q_layer_norm_backward_workspace(T, H) bytes (8 H per 4 rows, at most 2048 H), written
+ * Requires H as above.  With T == 0 dweight and dbias are zeros.  Errors: as fp8q_layer_norm.
+ */
+fp8q_status fp8q_layer_norm_backward(const void *dy, int32_t dy_dtype, const void *x, int32_t x_dtype,
+                                     const float *weight, const float *mean, const float *rstd, int64_t T, int64_t H,
+                                     void *dx, int32_t out_dtype, float *dweight, float *dbias, void *workspace,
+                                     void *stream);
+
+/* Bytes of fp8q_layer_norm_backward's workspace, or FP8Q_ERR_SHAPE. */
+int64_t fp8q_layer_norm_backward_workspace(int64_t T, int64_t H);
+
+enum { FP8Q_SCORE_SOFTMAX = 0, FP8Q_SCORE_SIGMOID = 1 };
+
+/*
+ * Router of an MoE layer over B sequences of S tokens.  Source: dlbhg.com page on DeepSeek-V3's
+ * training techniques, section 1.1 item 2 (8 of 256 routed experts per token, balanced by a bias per
+ * expert and a sequence-wise loss); the formulas are this library's reading.
+ * With a token's scores s = softmax(logits) or sigmoid(logits):
+ *   topk_ids : the k experts with the largest s + bias (without a bias: with the largest logits),
+ *              largest first, ties to the lower index; ranks are those of s and the sum in 64 bits
+ *   topk_weights[j] = scale s_j, or with normalize scale s_j / (sum of the k chosen s)
+ *   counts[b][e] : tokens of sequence b with expert e among their k
+ *   slope[b][e] = balance / B * E counts[b][e] / (n_b sum_e counts[b][e]), n_b the sequence's tokens
+ *   loss = sum over b, e of slope[b][e] * (sum over the tokens of p_e),  p = s / sum_e s_e
+ * so that slope is the loss's derivative by each p_e, with the counts held fixed.
+ *   logits : [B][S][E] BF16 or FP32 per dtype, finite or -inf (otherwise the token's weights, the
+ *            sequence's slope and the loss are unspecified; ids stay below E); an expert with logit -inf
+ *            is not chosen, slots left over get id -1 and weight 0
+ *   bias : [E] FP32 or NULL;  valid : [B][S] bytes, 0 for a token that does not count, or NULL
+ *          A token that does not count, or whose logits are all -inf, gets ids -1 and weights 0 and
+ *          enters neither counts nor loss; its logits are not used (they may be NaN).
+ *   topk_ids int32, topk_weights FP32 : [B][S][k] (out);  counts int32, slope FP32 : [B][E] (out);  loss : FP32 (out)
+ *   workspace : fp8q_moe_route_workspace(B, S, E) bytes, written
+ * Requires 1 <= E <= 1024, 1 <= k <= min(E, 64), 1 <= B <= 65535, B S k < 2^31, scale > 0 (it and its reciprocal
+ * FP32 numbers), balance an FP32 number.  Sums in FP32 and 64 bits, the same bits for the same inputs.  One launch for one
+ * sequence of up to 32 tokens (8 with more than 256 experts), two beyond.
+ * Errors: FP8Q_ERR_DTYPE (also score), FP8Q_ERR_SHAPE, FP8Q_ERR_VALUE, FP8Q_ERR_NULL, FP8Q_ERR_ALIGN (logits and
+ * workspace 16-byte, the rest 4-byte), FP8Q_ERR_DEVICE, FP8Q_ERR_LAUNCH.
+ */
+fp8q_status fp8q_moe_route(const void *logits, int32_t dtype, int64_t B, int64_t S, int64_t E, int64_t k,
+                           const float *bias, const uint8_t *valid, int32_t score, int32_t normalize, double scale,
+                           double balance, int32_t *topk_ids, float *topk_weights, int32_t *counts, float *loss,
+                           float *slope, void *workspace, void *stream);
+
+/* Bytes of fp8q_moe_route's workspace, or FP8Q_ERR_SHAPE. */
+int64_t fp8q_moe_route_workspace(int64_t B, int64_t S, int64_t E);
+
+/*
+ * Gradient of fp8q_moe_route by the logits, from dw (the gradient of topk_weights) and dloss (that of
+ * loss): dlogits = sum_j dw_j d topk_weights_j / d logits + dloss * d loss / d logits, the choice of the
+ * experts and the counts held fixed; zeros for a token whose ids are -1.  FP32, rounded once.
+ *   logits, topk_ids, topk_weights, slope, score, normalize, scale : as given to and written by fp8q_moe_route
+ *   dw : [B][S][k] FP32 (slots with id -1 are not used);  dloss : DEVICE FP32 or NULL for 1
+ *   dlogits : [B][S][E] in out_dtype (out)
+ * Requirements and errors as for fp8q_moe_route; S == 0 is a no-op.
+ */
+fp8q_status fp8q_moe_route_backward(const void *logits, int32_t dtype, int64_t B, int64_t S, int64_t E, int64_t k,
+                                    const int32_t *topk_ids, const float *topk_weights, const float *dw,
+                                    const float *slope, const float *dloss, int32_t score, int32_t normalize,
+                                    double scale, void *dlogits, int32_t out_dtype, void *stream);
 
 /* Static, human-readable text for a status code (never NULL). */
 const char *fp8q_status_string(fp8q_status status);
