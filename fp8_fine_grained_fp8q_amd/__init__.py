@@ -33,6 +33,8 @@ Around the experts:
     dx, dweight, dbias = fp8q_layer_norm_backward(dy, x, weight, mean, rstd, want_bias=True)
     topk_ids, topk_w, counts, loss, slope = fp8q_moe_route(logits, k, bias, balance=1e-4)
     dlogits = fp8q_moe_route_backward(logits, topk_ids, topk_w, dw, slope, dloss)
+    out = fp8q_orthogonalize(x)                                  # singular values near one
+    fp8q_muon(param, grad, momentum, lr=2e-4)                    # the optimizer for matrices, in place
 
 Layouts: xq uint8 [M, K]; sa float32 [K/128, M]; wq uint8 [G, N, K]; sb float32
 [G, N/128, K/128]; C row-major [M, N].
@@ -65,7 +67,8 @@ EXPORTED = ("fp8q_quantize_act_1x128", "fp8q_quantize_w_128x128", "fp8q_gemm_blo
             "fp8q_moe_sort_backward", "fp8q_moe_combine_backward", "fp8q_swiglu_backward",
             "fp8q_quantize_act_grouped", "fp8q_grouped_gemm_rowscaled", "fp8q_adamw", "fp8q_layer_norm",
             "fp8q_layer_norm_backward", "fp8q_layer_norm_backward_workspace", "fp8q_moe_route",
-            "fp8q_moe_route_workspace", "fp8q_moe_route_backward", "fp8q_status_string", "fp8q_abi_version")
+            "fp8q_moe_route_workspace", "fp8q_moe_route_backward", "fp8q_orthogonalize", "fp8q_muon",
+            "fp8q_muon_workspace", "fp8q_status_string", "fp8q_abi_version")
 
 
 class Fp8qError(RuntimeError):
@@ -84,6 +87,17 @@ class _AdamwHyper(ctypes.Structure):
     """fp8q_adamw_hyper of include/fp8q.h."""
     _fields_ = [(name, ctypes.c_double) for name in ("lr", "beta1", "beta2", "eps", "weight_decay", "grad_scale")] + [
         ("step", ctypes.c_int64), ("scalars", ctypes.c_void_p)]
+
+
+class _NewtonSchulz(ctypes.Structure):
+    """fp8q_newton_schulz of include/fp8q.h."""
+    _fields_ = [(name, ctypes.c_double) for name in "abc"] + [("steps", ctypes.c_int64)]
+
+
+class _MuonHyper(ctypes.Structure):
+    """fp8q_muon_hyper of include/fp8q.h."""
+    _fields_ = [(name, ctypes.c_double) for name in ("lr", "beta", "weight_decay", "scale", "grad_scale")] + [
+        ("ns", _NewtonSchulz), ("nesterov", ctypes.c_int64), ("device_lr", ctypes.c_void_p)]
 
 
 _lib = None
@@ -125,6 +139,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.fp8q_moe_route.argtypes = [vp, i32, i64, i64, i64, i64, vp, vp, i32, i32, f64, f64, vp, vp, vp, vp, vp, vp, vp]
     lib.fp8q_moe_route_workspace.argtypes = [i64, i64, i64]
     lib.fp8q_moe_route_backward.argtypes = [vp, i32, i64, i64, i64, i64, vp, vp, vp, vp, vp, i32, i32, f64, vp, i32, vp]
+    lib.fp8q_orthogonalize.argtypes = [vp, i32, i64, i64, i64, ctypes.POINTER(_NewtonSchulz), vp, vp, vp]
+    lib.fp8q_muon.argtypes = [vp, vp, i32, vp, i64, i64, i64, ctypes.POINTER(_MuonHyper), vp, vp, vp]
+    lib.fp8q_muon_workspace.argtypes = [i64, i64, i64]
     for name in EXPORTED:
         getattr(lib, name).restype = i64 if name.endswith("_workspace") else i32
     lib.fp8q_status_string.argtypes = [i32]
@@ -873,6 +890,72 @@ def fp8q_moe_route_backward(logits: torch.Tensor, topk_ids: torch.Tensor, topk_w
     return dlogits
 
 
+def _need_matrices(t, name: str):
+    """A contiguous bf16 or float32 [P, Q] or [G, P, Q]; returns (G, P, Q)."""
+    if not isinstance(t, torch.Tensor) or (t.dtype != torch.bfloat16 and t.dtype != torch.float32):
+        raise ValueError(f"{name} must be a bfloat16 or float32 tensor")
+    if not t.is_cuda or not t.is_contiguous() or t.dim() not in (2, 3):
+        raise ValueError(f"{name} must be a contiguous CUDA tensor [P, Q] or [G, P, Q]")
+    return (1, *t.shape) if t.dim() == 2 else tuple(t.shape)
+
+
+NEWTON_SCHULZ = (3.4445, -4.7750, 2.0315)  # a + b s^2 + c s^4 takes singular values from 0.002 to 1 near one in five steps
+
+
+def fp8q_orthogonalize(x: torch.Tensor, steps: int = 5, coefficients=NEWTON_SCHULZ, out: torch.Tensor | None = None,
+                       stream=None):
+    """The matrices x (bf16 or float32 [P, Q] or [G, P, Q]) with their singular values brought near one, as bf16
+    like x: `steps` times X = (a I + b X X^T + c (X X^T)^2) X, from X = x / |x|_F."""
+    if stream is not None:
+        with _on(stream):
+            return fp8q_orthogonalize(x, steps, coefficients, out)
+    G, P, Q = _need_matrices(x, "x")
+    s = _here(x, out)
+    if G == 0:
+        return _out(out, torch.bfloat16, "out", x.shape, x)
+    lib = load_library()
+    out = _out(out, torch.bfloat16, "out", x.shape, x)
+    work = _workspace(lib.fp8q_muon_workspace(G, P, Q), x)
+    ns = _NewtonSchulz(*coefficients, steps)
+    _check(lib.fp8q_orthogonalize(_ptr(x), _out_code(x.dtype), G, P, Q, ctypes.byref(ns), _ptr(out), _ptr(work), s),
+           "fp8q_orthogonalize")
+    return out
+
+
+def fp8q_muon(param: torch.Tensor, grad: torch.Tensor, momentum: torch.Tensor, lr: float, beta: float = 0.95,
+              nesterov: bool = True, weight_decay: float = 0.0, scale: float | None = None, steps: int = 5,
+              coefficients=NEWTON_SCHULZ, grad_scale: float = 1.0, copy: torch.Tensor | None = None,
+              device_lr: torch.Tensor | None = None, stream=None) -> None:
+    """One Muon step in place on a matrix [P, Q] or on G of them [G, P, Q]: param and momentum float32, grad bf16 or
+    float32.  param = param (1 - lr weight_decay) - lr scale O with O the momentum (Nesterov's, by default) made
+    orthogonal as by fp8q_orthogonalize; scale defaults to 0.2 sqrt(max(P, Q)).  copy: bf16, written with the new
+    parameters.  device_lr: a device float32 [1] read by the kernels in place of lr."""
+    if stream is not None:
+        with _on(stream):
+            return fp8q_muon(param, grad, momentum, lr, beta, nesterov, weight_decay, scale, steps, coefficients,
+                             grad_scale, copy, device_lr)
+    G, P, Q = _need_matrices(grad, "grad")
+    _need(param, torch.float32, "param", grad.shape)
+    _need(momentum, torch.float32, "momentum", grad.shape)
+    if copy is not None:
+        _need(copy, torch.bfloat16, "copy", grad.shape)
+    if device_lr is not None:
+        _need(device_lr, torch.float32, "device_lr", (1,))
+    s = _here(param, grad, momentum, copy, device_lr)
+    if G == 0:
+        return
+    spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in (param, grad, momentum, copy)
+                   if t is not None)
+    if any(b[0] < a[1] for a, b in zip(spans, spans[1:])):
+        raise ValueError("param, grad, momentum and copy must not share memory")
+    lib = load_library()
+    work = _workspace(lib.fp8q_muon_workspace(G, P, Q), grad)
+    hyper = _MuonHyper(lr, beta, weight_decay, 0.2 * max(P, Q) ** 0.5 if scale is None else scale, grad_scale,
+                       _NewtonSchulz(*coefficients, steps), bool(nesterov), _ptr(device_lr) or None)
+    _check(lib.fp8q_muon(_ptr(param), _ptr(grad), _out_code(grad.dtype), _ptr(momentum), G, P, Q, ctypes.byref(hyper),
+                         _ptr(copy), _ptr(work), s), "fp8q_muon")
+
+
 quantize_act_1x128 = fp8q_quantize_act_1x128
 quantize_w_128x128 = fp8q_quantize_w_128x128
 gemm_blockscaled = fp8q_gemm_blockscaled
@@ -894,3 +977,5 @@ layer_norm = fp8q_layer_norm
 layer_norm_backward = fp8q_layer_norm_backward
 moe_route = fp8q_moe_route
 moe_route_backward = fp8q_moe_route_backward
+orthogonalize = fp8q_orthogonalize
+muon = fp8q_muon

@@ -56,6 +56,19 @@ bool bad_route(int64_t B, int64_t S, int64_t E, int64_t k) {
          B * S * k >= kMaxDim;
 }
 
+// Shared checks of Muon's matrices [G][P][Q] and of its Newton-Schulz products.
+constexpr int64_t kMaxMuonSize = int64_t(1) << 20;
+constexpr int64_t kMaxMuonSteps = 100;
+
+bool bad_matrices(int64_t G, int64_t P, int64_t Q) {
+  return G < 1 || bad_dim(G) || P < 0 || P > kMaxMuonSize || Q < 0 || Q > kMaxMuonSize || too_many(G * 64, P * Q) ||
+         (P > 0 && Q > 0 && !fp8q::muon_grids_fit(G, P, Q));
+}
+
+bool bad_newton_schulz(const fp8q_newton_schulz &ns) {
+  return !f32_number(ns.a) || !f32_number(ns.b) || !f32_number(ns.c) || ns.steps < 1 || ns.steps > kMaxMuonSteps;
+}
+
 // Shared checks of the two GEMM entry points (everything except the grouped extras).
 fp8q_status check_gemm(const uint8_t *xq, const float *sa, const uint8_t *wq, const float *sb,
                        int64_t M, int64_t N, int64_t K, void *c, int32_t out_dtype) {
@@ -456,6 +469,47 @@ fp8q_status fp8q_moe_route_backward(const void *logits, int32_t dtype, int64_t B
                                                   as_stream(stream)));
 }
 
+int64_t fp8q_muon_workspace(int64_t G, int64_t P, int64_t Q) {
+  if (bad_matrices(G, P, Q)) return FP8Q_ERR_SHAPE;
+  return P == 0 || Q == 0 ? 0 : fp8q::muon_workspace(G, P, Q);
+}
+
+fp8q_status fp8q_orthogonalize(const void *x, int32_t dtype, int64_t G, int64_t P, int64_t Q,
+                               const fp8q_newton_schulz *ns, uint16_t *out_bf16, void *workspace, void *stream) {
+  if (bad_dtype(dtype)) return FP8Q_ERR_DTYPE;
+  if (bad_matrices(G, P, Q)) return FP8Q_ERR_SHAPE;
+  if (!ns) return FP8Q_ERR_NULL;
+  if (bad_newton_schulz(*ns)) return FP8Q_ERR_VALUE;
+  if (P == 0 || Q == 0) return FP8Q_OK;
+  if (!x || !out_bf16 || !workspace) return FP8Q_ERR_NULL;
+  if (misaligned(x) || misaligned(out_bf16) || misaligned(workspace)) return FP8Q_ERR_ALIGN;
+  if (device_ok() != FP8Q_OK) return FP8Q_ERR_DEVICE;
+  return launched(fp8q::launch_orthogonalize(x, dtype == FP8Q_OUT_F32, G, P, Q, *ns, out_bf16, workspace,
+                                             as_stream(stream)));
+}
+
+fp8q_status fp8q_muon(float *param, const void *grad, int32_t grad_dtype, float *momentum, int64_t G, int64_t P, int64_t Q,
+                      const fp8q_muon_hyper *hyper, uint16_t *p_bf16, void *workspace, void *stream) {
+  if (bad_dtype(grad_dtype)) return FP8Q_ERR_DTYPE;
+  if (bad_matrices(G, P, Q)) return FP8Q_ERR_SHAPE;
+  if (!hyper) return FP8Q_ERR_NULL;
+  const fp8q_muon_hyper &h = *hyper;
+  const double numbers[] = {h.lr, h.beta, h.weight_decay, h.scale, h.grad_scale};
+  for (double v : numbers)
+    if (!f32_number(v)) return FP8Q_ERR_VALUE;
+  if (!f32_beta(h.beta) || bad_newton_schulz(h.ns)) return FP8Q_ERR_VALUE;
+  if (!h.device_lr && (!(fabs(1.0 - h.lr * h.weight_decay) <= FLT_MAX) || !(fabs(h.lr * h.scale) <= FLT_MAX)))
+    return FP8Q_ERR_VALUE;
+  if (P == 0 || Q == 0) return FP8Q_OK;
+  if (!param || !grad || !momentum || !workspace) return FP8Q_ERR_NULL;
+  if (misaligned(param) || misaligned(grad) || misaligned(momentum) || misaligned(p_bf16) || misaligned(h.device_lr, 4) ||
+      misaligned(workspace))
+    return FP8Q_ERR_ALIGN;
+  if (device_ok() != FP8Q_OK) return FP8Q_ERR_DEVICE;
+  return launched(fp8q::launch_muon(param, grad, grad_dtype == FP8Q_OUT_F32, momentum, G, P, Q, h, p_bf16, workspace,
+                                    as_stream(stream)));
+}
+
 const char *fp8q_status_string(fp8q_status status) {
   switch (status) {
     case FP8Q_OK: return "ok";
@@ -466,7 +520,7 @@ const char *fp8q_status_string(fp8q_status status) {
     case FP8Q_ERR_DEVICE: return "no usable HIP device";
     case FP8Q_ERR_LAUNCH: return "kernel launch failed";
     case FP8Q_ERR_OFFSETS: return "grouped GEMM offsets invalid (offsets[0] != 0, decreasing, or offsets[G] != M_tot)";
-    case FP8Q_ERR_VALUE: return "hyperparameter out of range (not a finite FP32 number, beta outside [0, 1), eps < 0, step < 1, scale <= 0, or lr / (1 - beta1^step) or lr * weight_decay past FP32)";
+    case FP8Q_ERR_VALUE: return "hyperparameter out of range (not a finite FP32 number, beta outside [0, 1), eps < 0, a step count out of range, a router's scale <= 0, or lr / (1 - beta1^step) or lr * weight_decay past FP32)";
     default: return "unknown status";
   }
 }

@@ -140,4 +140,16 @@ hipError_t launch_moe_route_backward(const void *logits, bool f32, int64_t B, in
                                      const float *dloss, bool softmax, bool normalize, float scale, void *dlogits,
                                      bool out_f32, hipStream_t stream);
 
+// Bytes of the workspace of the two calls below (16-byte aligned), and whether their launches fit HIP's grids.
+int64_t muon_workspace(int64_t G, int64_t P, int64_t Q);
+bool muon_grids_fit(int64_t G, int64_t P, int64_t Q);
+
+// BF16 matrices [G][P][Q] with the singular vectors of x and singular values near one.
+hipError_t launch_orthogonalize(const void *x, bool f32, int64_t G, int64_t P, int64_t Q, const fp8q_newton_schulz &ns,
+                                uint16_t *out, void *workspace, hipStream_t stream);
+
+// A Muon step on G matrices: momentum, the update made orthogonal, the parameter (and its BF16 copy unless null).
+hipError_t launch_muon(float *param, const void *grad, bool f32, float *momentum, int64_t G, int64_t P, int64_t Q,
+                       const fp8q_muon_hyper &hyper, uint16_t *copy, void *workspace, hipStream_t stream);
+
 }  // namespace fp8q

@@ -556,6 +556,59 @@ fp8q_status fp8q_moe_route_backward(const void *logits, int32_t dtype, int64_t B
                                     const float *slope, const float *dloss, int32_t score, int32_t normalize,
                                     double scale, void *dlogits, int32_t out_dtype, void *stream);
 
+/*
+ * Muon, the optimizer for weight matrices beside fp8q_adamw: the update of a matrix is replaced by one with
+ * the same singular vectors and singular values near one, by `steps` products
+ *   X = U / |U|_F;  A = X X^T,  X = (a I + b A + c A^2) X.
+ * (This library's reading of a training step's optimizer; the pages name none for matrices.)
+ * X, A and C = a I + b A + c A^2 are multiplied as FP16 with FP32 sums (11 significant bits of what is off the
+ * diagonals; the diagonals in FP32, X itself kept in 22 bits): the result is off by 1e-4 to 1e-3 of its norm.  |U|_F is
+ * summed in 64 bits.  Coefficients must keep every singular value below 15 in between (those here keep
+ * them below 1.3), or the result is not finite.  U is finite; a matrix of zeros gives zeros.
+ *   ns : HOST struct, read during the call only; 1 <= steps <= 100; usual: {3.4445, -4.7750, 2.0315, 5}
+ *   workspace : fp8q_muon_workspace(G, P, Q) bytes: about 8 per element of the matrices (their sizes rounded up to
+ *               128) and 4 per element of the G square matrices of the smaller size; written
+ */
+typedef struct {
+  double a, b, c;
+  int64_t steps;
+} fp8q_newton_schulz;
+
+/*
+ * out = the matrices x made orthogonal.
+ *   x : [G][P][Q] BF16 or FP32 per dtype;  out_bf16 : [G][P][Q] (out)
+ * Requires G >= 1, 0 <= P, Q <= 2^20 (and G P Q such that the grids fit).  P == 0 or Q == 0 is a no-op.
+ * 2 + 3 steps launches.  Errors: FP8Q_ERR_DTYPE, FP8Q_ERR_SHAPE, FP8Q_ERR_VALUE, FP8Q_ERR_NULL, FP8Q_ERR_ALIGN,
+ * FP8Q_ERR_DEVICE, FP8Q_ERR_LAUNCH.
+ */
+fp8q_status fp8q_orthogonalize(const void *x, int32_t dtype, int64_t G, int64_t P, int64_t Q,
+                               const fp8q_newton_schulz *ns, uint16_t *out_bf16, void *workspace, void *stream);
+
+/*
+ * One Muon step on G matrices, in place, with g = grad_scale * grad:
+ *   momentum = beta momentum + g,  U = nesterov ? g + beta momentum : momentum,  O = U made orthogonal,
+ *   param = param (1 - lr weight_decay) - lr scale O,   FP32 (O not rounded before).
+ *   param, momentum : [G][P][Q] FP32 (in, out);  grad : [G][P][Q] BF16 or FP32 per grad_dtype
+ *   p_bf16 : [G][P][Q] BF16 (out), the new param rounded to nearest even, or NULL
+ *   hyper : HOST struct, read during the call only; 0 <= beta < 1, numbers that FP32 holds (also 1 - lr weight_decay
+ *           and lr scale).  scale is often 0.2 sqrt(max(P, Q)) (the size of an AdamW update).  device_lr, if not
+ *           NULL, is a DEVICE float read by the kernels in place of lr (not checked), so that a captured
+ *           step can be replayed with new values.
+ * All memory disjoint.  Otherwise as fp8q_orthogonalize.
+ */
+typedef struct {
+  double lr, beta, weight_decay, scale, grad_scale;
+  fp8q_newton_schulz ns;
+  int64_t nesterov;
+  const float *device_lr;
+} fp8q_muon_hyper;
+
+fp8q_status fp8q_muon(float *param, const void *grad, int32_t grad_dtype, float *momentum, int64_t G, int64_t P, int64_t Q,
+                      const fp8q_muon_hyper *hyper, uint16_t *p_bf16, void *workspace, void *stream);
+
+/* Bytes of the workspace of the two calls above, or FP8Q_ERR_SHAPE. */
+int64_t fp8q_muon_workspace(int64_t G, int64_t P, int64_t Q);
+
 /* Static, human-readable text for a status code (never NULL). */
 const char *fp8q_status_string(fp8q_status status);
 
