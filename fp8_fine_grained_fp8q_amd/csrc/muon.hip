@@ -33,10 +33,10 @@ namespace fp8q {
 namespace {
 
 #define FP8Q_LDS __attribute__((address_space(3)))
-typedef int v4i __attribute__((ext_vector_type(4)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 typedef _Float16 v4h __attribute__((ext_vector_type(4)));
+typedef short v4s __attribute__((ext_vector_type(4)));
 
 constexpr float kScale = 4096.0f;  // of X, A and C as stored
 constexpr int64_t kPad = 128;      // sizes of the stored matrices
@@ -58,6 +58,17 @@ struct Update {
 template <bool kF32>
 __device__ __forceinline__ float value_at(const void *p, int64_t i) {
   return kF32 ? static_cast<const float *>(p)[i] : bf16_lo(static_cast<const uint16_t *>(p)[i]);
+}
+
+template <bool kF32>
+__device__ __forceinline__ void load4(const void *p, int64_t i, float (&v)[4]) {
+  if (kF32) {
+    const float4 u = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
+    v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+  } else {
+    const uint2 u = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + i);
+    v[0] = bf16_lo(u.x), v[1] = bf16_hi(u.x), v[2] = bf16_lo(u.y), v[3] = bf16_hi(u.y);
+  }
 }
 
 // The update from a gradient and the new momentum.
@@ -112,23 +123,45 @@ __global__ __launch_bounds__(256) void muon_momentum_kernel(const Update u, int6
     sums[static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x] = (waves[0] + waves[1]) + (waves[2] + waves[3]);
 }
 
-// X in the workspace: hi + lo = kScale X, [mp][np], and hi transposed, [np][mp]; zeros in the padding.
+// X as it is stored: hi in FP16, 11 bits, and lo in E4M3, 4 more, with hi + lo / kLow = kScale X, [Pp][Qp] in the
+// orientation of the matrix itself, zeros in the padding.
 struct Matrices {
-  _Float16 *hi, *lo, *hit;
-  int64_t mp, np;
+  const _Float16 *hi;  // read
+  _Float16 *next;      // written
+  uint8_t *lo;         // both
+  int64_t Pp, Qp;
 };
 
-__device__ __forceinline__ void split(float v, _Float16 &hi, _Float16 &lo) {
-  hi = static_cast<_Float16>(v);
-  lo = static_cast<_Float16>(v - static_cast<float>(hi));
+constexpr float kLow = 256.0f;
+
+// Four values as hi and lo.
+__device__ __forceinline__ v4h split(v4f v, uint32_t &lo) {
+  v4h hi;
+  v4f rest;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    hi[k] = static_cast<_Float16>(v[k]);
+    rest[k] = (v[k] - static_cast<float>(hi[k])) * kLow;
+  }
+  lo = pack4_e4m3(rest[0], rest[1], rest[2], rest[3]);
+  return hi;
 }
 
-// Workgroup (x, y, z): a tile of 64 x 64 of matrix z, [P][Q], rows 64 y.
-template <bool kF32, bool kTall>
+__device__ __forceinline__ v4f join(v4h hi, uint32_t lo) {
+  const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(lo), false);
+  const f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(lo), true);
+  const float rest[4] = {a.x, a.y, b.x, b.y};
+  v4f v;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = __builtin_fmaf(rest[k], 1.0f / kLow, static_cast<float>(hi[k]));
+  return v;
+}
+
+// Workgroup (x, y, z): 4 rows of 256 columns of matrix z, and every gridDim.y-th four after them.
+template <bool kF32, bool kVector>
 __global__ __launch_bounds__(256) void muon_start_kernel(const Update u, const double *__restrict__ sums, int count,
                                                          int64_t P, int64_t Q, const Matrices x) {
   __shared__ double waves[4];
-  __shared__ float tile[64][65];
   double sum = 0.0;
   for (int i = threadIdx.x; i < count; i += 256) sum += sums[static_cast<int64_t>(blockIdx.z) * count + i];
   for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
@@ -137,143 +170,405 @@ __global__ __launch_bounds__(256) void muon_start_kernel(const Update u, const d
   sum = (waves[0] + waves[1]) + (waves[2] + waves[3]);
   const double by = sum > 0.0 ? static_cast<double>(kScale) / sqrt(sum) : 0.0;
 
-  const int64_t r0 = static_cast<int64_t>(blockIdx.y) * 64, c0 = static_cast<int64_t>(blockIdx.x) * 64;
-  const int64_t base = blockIdx.z * P * Q;
-  const int c = threadIdx.x & 63;
-#pragma unroll 4
-  for (int r = threadIdx.x >> 6; r < 64; r += 4) {
-    float v = 0.0f;
-    if (r0 + r < P && c0 + c < Q) {
-      const int64_t at = base + (r0 + r) * Q + c0 + c;
-      const float g = value_at<kF32>(u.grad, at);
-      v = u.momentum != nullptr ? update_of(u, g, u.momentum[at]) : g;
-      v = static_cast<float>(v * by);
-    }
-    tile[r][c] = v;
-  }
-  __syncthreads();
-  // hi and lo by rows of X, then hi by its columns; 4 values per store
-  const int64_t area = x.mp * x.np, at0 = blockIdx.z * area;
-  const int64_t i0 = kTall ? c0 : r0, j0 = kTall ? r0 : c0;  // the tile's place in X
-  const int q = (threadIdx.x & 15) * 4;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 256 + (threadIdx.x & 63) * 4;
+  if (c >= x.Qp) return;
+  for (int64_t r = static_cast<int64_t>(blockIdx.y) * 4 + (threadIdx.x >> 6); r < x.Pp; r += gridDim.y * 4) {
+    v4f v = {};
+    if (r < P) {
+      const int64_t at = (blockIdx.z * P + r) * Q + c;
+      if (kVector) {  // Q % 4 == 0
+        if (c < Q) {
+          float g[4], m[4];
+          load4<kF32>(u.grad, at, g);
+          if (u.momentum != nullptr) load4<true>(u.momentum, at, m);
 #pragma unroll
-  for (int r = threadIdx.x >> 4; r < 64; r += 16) {
-    v4h hi, lo, hit;
+          for (int k = 0; k < 4; ++k)
+            v[k] = static_cast<float>((u.momentum != nullptr ? update_of(u, g[k], m[k]) : g[k]) * by);
+        }
+      } else {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      _Float16 h, l;
-      split(kTall ? tile[q + k][r] : tile[r][q + k], h, l);
-      hi[k] = h;
-      lo[k] = l;
-      hit[k] = static_cast<_Float16>(kTall ? tile[r][q + k] : tile[q + k][r]);
+        for (int k = 0; k < 4; ++k) {
+          if (c + k >= Q) break;
+          const float g = value_at<kF32>(u.grad, at + k);
+          v[k] = static_cast<float>((u.momentum != nullptr ? update_of(u, g, u.momentum[at + k]) : g) * by);
+        }
+      }
     }
-    *reinterpret_cast<v4h *>(x.hi + at0 + (i0 + r) * x.np + j0 + q) = hi;
-    *reinterpret_cast<v4h *>(x.lo + at0 + (i0 + r) * x.np + j0 + q) = lo;
-    *reinterpret_cast<v4h *>(x.hit + at0 + (j0 + r) * x.mp + i0 + q) = hit;
+    uint32_t lo;
+    const v4h hi = split(v, lo);
+    const int64_t to = (blockIdx.z * x.Pp + r) * x.Qp + c;
+    *reinterpret_cast<v4h *>(x.next + to) = hi;
+    *reinterpret_cast<uint32_t *>(x.lo + to) = lo;
   }
 }
 
 // ---------------------------------------------------------------------------------------
-// Products.  A workgroup of 8 waves (4 x 2) makes a tile of kTile x kTile of P Q^T; each wave kTile / 4
-// rows by kTile / 2 columns.  Stages of 64 K (128 bytes a row) of both operands go to LDS by
-// buffer_load ... lds, double buffered: rows r and r + 8 of a group of 16 share a 256-byte line, the
-// 16-byte chunks of a row are swapped by r mod 8, so that the 16 rows of a fragment read use all 64
-// banks.  The operand with the output's columns is the instruction's first one: a lane then owns
-// one output row and four consecutive columns.
+// Products, out = P Q with P's rows and Q's columns contiguous or not: an operand is "by rows" where the
+// contracted index is contiguous, "by columns" where the output's is.  A workgroup of 8 waves
+// (4 x 2) makes a tile of kTile x kTile; each wave kTile / 4 rows by kTile / 2 columns.
+//
+// Stages of 64 of the contracted index go to LDS by buffer_load ... lds in panels of 64 rows of 128 bytes (by
+// rows: 64 of the output's rows; by columns: 64 of the contracted index by 64 columns); a wave moves 1 KB of
+// every panel.  In a panel rows r and r + 8 of a group of 16 share a 256-byte line and the 16-byte
+// chunks of a row are swapped among themselves, so that a fragment read touches every bank once: by rows
+// ds_read_b128 takes one chunk of 16 rows (chunk ^ r mod 8), by columns ds_read_b64_tr_b16 two neighbouring
+// chunks of 8 rows (chunk ^ 2 (r mod 4)) and turns them.
+//
+// The operand with the output's columns is the instruction's first one: a lane then owns one output row
+// and four consecutive columns per fragment.
 // ---------------------------------------------------------------------------------------
-__device__ __forceinline__ int lds_pos(int row, int c) {
-  const int r = row & 15;
-  return (row >> 4) * 2048 + (r & 7) * 256 + (r >> 3) * 128 + ((c ^ (r & 7)) << 4);
+constexpr int kPanel = 8192;
+
+__device__ __forceinline__ int panel_pos(int row, int slot) {
+  return (row >> 4) * 2048 + (row & 7) * 256 + ((row >> 3) & 1) * 128 + slot * 16;
 }
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void *p, int64_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), static_cast<short>(0), static_cast<int>(bytes),
-                                           0x00020000);
+// One operand's part of a tile: where its panels come from.
+template <bool kCols>
+struct Source {
+  const uint8_t *p;
+  int64_t stride;  // bytes of a row
+  int64_t bytes;   // by rows: of the tile's rows; by columns: of a stage
+  int voff, stages;
+
+  // By rows: rows [at, at + most) of `rows`; by columns: columns from `at` on, K rows.
+  __device__ __forceinline__ Source(const _Float16 *from, int64_t at, int64_t rows, int most, int64_t ld, int64_t K) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    stride = ld * 2;
+    stages = static_cast<int>(K / 64);
+    const int line = 4 * (wave & 1) + (lane >> 4), row = 16 * (wave >> 1) + line + 8 * ((lane >> 3) & 1);
+    const int chunk = (lane & 7) ^ (kCols ? 2 * (line & 3) : line);
+    voff = row * static_cast<int>(stride) + chunk * 16;
+    if (kCols) {
+      p = reinterpret_cast<const uint8_t *>(from + at);
+      bytes = 64 * stride - at * 2;  // columns past the last are others' or zeros, and their output is not used
+    } else {
+      p = reinterpret_cast<const uint8_t *>(from + at * ld);
+      bytes = (rows - at < most ? rows - at : most) * stride;  // rows past the last are zeros
+    }
+  }
+  // The wave's 1 KB of panel i of stage s; past the last stage zeros without traffic, so that every wave
+  // always has the same number of copies in flight.
+  __device__ __forceinline__ void copy(int s, int i, uint8_t *panel) const {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint8_t *const from = kCols ? p + s * 64 * stride : p;
+    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint8_t *>(from), static_cast<short>(0), s < stages ? static_cast<int>(bytes) : 0, 0x00020000);
+    const int soff = kCols ? i * 128 : s * 128 + i * 64 * static_cast<int>(stride);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (FP8Q_LDS void *)(panel + wave * 1024), 16, voff, s < stages ? soff : 0, 0, 0);
+  }
+};
+
+// A lane's places in LDS of the fragments first .. first + kCount - 1 (16 rows or columns each) of a region.
+template <bool kCols, int kCount>
+struct Places {
+  uint32_t at[kCols ? kCount : 2];
+  __device__ __forceinline__ explicit Places(int first) {
+    const int l = threadIdx.x & 15, kg = (threadIdx.x & 63) >> 4;
+    if (kCols) {
+      const int k = 8 * kg + (l >> 2);
+#pragma unroll
+      for (int f = 0; f < kCount; ++f) {
+        const int g = first + f, chunk = 2 * (g & 3) + ((l >> 1) & 1);
+        at[f] = (g >> 2) * kPanel + panel_pos(k, chunk ^ (2 * (k & 3))) + 8 * (l & 1);
+      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) at[h] = first * 2048 + panel_pos(l, (kg + 4 * h) ^ (l & 7));
+    }
+  }
+  // x[h][f]: fragment first + f, contracted indices 32 h + 8 (lane / 16) + 0 .. 7, of the region at LDS address
+  // `base`.  In assembly, with their wait: the compiler would wait for every copy in flight.
+  template <int kN>
+  __device__ __forceinline__ void read(v8h (&x)[2][kN], uint32_t base, int first) const {
+    if constexpr (kCols) {
+      v4s r[2][kN][2];
+      if constexpr (kN == 2) {
+        asm volatile(
+            "ds_read_b64_tr_b16 %0, %8 offset:0\n\tds_read_b64_tr_b16 %1, %8 offset:1024\n\t"
+            "ds_read_b64_tr_b16 %2, %9 offset:0\n\tds_read_b64_tr_b16 %3, %9 offset:1024\n\t"
+            "ds_read_b64_tr_b16 %4, %8 offset:4096\n\tds_read_b64_tr_b16 %5, %8 offset:5120\n\t"
+            "ds_read_b64_tr_b16 %6, %9 offset:4096\n\tds_read_b64_tr_b16 %7, %9 offset:5120\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(r[0][0][0]), "=&v"(r[0][0][1]), "=&v"(r[0][1][0]), "=&v"(r[0][1][1]), "=&v"(r[1][0][0]),
+              "=&v"(r[1][0][1]), "=&v"(r[1][1][0]), "=&v"(r[1][1][1])
+            : "v"(base + at[first + 0]), "v"(base + at[first + 1])
+            : "memory");
+      } else if constexpr (kN == 3) {
+        asm volatile(
+            "ds_read_b64_tr_b16 %0, %12 offset:0\n\tds_read_b64_tr_b16 %1, %12 offset:1024\n\t"
+            "ds_read_b64_tr_b16 %2, %13 offset:0\n\tds_read_b64_tr_b16 %3, %13 offset:1024\n\t"
+            "ds_read_b64_tr_b16 %4, %14 offset:0\n\tds_read_b64_tr_b16 %5, %14 offset:1024\n\t"
+            "ds_read_b64_tr_b16 %6, %12 offset:4096\n\tds_read_b64_tr_b16 %7, %12 offset:5120\n\t"
+            "ds_read_b64_tr_b16 %8, %13 offset:4096\n\tds_read_b64_tr_b16 %9, %13 offset:5120\n\t"
+            "ds_read_b64_tr_b16 %10, %14 offset:4096\n\tds_read_b64_tr_b16 %11, %14 offset:5120\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(r[0][0][0]), "=&v"(r[0][0][1]), "=&v"(r[0][1][0]), "=&v"(r[0][1][1]), "=&v"(r[0][2][0]),
+              "=&v"(r[0][2][1]), "=&v"(r[1][0][0]), "=&v"(r[1][0][1]), "=&v"(r[1][1][0]), "=&v"(r[1][1][1]),
+              "=&v"(r[1][2][0]), "=&v"(r[1][2][1])
+            : "v"(base + at[first + 0]), "v"(base + at[first + 1]), "v"(base + at[first + 2])
+            : "memory");
+      } else if constexpr (kN == 4) {
+        asm volatile(
+            "ds_read_b64_tr_b16 %0, %16 offset:0\n\tds_read_b64_tr_b16 %1, %16 offset:1024\n\t"
+            "ds_read_b64_tr_b16 %2, %17 offset:0\n\tds_read_b64_tr_b16 %3, %17 offset:1024\n\t"
+            "ds_read_b64_tr_b16 %4, %18 offset:0\n\tds_read_b64_tr_b16 %5, %18 offset:1024\n\t"
+            "ds_read_b64_tr_b16 %6, %19 offset:0\n\tds_read_b64_tr_b16 %7, %19 offset:1024\n\t"
+            "ds_read_b64_tr_b16 %8, %16 offset:4096\n\tds_read_b64_tr_b16 %9, %16 offset:5120\n\t"
+            "ds_read_b64_tr_b16 %10, %17 offset:4096\n\tds_read_b64_tr_b16 %11, %17 offset:5120\n\t"
+            "ds_read_b64_tr_b16 %12, %18 offset:4096\n\tds_read_b64_tr_b16 %13, %18 offset:5120\n\t"
+            "ds_read_b64_tr_b16 %14, %19 offset:4096\n\tds_read_b64_tr_b16 %15, %19 offset:5120\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(r[0][0][0]), "=&v"(r[0][0][1]), "=&v"(r[0][1][0]), "=&v"(r[0][1][1]), "=&v"(r[0][2][0]),
+              "=&v"(r[0][2][1]), "=&v"(r[0][3][0]), "=&v"(r[0][3][1]), "=&v"(r[1][0][0]), "=&v"(r[1][0][1]),
+              "=&v"(r[1][1][0]), "=&v"(r[1][1][1]), "=&v"(r[1][2][0]), "=&v"(r[1][2][1]), "=&v"(r[1][3][0]),
+              "=&v"(r[1][3][1])
+            : "v"(base + at[first + 0]), "v"(base + at[first + 1]), "v"(base + at[first + 2]),
+              "v"(base + at[first + 3])
+            : "memory");
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int f = 0; f < kN; ++f)
+          x[h][f] = __builtin_bit_cast(v8h, __builtin_shufflevector(r[h][f][0], r[h][f][1], 0, 1, 2, 3, 4, 5, 6, 7));
+    } else {
+      base += first * 2048;
+      if constexpr (kN == 2) {
+        asm volatile(
+            "ds_read_b128 %0, %4 offset:0\n\tds_read_b128 %1, %4 offset:2048\n\t"
+            "ds_read_b128 %2, %5 offset:0\n\tds_read_b128 %3, %5 offset:2048\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(x[0][0]), "=&v"(x[0][1]), "=&v"(x[1][0]), "=&v"(x[1][1])
+            : "v"(base + at[0]), "v"(base + at[1])
+            : "memory");
+      } else if constexpr (kN == 3) {
+        asm volatile(
+            "ds_read_b128 %0, %6 offset:0\n\tds_read_b128 %1, %6 offset:2048\n\t"
+            "ds_read_b128 %2, %6 offset:4096\n\tds_read_b128 %3, %7 offset:0\n\t"
+            "ds_read_b128 %4, %7 offset:2048\n\tds_read_b128 %5, %7 offset:4096\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(x[0][0]), "=&v"(x[0][1]), "=&v"(x[0][2]), "=&v"(x[1][0]), "=&v"(x[1][1]), "=&v"(x[1][2])
+            : "v"(base + at[0]), "v"(base + at[1])
+            : "memory");
+      } else if constexpr (kN == 4) {
+        asm volatile(
+            "ds_read_b128 %0, %8 offset:0\n\tds_read_b128 %1, %8 offset:2048\n\t"
+            "ds_read_b128 %2, %8 offset:4096\n\tds_read_b128 %3, %8 offset:6144\n\t"
+            "ds_read_b128 %4, %9 offset:0\n\tds_read_b128 %5, %9 offset:2048\n\t"
+            "ds_read_b128 %6, %9 offset:4096\n\tds_read_b128 %7, %9 offset:6144\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(x[0][0]), "=&v"(x[0][1]), "=&v"(x[0][2]), "=&v"(x[0][3]), "=&v"(x[1][0]), "=&v"(x[1][1]),
+              "=&v"(x[1][2]), "=&v"(x[1][3])
+            : "v"(base + at[0]), "v"(base + at[1])
+            : "memory");
+      }
+    }
+  }
+};
+
+__device__ __forceinline__ uint32_t lds_address(const uint8_t *p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const FP8Q_LDS uint8_t *)p));
 }
+
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// Waits for the wave's LDS reads, then for the other waves.  Not __syncthreads(), whose fence would wait
+// for the copies in flight.
+__device__ __forceinline__ void meet() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+__device__ __forceinline__ void in_order() { asm volatile("" ::: "memory"); }
 
 template <int kTile>
 struct Tile {
   static constexpr int kM = kTile / 64, kN = kTile / 32;  // fragments of a wave
   v4f acc[kM][kN];
-  int row, col;  // of the lane in the tile: + 16 i, + 16 j (then four columns)
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < kM; ++i)
+#pragma unroll
+      for (int j = 0; j < kN; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  // acc += fragments a times fragments b of columns first .. first + kCount - 1
+  template <int kCount>
+  __device__ __forceinline__ void add(const v8h (&a)[2][kM], const v8h (&b)[2][kCount], int first) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < kCount; ++j)
+#pragma unroll
+        for (int i = 0; i < kM; ++i)
+          acc[i][first + j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b[h][j], a[h][i], acc[i][first + j], 0, 0, 0);
+  }
 };
 
-// acc = rows [p, p + kTile) of P times rows [q, q + kTile) of Q; rows past the end count as zeros.  K % 128 == 0.
-template <int kTile>
-__device__ __forceinline__ void multiply(Tile<kTile> &t, const _Float16 *p, int64_t p_rows, const _Float16 *q,
-                                         int64_t q_rows, int64_t K) {
-  constexpr int kM = Tile<kTile>::kM, kN = Tile<kTile>::kN, kLoads = kTile / 64, kBytes = kTile * 128;
-  __shared__ __attribute__((aligned(1024))) uint8_t p0[kBytes], p1[kBytes], q0[kBytes], q1[kBytes];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave >> 1, wn = wave & 1;
-  const int64_t ld = K * 2;
-  const __amdgpu_buffer_rsrc_t rp = rsrc_of(p, (p_rows < kTile ? p_rows : kTile) * ld);
-  const __amdgpu_buffer_rsrc_t rq = rsrc_of(q, (q_rows < kTile ? q_rows : kTile) * ld);
-  uint32_t off[kLoads];
+// Tiles of 256.  The two waves of a SIMD (w and w + 4) take turns: one multiplies while the other reads
+// fragments from LDS and issues copies; a barrier ends each phase, and waves 0-3 run one phase ahead.  A
+// stage is two of each: M0 reads the row fragments and the first half of the wave's columns (regions p
+// and q0), C0 multiplies them, M1 reads the other half (region q1), C1 multiplies.  Regions are
+// double buffered, 128 KB in all; a region is free two phases after its last read.  In M0 of stage
+// s the copies of q1 of stage s + 1 are issued, in M1 those of p and q0 of stage s + 2, so that a
+// copy has about one and a half stages (3000 cycles) to land.  Each wave waits at the end of its M phases
+// for the copies that the phase after next reads, all but the eight issued last.
+template <bool kPCols, bool kQCols>
+__device__ __forceinline__ void multiply(Tile<256> &t, const Source<kPCols> &p, const Source<kQCols> &q) {
+  __shared__ __attribute__((aligned(1024))) uint8_t p_0[4 * kPanel], p_1[4 * kPanel], q0_0[2 * kPanel], q0_1[2 * kPanel],
+      q1_0[2 * kPanel], q1_1[2 * kPanel];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const bool lead = wave < 4;
+  const Places<kPCols, 4> at_p((wave >> 1) * 4);
+  const Places<kQCols, 4> at_q((wave & 1) * 4);
+  auto copy_first = [&](int s, uint8_t *to_p, uint8_t *to_q) {
 #pragma unroll
-  for (int i = 0; i < kLoads; ++i) {
-    const int b = 8 * i + wave;  // 1 KB block: 4 lines of row group b / 2
-    const int line = 4 * (b & 1) + (lane >> 4);
-    off[i] = static_cast<uint32_t>(16 * (b >> 1) + line + 8 * ((lane >> 3) & 1)) * static_cast<uint32_t>(ld) +
-             (((lane & 7) ^ line) << 4);
-  }
-  auto copy = [&](uint8_t *to_p, uint8_t *to_q, int64_t s) {
+    for (int i = 0; i < 4; ++i) p.copy(s, i, to_p + i * kPanel);
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rp, (FP8Q_LDS void *)(to_p + (8 * i + wave) * 1024), 16,
-                                               static_cast<int>(off[i]), static_cast<int>(s * 128), 0, 0);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rq, (FP8Q_LDS void *)(to_q + (8 * i + wave) * 1024), 16,
-                                               static_cast<int>(off[i]), static_cast<int>(s * 128), 0, 0);
-    }
+    for (int i = 0; i < 2; ++i) q.copy(s, 2 * i, to_q + i * kPanel);
   };
-  const int r = lane & 15, kg = lane >> 4;
-  const int at[2] = {lds_pos(r, kg), lds_pos(r, kg + 4)};
+  auto copy_second = [&](int s, uint8_t *to) {
 #pragma unroll
-  for (int i = 0; i < kM; ++i)
-#pragma unroll
-    for (int j = 0; j < kN; ++j) t.acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-  auto compute = [&](const uint8_t *from_p, const uint8_t *from_q) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      v8h a[kM], b[kN];
-#pragma unroll
-      for (int i = 0; i < kM; ++i) a[i] = *reinterpret_cast<const v8h *>(from_p + (wm * kM + i) * 2048 + at[h]);
-#pragma unroll
-      for (int j = 0; j < kN; ++j) b[j] = *reinterpret_cast<const v8h *>(from_q + (wn * kN + j) * 2048 + at[h]);
-#pragma unroll
-      for (int i = 0; i < kM; ++i)
-#pragma unroll
-        for (int j = 0; j < kN; ++j) t.acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b[j], a[i], t.acc[i][j], 0, 0, 0);
-    }
+    for (int i = 0; i < 2; ++i) q.copy(s, 2 * i + 1, to + i * kPanel);
   };
-  // A wave waits for its own copies, then for the other waves: every copy of the stage has landed and
-  // every wave has read the other buffer, which takes the next stage.
-  auto meet = [&]() {
-    __builtin_amdgcn_sched_barrier(0);
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
-  };
-  const int64_t stages = K / 64;  // even
-  copy(p0, q0, 0);
-  for (int64_t s = 0; s < stages; s += 2) {
+  t.clear();
+  copy_first(0, p_0, q0_0);
+  in_order();
+  copy_second(0, q1_0);
+  in_order();
+  copy_first(1, p_1, q0_1);
+  wait_copies<8>();
+  meet();
+  if (!lead) meet();
+  v8h a[2][4], b[2][4];
+  auto stage = [&](int s, uint8_t *sp, uint8_t *s0, uint8_t *s1, uint8_t *next1) {
+    at_p.read(a, lds_address(sp), 0);
+    at_q.read(b, lds_address(s0), 0);
+    in_order();
+    copy_second(s + 1, next1);
+    wait_copies<8>();
     meet();
-    copy(p1, q1, s + 1);
-    compute(p0, q0);
+    t.add<4>(a, b, 0);
     meet();
-    if (s + 2 < stages) copy(p0, q0, s + 2);
-    compute(p1, q1);
+    at_q.read(b, lds_address(s1), 0);
+    in_order();
+    copy_first(s + 2, sp, s0);
+    wait_copies<8>();
+    meet();
+    t.add<4>(a, b, 4);
+    meet();
+  };
+  for (int s = 0; s < p.stages; s += 2) {  // an even number
+    stage(s, p_0, q0_0, q1_0, q1_1);
+    stage(s + 1, p_1, q0_1, q1_1, q1_0);
   }
-  t.row = wm * (kTile / 4) + r;
-  t.col = wn * (kTile / 2) + kg * 4;
+  if (lead) meet();
+  wait_copies<0>();
 }
 
-// f(i, j) for every fragment of the lane: row t.row + 16 i, columns t.col + 16 j and the three after.
+// Tiles of 192: the same phases with three buffers for whole stages (144 KB).  In M0 of stage s all
+// copies of stage s + 2 are issued, into the buffer that was last read two phases before.
+template <bool kPCols, bool kQCols>
+__device__ __forceinline__ void multiply(Tile<192> &t, const Source<kPCols> &p, const Source<kQCols> &q) {
+  __shared__ __attribute__((aligned(1024))) uint8_t b_0[6 * kPanel], b_1[6 * kPanel], b_2[6 * kPanel];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const bool lead = wave < 4;
+  const Places<kPCols, 3> at_p((wave >> 1) * 3);
+  const Places<kQCols, 6> at_q((wave & 1) * 6);
+  auto copy = [&](int s, uint8_t *to) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) p.copy(s, i, to + i * kPanel);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) q.copy(s, i, to + (3 + i) * kPanel);
+  };
+  t.clear();
+  copy(0, b_0);
+  in_order();
+  copy(1, b_1);
+  wait_copies<6>();
+  meet();
+  if (!lead) meet();
+  v8h a[2][3], b[2][3];
+  auto stage = [&](int s, uint8_t *cur, uint8_t *free) {
+    at_p.read(a, lds_address(cur), 0);
+    at_q.read(b, lds_address(cur + 3 * kPanel), 0);
+    in_order();
+    copy(s + 2, free);
+    meet();
+    t.add<3>(a, b, 0);
+    meet();
+    at_q.read(b, lds_address(cur + 3 * kPanel), 3);
+    wait_copies<6>();
+    meet();
+    t.add<3>(a, b, 3);
+    meet();
+  };
+  for (int s = 0;;) {
+    stage(s, b_0, b_2);
+    if (++s == p.stages) break;
+    stage(s, b_1, b_0);
+    if (++s == p.stages) break;
+    stage(s, b_2, b_1);
+    if (++s == p.stages) break;
+  }
+  if (lead) meet();
+  wait_copies<0>();
+}
+
+// Tiles of 128, for few of them: four buffers, every wave in step, so that three stages are in flight.
+template <bool kPCols, bool kQCols>
+__device__ __forceinline__ void multiply(Tile<128> &t, const Source<kPCols> &p, const Source<kQCols> &q) {
+  __shared__ __attribute__((aligned(1024))) uint8_t b_0[4 * kPanel], b_1[4 * kPanel], b_2[4 * kPanel], b_3[4 * kPanel];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Places<kPCols, 2> at_p((wave >> 1) * 2);
+  const Places<kQCols, 4> at_q((wave & 1) * 4);
+  auto copy = [&](int s, uint8_t *to) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) p.copy(s, i, to + i * kPanel);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) q.copy(s, i, to + (2 + i) * kPanel);
+  };
+  t.clear();
+  copy(0, b_0);
+  in_order();
+  copy(1, b_1);
+  in_order();
+  copy(2, b_2);
+  auto stage = [&](int s, uint8_t *cur, uint8_t *free) {
+    wait_copies<8>();
+    meet();  // the stage has landed, and every wave has read the one before it
+    copy(s + 3, free);
+    v8h a[2][2], b[2][4];
+    at_p.read(a, lds_address(cur), 0);
+    at_q.read(b, lds_address(cur + 2 * kPanel), 0);
+    t.add<4>(a, b, 0);
+  };
+  for (int s = 0;;) {
+    stage(s, b_0, b_3);
+    if (++s == p.stages) break;
+    stage(s, b_1, b_0);
+    if (++s == p.stages) break;
+    stage(s, b_2, b_1);
+    if (++s == p.stages) break;
+    stage(s, b_3, b_2);
+    if (++s == p.stages) break;
+  }
+  wait_copies<0>();
+}
+
+// f(row, column, four values) for every fragment of the lane, in the tile.
 template <int kTile, class F>
 __device__ __forceinline__ void each(const Tile<kTile> &t, F f) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int row = (wave >> 1) * (kTile / 4) + (lane & 15), col = (wave & 1) * (kTile / 2) + (lane >> 4) * 4;
 #pragma unroll
   for (int i = 0; i < Tile<kTile>::kM; ++i)
 #pragma unroll
-    for (int j = 0; j < Tile<kTile>::kN; ++j) f(t.row + 16 * i, t.col + 16 * j, t.acc[i][j]);
+    for (int j = 0; j < Tile<kTile>::kN; ++j) f(row + 16 * i, col + 16 * j, t.acc[i][j]);
 }
 
 // Unit of a workgroup: each XCD (blockIdx % 8) takes a run of neighbouring tiles, which share operands in
@@ -295,34 +590,36 @@ struct Coefficients {
   float a, b, c;
 };
 
-// kSquare false: A = X X^T and its diagonal; true: C = a I + b A + c A^2 from A and its diagonal.  Diagonals are
-// unscaled and FP32, the matrices' own diagonals zero.
-template <int kTile, bool kSquare>
-__global__ __launch_bounds__(kThreads, kTile == 128 ? 4 : 2) void muon_symmetric_kernel(
-    const _Float16 *__restrict__ from, int64_t K, int64_t mp, int G, const float *__restrict__ diagonal_in, Coefficients co,
-    _Float16 *__restrict__ out, float *__restrict__ diagonal) {
-  const int tiles = static_cast<int>((mp + kTile - 1) / kTile), per = tiles * (tiles + 1) / 2;
+// kSquare false: A = X X^T (or X^T X, kCols) and its diagonal; true: C = a I + b A + c A^2 from A and its diagonal.
+// Diagonals are unscaled and FP32, the matrices' own diagonals zero.  m: the size of A.
+template <int kTile, bool kSquare, bool kCols>
+__global__ __launch_bounds__(kThreads, 2) void muon_symmetric_kernel(const _Float16 *__restrict__ from, int64_t ld,
+                                                                     int64_t K, int64_t m, int G,
+                                                                     const float *__restrict__ diagonal_in,
+                                                                     Coefficients co, _Float16 *__restrict__ out,
+                                                                     float *__restrict__ diagonal) {
+  const int tiles = static_cast<int>((m + kTile - 1) / kTile), per = tiles * (tiles + 1) / 2;
   const int64_t unit = unit_of(static_cast<int64_t>(per) * G);
   if (unit >= static_cast<int64_t>(per) * G) return;
   const int g = static_cast<int>(unit / per);
   int ti, tj;
   triangle(static_cast<int>(unit % per), ti, tj);
   const int64_t r0 = static_cast<int64_t>(ti) * kTile, c0 = static_cast<int64_t>(tj) * kTile;
-  const _Float16 *x = from + g * mp * K;
+  const _Float16 *x = from + g * m * K;
   Tile<kTile> t;
-  multiply<kTile>(t, x + r0 * K, mp - r0, x + c0 * K, mp - c0, K);
-  _Float16 *const o = out + g * mp * mp;
-  float *const d = diagonal + g * mp;
-  const float *const d_in = kSquare ? diagonal_in + g * mp : nullptr;
+  multiply(t, Source<kCols>(x, r0, m, kTile, ld, K), Source<kCols>(x, c0, m, kTile, ld, K));
+  _Float16 *const o = out + g * m * m;
+  float *const d = diagonal + g * m;
+  const float *const d_in = kSquare ? diagonal_in + g * m : nullptr;
   each<kTile>(t, [&](int row, int col, v4f v) {
     const int64_t i = r0 + row, j = c0 + col;
-    if (i >= mp || j >= mp) return;
+    if (i >= m || j >= m) return;
     v4h h;
     v4h a = {};
     v4f dj = {};
     float di = 0.0f;
     if (kSquare) {
-      a = *reinterpret_cast<const v4h *>(x + i * mp + j);
+      a = *reinterpret_cast<const v4h *>(x + i * m + j);
       dj = *reinterpret_cast<const v4f *>(d_in + j);
       di = d_in[i];
     }
@@ -339,10 +636,10 @@ __global__ __launch_bounds__(kThreads, kTile == 128 ? 4 : 2) void muon_symmetric
       }
       h[k] = static_cast<_Float16>(s);
     }
-    *reinterpret_cast<v4h *>(o + i * mp + j) = h;
+    *reinterpret_cast<v4h *>(o + i * m + j) = h;
     if (ti != tj) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) o[(j + k) * mp + i] = h[k];
+      for (int k = 0; k < 4; ++k) o[(j + k) * m + i] = h[k];
     }
   });
 }
@@ -365,72 +662,83 @@ __device__ __forceinline__ void raster(int u, int rows, int cols, int &i, int &j
   j = in / height;
 }
 
-// kLast false: X = C X in place and X^T into `hit`; true: the result, [P][Q].
+// X = C X (kTall: the transposed matrix X = X C); kLast: the result, [P][Q], in its place.
 template <int kTile, bool kLast, bool kTall>
-__global__ __launch_bounds__(kThreads, kTile == 128 ? 4 : 2) void muon_apply_kernel(
-    const _Float16 *__restrict__ c, const float *__restrict__ diagonal, const _Float16 *__restrict__ xt, const Matrices x,
-    int G, const Result res) {
-  const int64_t mp = x.mp, np = x.np;
-  const int rows = static_cast<int>((mp + kTile - 1) / kTile), cols = static_cast<int>((np + kTile - 1) / kTile);
+__global__ __launch_bounds__(kThreads, 2) void muon_apply_kernel(const _Float16 *__restrict__ c,
+                                                                 const float *__restrict__ diagonal, const Matrices x,
+                                                                 int G, const Result res) {
+  const int64_t Pp = x.Pp, Qp = x.Qp, m = kTall ? Qp : Pp;
+  const int rows = static_cast<int>((Pp + kTile - 1) / kTile), cols = static_cast<int>((Qp + kTile - 1) / kTile);
   const int64_t per = static_cast<int64_t>(rows) * cols, unit = unit_of(per * G);
   if (unit >= per * G) return;
   const int64_t g = unit / per;
   int ti, tj;
   raster(static_cast<int>(unit % per), rows, cols, ti, tj);
   const int64_t r0 = static_cast<int64_t>(ti) * kTile, c0 = static_cast<int64_t>(tj) * kTile;
+  const _Float16 *const hi = x.hi + g * Pp * Qp, *const cg = c + g * m * m;
   Tile<kTile> t;
-  multiply<kTile>(t, c + g * mp * mp + r0 * mp, mp - r0, xt + g * mp * np + c0 * mp, np - c0, mp);
-  _Float16 *const hi = x.hi + g * mp * np, *const lo = x.lo + g * mp * np, *const hit = x.hit + g * mp * np;
-  const float *const d = diagonal + g * mp;
+  if constexpr (kTall)
+    multiply(t, Source<false>(hi, r0, Pp, kTile, Qp, m), Source<false>(cg, c0, m, kTile, m, m));
+  else
+    multiply(t, Source<false>(cg, r0, m, kTile, m, m), Source<true>(hi, c0, Qp, kTile, Qp, m));
+  uint8_t *const lo = x.lo + g * Pp * Qp;
+  _Float16 *const next = x.next + g * Pp * Qp;
+  const float *const d = diagonal + g * m;
   const float lr = kLast && res.param != nullptr ? (res.lr != nullptr ? *res.lr : res.lr_host) : 0.0f;
   const float keep = 1.0f - lr * res.decay, step = lr * res.scale;
-  const int64_t m = kTall ? res.Q : res.P, n = kTall ? res.P : res.Q;
   each<kTile>(t, [&](int row, int col, v4f v) {
     const int64_t i = r0 + row, j = c0 + col;
-    if (i >= mp || j >= np) return;
-    const v4h h0 = *reinterpret_cast<const v4h *>(hi + i * np + j), l0 = *reinterpret_cast<const v4h *>(lo + i * np + j);
-    const float di = d[i];
+    if (i >= Pp || j >= Qp) return;
+    const v4f old = join(*reinterpret_cast<const v4h *>(hi + i * Qp + j), *reinterpret_cast<const uint32_t *>(lo + i * Qp + j));
+    const v4f by = kTall ? *reinterpret_cast<const v4f *>(d + j) : v4f{d[i], d[i], d[i], d[i]};
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      v[k] = __builtin_fmaf(di, static_cast<float>(h0[k]) + static_cast<float>(l0[k]), v[k] * (1.0f / kScale));
+    for (int k = 0; k < 4; ++k) v[k] = __builtin_fmaf(by[k], old[k], v[k] * (1.0f / kScale));
     if constexpr (!kLast) {
-      v4h h, l;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        _Float16 a, b;
-        split(v[k], a, b);
-        h[k] = a;
-        l[k] = b;
-        hit[(j + k) * mp + i] = a;
-      }
-      *reinterpret_cast<v4h *>(hi + i * np + j) = h;
-      *reinterpret_cast<v4h *>(lo + i * np + j) = l;
+      uint32_t low;
+      *reinterpret_cast<v4h *>(next + i * Qp + j) = split(v, low);
+      *reinterpret_cast<uint32_t *>(lo + i * Qp + j) = low;
     } else {
-      if (i >= m) return;
+      if (i >= res.P) return;
+      const int64_t at = (g * res.P + i) * res.Q + j;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] *= 1.0f / kScale;
+      if ((res.Q & 3) == 0) {
+        if (j >= res.Q) return;
+        if (res.param == nullptr) {
+          *reinterpret_cast<uint2 *>(res.out + at) = make_uint2(pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3]));
+          return;
+        }
+        v4f p = *reinterpret_cast<const v4f *>(res.param + at);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) p[k] = p[k] * keep - step * v[k];
+        *reinterpret_cast<v4f *>(res.param + at) = p;
+        if (res.copy != nullptr)
+          *reinterpret_cast<uint2 *>(res.copy + at) = make_uint2(pack2_bf16(p[0], p[1]), pack2_bf16(p[2], p[3]));
+        return;
+      }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        if (j + k >= n) break;
-        const int64_t at = g * res.P * res.Q + (kTall ? (j + k) * res.Q + i : i * res.Q + j + k);
-        const float o = v[k] * (1.0f / kScale);
+        if (j + k >= res.Q) break;
         if (res.param == nullptr) {
-          res.out[at] = static_cast<uint16_t>(pack2_bf16(o, 0.0f));
+          res.out[at + k] = static_cast<uint16_t>(pack2_bf16(v[k], 0.0f));
         } else {
-          const float p = res.param[at] * keep - step * o;
-          res.param[at] = p;
-          if (res.copy != nullptr) res.copy[at] = static_cast<uint16_t>(pack2_bf16(p, 0.0f));
+          const float p = res.param[at + k] * keep - step * v[k];
+          res.param[at + k] = p;
+          if (res.copy != nullptr) res.copy[at + k] = static_cast<uint16_t>(pack2_bf16(p, 0.0f));
         }
       }
     }
   });
 }
 
-// The workspace: sums of squares, X (hi, lo), X^T twice, A, C and their diagonals.
+// The workspace: sums of squares, X (hi twice, lo), A, C and their diagonals.
 struct Layout {
-  int64_t G, P, Q, mp, np, count;  // count: workgroups that sum a matrix's squares
-  int64_t sums, hi, lo, hit[2], a, c, da, dc, bytes;
+  int64_t G, P, Q, Pp, Qp, m, count;  // count: workgroups that sum a matrix's squares
+  int64_t sums, hi[2], lo, a, c, da, dc, bytes;
   Layout(int64_t G, int64_t P, int64_t Q) : G(G), P(P), Q(Q) {
-    mp = padded(P < Q ? P : Q);
-    np = padded(P < Q ? Q : P);
+    Pp = padded(P);
+    Qp = padded(Q);
+    m = Pp < Qp ? Pp : Qp;
     count = (P * Q + kPerSum - 1) / kPerSum;
     int64_t at = 0;
     auto take = [&](int64_t size) {
@@ -439,14 +747,13 @@ struct Layout {
       return here;
     };
     sums = take(8 * G * count);
-    hi = take(2 * G * mp * np);
-    lo = take(2 * G * mp * np);
-    hit[0] = take(2 * G * mp * np);
-    hit[1] = take(2 * G * mp * np);
-    a = take(2 * G * mp * mp);
-    c = take(2 * G * mp * mp);
-    da = take(4 * G * mp);
-    dc = take(4 * G * mp);
+    hi[0] = take(2 * G * Pp * Qp);
+    hi[1] = take(2 * G * Pp * Qp);
+    lo = take(G * Pp * Qp);
+    a = take(2 * G * m * m);
+    c = take(2 * G * m * m);
+    da = take(4 * G * m);
+    dc = take(4 * G * m);
     bytes = at;
   }
 };
@@ -457,8 +764,7 @@ int tile_for(Units units, int64_t cus) {
   int best = 256;
   double least = 0;
   for (int tile : {256, 192, 128}) {
-    const int64_t at_once = tile == 128 ? 2 * cus : cus;
-    const double rounds = static_cast<double>((units(tile) + at_once - 1) / at_once) * (tile == 128 ? 2 : 1);
+    const double rounds = static_cast<double>((units(tile) + cus - 1) / cus);
     const double time = rounds * tile * tile * (tile == 256 ? 1.0 : tile == 192 ? 1.1 : 1.4);
     if (least == 0 || time < least) {
       least = time;
@@ -484,51 +790,57 @@ hipError_t run(const Layout &w, const Update &u, bool f32, const Coefficients &c
   auto halves = [&](int64_t at) { return reinterpret_cast<_Float16 *>(ws + at); };
   auto floats = [&](int64_t at) { return reinterpret_cast<float *>(ws + at); };
   double *const sums = reinterpret_cast<double *>(ws + w.sums);
-  const bool tall = w.P > w.Q, vector = w.P * w.Q % 8 == 0;
+  const bool tall = w.P > w.Q;
   const int64_t cus = device_cu_count();
   const int G = static_cast<int>(w.G);
-  Matrices x = {halves(w.hi), halves(w.lo), halves(w.hit[0]), w.mp, w.np};
-
+  Matrices x = {nullptr, halves(w.hi[0]), ws + w.lo, w.Pp, w.Qp};
   {
+    const bool vector = w.P * w.Q % 8 == 0;
     const dim3 grid(static_cast<uint32_t>(w.count), static_cast<uint32_t>(G)), block(256);
     auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, u, w.P * w.Q, sums); };
     if (f32)
       vector ? go(muon_momentum_kernel<true, true>) : go(muon_momentum_kernel<true, false>);
     else
       vector ? go(muon_momentum_kernel<false, true>) : go(muon_momentum_kernel<false, false>);
-    const dim3 tiles(static_cast<uint32_t>((tall ? w.mp : w.np) / 64), static_cast<uint32_t>((tall ? w.np : w.mp) / 64),
+    // about 16 rows for each thread: every workgroup adds up the sums first
+    const int64_t bands = (w.Pp + 63) / 64;
+    const dim3 tiles(static_cast<uint32_t>((w.Qp + 255) / 256), static_cast<uint32_t>(bands < 65535 ? bands : 65535),
                      static_cast<uint32_t>(G));
     auto start = [&](auto kernel) {
       hipLaunchKernelGGL(kernel, tiles, block, 0, stream, u, sums, static_cast<int>(w.count), w.P, w.Q, x);
     };
     if (f32)
-      tall ? start(muon_start_kernel<true, true>) : start(muon_start_kernel<true, false>);
+      w.Q % 4 == 0 ? start(muon_start_kernel<true, true>) : start(muon_start_kernel<true, false>);
     else
-      tall ? start(muon_start_kernel<false, true>) : start(muon_start_kernel<false, false>);
+      w.Q % 4 == 0 ? start(muon_start_kernel<false, true>) : start(muon_start_kernel<false, false>);
   }
   auto tiles = [](int64_t size, int tile) { return (size + tile - 1) / tile; };
-  auto triangle_units = [&](int tile) { return w.G * tiles(w.mp, tile) * (tiles(w.mp, tile) + 1) / 2; };
-  auto apply_units = [&](int tile) { return w.G * tiles(w.mp, tile) * tiles(w.np, tile); };
+  auto triangle_units = [&](int tile) { return w.G * tiles(w.m, tile) * (tiles(w.m, tile) + 1) / 2; };
+  auto apply_units = [&](int tile) { return w.G * tiles(w.Pp, tile) * tiles(w.Qp, tile); };
   const int sym = tile_for(triangle_units, cus), app = tile_for(apply_units, cus);
   auto grid_of = [](int64_t units) { return dim3(static_cast<uint32_t>((units + 7) / 8 * 8)); };
   for (int64_t s = 0; s < steps; ++s) {
+    x.hi = halves(w.hi[s & 1]);
+    x.next = halves(w.hi[(s + 1) & 1]);
     with_tile(sym, [&](auto tile) {
       constexpr int kT = decltype(tile)::value;
-      hipLaunchKernelGGL((muon_symmetric_kernel<kT, false>), grid_of(triangle_units(kT)), dim3(kThreads), 0, stream, x.hi,
-                         w.np, w.mp, G, nullptr, co, halves(w.a), floats(w.da));
-      hipLaunchKernelGGL((muon_symmetric_kernel<kT, true>), grid_of(triangle_units(kT)), dim3(kThreads), 0, stream,
-                         halves(w.a), w.mp, w.mp, G, floats(w.da), co, halves(w.c), floats(w.dc));
+      auto go = [&](auto kernel, const _Float16 *from, int64_t ld, int64_t K, const float *d_in, _Float16 *to, float *d) {
+        hipLaunchKernelGGL(kernel, grid_of(triangle_units(kT)), dim3(kThreads), 0, stream, from, ld, K, w.m, G, d_in, co, to,
+                           d);
+      };
+      if (tall)
+        go(muon_symmetric_kernel<kT, false, true>, x.hi, w.Qp, w.Pp, nullptr, halves(w.a), floats(w.da));
+      else
+        go(muon_symmetric_kernel<kT, false, false>, x.hi, w.Qp, w.Qp, nullptr, halves(w.a), floats(w.da));
+      go(muon_symmetric_kernel<kT, true, false>, halves(w.a), w.m, w.m, floats(w.da), halves(w.c), floats(w.dc));
     });
-    const _Float16 *const xt = halves(w.hit[s & 1]);
-    x.hit = halves(w.hit[(s + 1) & 1]);
     with_tile(app, [&](auto tile) {
       constexpr int kT = decltype(tile)::value;
       auto go = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, grid_of(apply_units(kT)), dim3(kThreads), 0, stream, halves(w.c), floats(w.dc), xt, x, G,
-                           res);
+        hipLaunchKernelGGL(kernel, grid_of(apply_units(kT)), dim3(kThreads), 0, stream, halves(w.c), floats(w.dc), x, G, res);
       };
       if (s + 1 < steps)
-        go(muon_apply_kernel<kT, false, false>);
+        tall ? go(muon_apply_kernel<kT, false, true>) : go(muon_apply_kernel<kT, false, false>);
       else
         tall ? go(muon_apply_kernel<kT, true, true>) : go(muon_apply_kernel<kT, true, false>);
     });
@@ -544,10 +856,9 @@ int64_t muon_workspace(int64_t G, int64_t P, int64_t Q) { return Layout(G, P, Q)
 
 bool muon_grids_fit(int64_t G, int64_t P, int64_t Q) {
   const Layout w(G, P, Q);
-  const int64_t rows = (w.mp + 127) / 128, cols = (w.np + 127) / 128;  // the smallest tiles
-  return G <= 65535 && grid_fits(w.count, 256) && (P + 63) / 64 <= 65534 && grid_fits(w.np / 64, 256) &&
-         rows * cols < (int64_t(1) << 30) / G && rows * rows < (int64_t(1) << 30) / G && grid_fits(G * rows * cols, kThreads) &&
-         grid_fits(G * rows * rows, kThreads);
+  const int64_t units = (w.Pp / 128) * (w.Qp / 128);  // the smallest tiles, of which a triangle has fewer
+  return G <= 65535 && grid_fits(w.count, 256) && units < (int64_t(1) << 31) / kThreads &&
+         grid_fits(G * units + 8, kThreads);
 }
 
 hipError_t launch_orthogonalize(const void *x, bool f32, int64_t G, int64_t P, int64_t Q, const fp8q_newton_schulz &ns,

@@ -22,6 +22,11 @@ def half(t):
     return (t * 4096.0).half().double() / 4096.0
 
 
+def low(t):
+    """What is left of X behind FP16, rounded to E4M3 at the kernels' scale."""
+    return (t * (4096.0 * 256)).float().clamp(-448, 448).to(torch.float8_e4m3fn).double() / (4096.0 * 256)
+
+
 def exact(x, steps=5, abc=ABC):
     """From the singular values, which the iteration changes alone."""
     u, s, v = torch.linalg.svd(x.double().cpu(), full_matrices=False)
@@ -43,7 +48,7 @@ def by_products(x, steps=5, abc=ABC, rounded=False):
     r = half if rounded else (lambda t: t)
     for _ in range(steps):
         hi = r(x)
-        x = hi + r(x - hi)
+        x = hi + low(x - hi) if rounded else x
         a = hi @ hi.transpose(-1, -2).contiguous()
         d = a * eye
         o = r(a - d)
