@@ -384,11 +384,19 @@ __device__ __forceinline__ void meet() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
+// LDS that other lanes of the wave have written is read behind this.
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 __device__ __forceinline__ void in_order() { asm volatile("" ::: "memory"); }
 
 template <int kTile>
 struct Tile {
   static constexpr int kM = kTile / 64, kN = kTile / 32;  // fragments of a wave
+  static constexpr int kLds = kTile == 192 ? 18 * kPanel : 16 * kPanel;
   v4f acc[kM][kN];
   __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -418,9 +426,9 @@ struct Tile {
 // copy has about one and a half stages (3000 cycles) to land.  Each wave waits at the end of its M phases
 // for the copies that the phase after next reads, all but the eight issued last.
 template <bool kPCols, bool kQCols>
-__device__ __forceinline__ void multiply(Tile<256> &t, const Source<kPCols> &p, const Source<kQCols> &q) {
-  __shared__ __attribute__((aligned(1024))) uint8_t p_0[4 * kPanel], p_1[4 * kPanel], q0_0[2 * kPanel], q0_1[2 * kPanel],
-      q1_0[2 * kPanel], q1_1[2 * kPanel];
+__device__ __forceinline__ void multiply(Tile<256> &t, const Source<kPCols> &p, const Source<kQCols> &q, uint8_t *lds) {
+  uint8_t *const p_0 = lds, *const p_1 = lds + 4 * kPanel, *const q0_0 = lds + 8 * kPanel, *const q0_1 = lds + 10 * kPanel,
+                 *const q1_0 = lds + 12 * kPanel, *const q1_1 = lds + 14 * kPanel;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const bool lead = wave < 4;
   const Places<kPCols, 4> at_p((wave >> 1) * 4);
@@ -473,8 +481,8 @@ __device__ __forceinline__ void multiply(Tile<256> &t, const Source<kPCols> &p, 
 // Tiles of 192: the same phases with three buffers for whole stages (144 KB).  In M0 of stage s all
 // copies of stage s + 2 are issued, into the buffer that was last read two phases before.
 template <bool kPCols, bool kQCols>
-__device__ __forceinline__ void multiply(Tile<192> &t, const Source<kPCols> &p, const Source<kQCols> &q) {
-  __shared__ __attribute__((aligned(1024))) uint8_t b_0[6 * kPanel], b_1[6 * kPanel], b_2[6 * kPanel];
+__device__ __forceinline__ void multiply(Tile<192> &t, const Source<kPCols> &p, const Source<kQCols> &q, uint8_t *lds) {
+  uint8_t *const b_0 = lds, *const b_1 = lds + 6 * kPanel, *const b_2 = lds + 12 * kPanel;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const bool lead = wave < 4;
   const Places<kPCols, 3> at_p((wave >> 1) * 3);
@@ -521,8 +529,8 @@ __device__ __forceinline__ void multiply(Tile<192> &t, const Source<kPCols> &p, 
 
 // Tiles of 128, for few of them: four buffers, every wave in step, so that three stages are in flight.
 template <bool kPCols, bool kQCols>
-__device__ __forceinline__ void multiply(Tile<128> &t, const Source<kPCols> &p, const Source<kQCols> &q) {
-  __shared__ __attribute__((aligned(1024))) uint8_t b_0[4 * kPanel], b_1[4 * kPanel], b_2[4 * kPanel], b_3[4 * kPanel];
+__device__ __forceinline__ void multiply(Tile<128> &t, const Source<kPCols> &p, const Source<kQCols> &q, uint8_t *lds) {
+  uint8_t *const b_0 = lds, *const b_1 = lds + 4 * kPanel, *const b_2 = lds + 8 * kPanel, *const b_3 = lds + 12 * kPanel;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Places<kPCols, 2> at_p((wave >> 1) * 2);
   const Places<kQCols, 4> at_q((wave & 1) * 4);
@@ -560,15 +568,60 @@ __device__ __forceinline__ void multiply(Tile<128> &t, const Source<kPCols> &p, 
   wait_copies<0>();
 }
 
-// f(row, column, four values) for every fragment of the lane, in the tile.
-template <int kTile, class F>
-__device__ __forceinline__ void each(const Tile<kTile> &t, F f) {
+// The lane's first row and column in the tile; fragment (i, j) is 16 i rows and 16 j columns further.
+template <int kTile>
+__device__ __forceinline__ void lane_place(int &row, int &col) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int row = (wave >> 1) * (kTile / 4) + (lane & 15), col = (wave & 1) * (kTile / 2) + (lane >> 4) * 4;
+  row = (wave >> 1) * (kTile / 4) + (lane & 15);
+  col = (wave & 1) * (kTile / 2) + (lane >> 4) * 4;
+}
+
+// Writes a wave's kTile / 4 x kTile / 2 block of FP16 values (v: its fragments) to out[row][column] and, if `mirror`, to
+// out[column][row], 16 bytes per lane: through LDS, 16 bytes behind each row so that 16 of them use all
+// banks.  r0, c0: the tile's place in out [rows][cols], both multiples of 8, the block's bounds checked by 8.
+template <int kTile>
+__device__ __forceinline__ void store_block(const v4h (&v)[Tile<kTile>::kM][Tile<kTile>::kN], uint8_t *lds, _Float16 *out,
+                                            int64_t r0, int64_t c0, int64_t m, bool mirror) {
+  constexpr int kM = Tile<kTile>::kM, kN = Tile<kTile>::kN, kHalf = (kM + 1) / 2;  // at most two parts of 32 rows
+  constexpr int kRow = kN * 32 + 16;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l = lane & 15, kg = lane >> 4;
+  uint8_t *const mine = lds + wave * (kHalf * 16 * kRow);
+  static_assert(8 * kHalf * 16 * kRow <= Tile<kTile>::kLds, "the blocks fit");
+  r0 += (wave >> 1) * (kTile / 4);
+  c0 += (wave & 1) * (kTile / 2);
 #pragma unroll
-  for (int i = 0; i < Tile<kTile>::kM; ++i)
+  for (int part = 0; part < kM; part += kHalf) {
+    constexpr int kChunks = kN * 2;  // of 16 bytes in a row
+    const int rows = (kM - part < kHalf ? kM - part : kHalf) * 16;
 #pragma unroll
-    for (int j = 0; j < Tile<kTile>::kN; ++j) f(row + 16 * i, col + 16 * j, t.acc[i][j]);
+    for (int i = 0; i < kHalf; ++i)
+      if (part + i < kM)
+#pragma unroll
+        for (int j = 0; j < kN; ++j)
+          *reinterpret_cast<v4h *>(mine + (16 * i + l) * kRow + (16 * j + 4 * kg) * 2) = v[part + i][j];
+    wave_order();
+    for (int n = lane; n < rows * kChunks; n += 64) {
+      const int r = n / kChunks, c = n % kChunks * 8;
+      const int64_t i = r0 + part * 16 + r, j = c0 + c;
+      if (i < m && j < m) *reinterpret_cast<uint4 *>(out + i * m + j) = *reinterpret_cast<const uint4 *>(mine + r * kRow + c * 2);
+    }
+    if (mirror) {
+      // 16 columns by 8 rows for each 16 lanes: lane l gets column l
+      const int blocks = rows / 8;
+      for (int n = kg; n < blocks * kN; n += 4) {
+        const int rb = n % blocks, cb = n / blocks;
+        const uint8_t *const at = mine + (8 * rb + (l >> 2)) * kRow + (16 * cb + 4 * (l & 3)) * 2;
+        const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((FP8Q_LDS v4s *)at);
+        const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((FP8Q_LDS v4s *)(at + 4 * kRow));
+        const int64_t i = r0 + part * 16 + 8 * rb, j = c0 + 16 * cb + l;
+        if (i < m && j < m)
+          *reinterpret_cast<uint4 *>(out + j * m + i) =
+              __builtin_bit_cast(uint4, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+      }
+    }
+    wave_order();
+  }
 }
 
 // Unit of a workgroup: each XCD (blockIdx % 8) takes a run of neighbouring tiles, which share operands in
@@ -606,42 +659,54 @@ __global__ __launch_bounds__(kThreads, 2) void muon_symmetric_kernel(const _Floa
   triangle(static_cast<int>(unit % per), ti, tj);
   const int64_t r0 = static_cast<int64_t>(ti) * kTile, c0 = static_cast<int64_t>(tj) * kTile;
   const _Float16 *x = from + g * m * K;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[Tile<kTile>::kLds];
+  constexpr int kM = Tile<kTile>::kM, kN = Tile<kTile>::kN;
   Tile<kTile> t;
-  multiply(t, Source<kCols>(x, r0, m, kTile, ld, K), Source<kCols>(x, c0, m, kTile, ld, K));
-  _Float16 *const o = out + g * m * m;
+  multiply(t, Source<kCols>(x, r0, m, kTile, ld, K), Source<kCols>(x, c0, m, kTile, ld, K), lds);
   float *const d = diagonal + g * m;
   const float *const d_in = kSquare ? diagonal_in + g * m : nullptr;
-  each<kTile>(t, [&](int row, int col, v4f v) {
-    const int64_t i = r0 + row, j = c0 + col;
-    if (i >= m || j >= m) return;
-    v4h h;
-    v4h a = {};
-    v4f dj = {};
-    float di = 0.0f;
-    if (kSquare) {
-      a = *reinterpret_cast<const v4h *>(x + i * m + j);
-      dj = *reinterpret_cast<const v4f *>(d_in + j);
-      di = d_in[i];
+  int row, col;
+  lane_place<kTile>(row, col);
+  v4h h[kM][kN];
+  v4f dj[kSquare ? kN : 1];
+  if constexpr (kSquare) {  // A's own tile, all of it on its way at once
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+      const int64_t c = c0 + col + 16 * j;
+      dj[j] = c < m ? *reinterpret_cast<const v4f *>(d_in + c) : v4f{};
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      float s = v[k] * (1.0f / kScale);
-      if (i == j + k) {
-        s *= 1.0f / kScale;
-        d[i] = kSquare ? __builtin_fmaf(co.c, __builtin_fmaf(di, di, s), __builtin_fmaf(co.b, di, co.a)) : s;
-        s = 0.0f;
-      } else if (kSquare) {
-        const float e = static_cast<float>(a[k]);
-        s = __builtin_fmaf(co.c, __builtin_fmaf(di + dj[k], e, s), co.b * e);
+    for (int i = 0; i < kM; ++i)
+#pragma unroll
+      for (int j = 0; j < kN; ++j) {
+        const int64_t r = r0 + row + 16 * i, c = c0 + col + 16 * j;
+        h[i][j] = r < m && c < m ? *reinterpret_cast<const v4h *>(x + r * m + c) : v4h{};
       }
-      h[k] = static_cast<_Float16>(s);
-    }
-    *reinterpret_cast<v4h *>(o + i * m + j) = h;
-    if (ti != tj) {
+  }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) o[(j + k) * m + i] = h[k];
+  for (int i = 0; i < kM; ++i) {
+    const int64_t r = r0 + row + 16 * i;
+    const float di = kSquare && r < m ? d_in[r] : 0.0f;
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+      const int64_t c = c0 + col + 16 * j;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float s = t.acc[i][j][k] * (1.0f / kScale);
+        if (r == c + k) {
+          s *= 1.0f / kScale;
+          if (r < m) d[r] = kSquare ? __builtin_fmaf(co.c, __builtin_fmaf(di, di, s), __builtin_fmaf(co.b, di, co.a)) : s;
+          s = 0.0f;
+        } else if constexpr (kSquare) {
+          const float e = static_cast<float>(h[i][j][k]);
+          s = __builtin_fmaf(co.c, __builtin_fmaf(di + dj[j][k], e, s), co.b * e);
+        }
+        h[i][j][k] = static_cast<_Float16>(s);
+      }
     }
-  });
+  }
+  meet();  // every wave's copies are done, and its reads
+  store_block<kTile>(h, lds, out + g * m * m, r0, c0, m, ti != tj);
 }
 
 struct Result {
@@ -652,6 +717,45 @@ struct Result {
   float lr_host, decay, scale;
   int64_t P, Q;
 };
+
+// The parameters at row i, columns j .. j + 3 of matrix g, if there is a step to take and they are aligned.
+__device__ __forceinline__ v4f old_param(const Result &res, int64_t g, int64_t i, int64_t j) {
+  if (res.param == nullptr || (res.Q & 3) != 0 || i >= res.P || j >= res.Q) return v4f{};
+  return *reinterpret_cast<const v4f *>(res.param + (g * res.P + i) * res.Q + j);
+}
+
+// The result there, from kScale X and old_param's.
+__device__ __forceinline__ void finish(const Result &res, int64_t g, int64_t i, int64_t j, v4f v, v4f p, float keep,
+                                       float step) {
+  if (i >= res.P) return;
+  const int64_t at = (g * res.P + i) * res.Q + j;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] *= 1.0f / kScale;
+  if ((res.Q & 3) == 0) {
+    if (j >= res.Q) return;
+    if (res.param == nullptr) {
+      *reinterpret_cast<uint2 *>(res.out + at) = make_uint2(pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3]));
+      return;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) p[k] = p[k] * keep - step * v[k];
+    *reinterpret_cast<v4f *>(res.param + at) = p;
+    if (res.copy != nullptr)
+      *reinterpret_cast<uint2 *>(res.copy + at) = make_uint2(pack2_bf16(p[0], p[1]), pack2_bf16(p[2], p[3]));
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (j + k >= res.Q) break;
+    if (res.param == nullptr) {
+      res.out[at + k] = static_cast<uint16_t>(pack2_bf16(v[k], 0.0f));
+    } else {
+      const float one = res.param[at + k] * keep - step * v[k];
+      res.param[at + k] = one;
+      if (res.copy != nullptr) res.copy[at + k] = static_cast<uint16_t>(pack2_bf16(one, 0.0f));
+    }
+  }
+}
 
 // Tiles of C X.  Raster: 8 tiles of rows at a time, so that an XCD's run reads few panels.
 __device__ __forceinline__ void raster(int u, int rows, int cols, int &i, int &j) {
@@ -676,59 +780,72 @@ __global__ __launch_bounds__(kThreads, 2) void muon_apply_kernel(const _Float16 
   raster(static_cast<int>(unit % per), rows, cols, ti, tj);
   const int64_t r0 = static_cast<int64_t>(ti) * kTile, c0 = static_cast<int64_t>(tj) * kTile;
   const _Float16 *const hi = x.hi + g * Pp * Qp, *const cg = c + g * m * m;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[Tile<kTile>::kLds];
+  constexpr int kM = Tile<kTile>::kM, kN = Tile<kTile>::kN;
   Tile<kTile> t;
   if constexpr (kTall)
-    multiply(t, Source<false>(hi, r0, Pp, kTile, Qp, m), Source<false>(cg, c0, m, kTile, m, m));
+    multiply(t, Source<false>(hi, r0, Pp, kTile, Qp, m), Source<false>(cg, c0, m, kTile, m, m), lds);
   else
-    multiply(t, Source<false>(cg, r0, m, kTile, m, m), Source<true>(hi, c0, Qp, kTile, Qp, m));
+    multiply(t, Source<false>(cg, r0, m, kTile, m, m), Source<true>(hi, c0, Qp, kTile, Qp, m), lds);
   uint8_t *const lo = x.lo + g * Pp * Qp;
   _Float16 *const next = x.next + g * Pp * Qp;
   const float *const d = diagonal + g * m;
   const float lr = kLast && res.param != nullptr ? (res.lr != nullptr ? *res.lr : res.lr_host) : 0.0f;
   const float keep = 1.0f - lr * res.decay, step = lr * res.scale;
-  each<kTile>(t, [&](int row, int col, v4f v) {
-    const int64_t i = r0 + row, j = c0 + col;
-    if (i >= Pp || j >= Qp) return;
-    const v4f old = join(*reinterpret_cast<const v4h *>(hi + i * Qp + j), *reinterpret_cast<const uint32_t *>(lo + i * Qp + j));
-    const v4f by = kTall ? *reinterpret_cast<const v4f *>(d + j) : v4f{d[i], d[i], d[i], d[i]};
+  int row, col;
+  lane_place<kTile>(row, col);
+  // The old X of a row of fragments is on its way while the row before it is worked on.
+  v4h h[2][kN];
+  uint32_t l[2][kN];
+  auto load = [&](int i) {
+    const int64_t r = r0 + row + 16 * i;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = __builtin_fmaf(by[k], old[k], v[k] * (1.0f / kScale));
-    if constexpr (!kLast) {
-      uint32_t low;
-      *reinterpret_cast<v4h *>(next + i * Qp + j) = split(v, low);
-      *reinterpret_cast<uint32_t *>(lo + i * Qp + j) = low;
-    } else {
-      if (i >= res.P) return;
-      const int64_t at = (g * res.P + i) * res.Q + j;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] *= 1.0f / kScale;
-      if ((res.Q & 3) == 0) {
-        if (j >= res.Q) return;
-        if (res.param == nullptr) {
-          *reinterpret_cast<uint2 *>(res.out + at) = make_uint2(pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3]));
-          return;
-        }
-        v4f p = *reinterpret_cast<const v4f *>(res.param + at);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) p[k] = p[k] * keep - step * v[k];
-        *reinterpret_cast<v4f *>(res.param + at) = p;
-        if (res.copy != nullptr)
-          *reinterpret_cast<uint2 *>(res.copy + at) = make_uint2(pack2_bf16(p[0], p[1]), pack2_bf16(p[2], p[3]));
-        return;
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (j + k >= res.Q) break;
-        if (res.param == nullptr) {
-          res.out[at + k] = static_cast<uint16_t>(pack2_bf16(v[k], 0.0f));
-        } else {
-          const float p = res.param[at + k] * keep - step * v[k];
-          res.param[at + k] = p;
-          if (res.copy != nullptr) res.copy[at + k] = static_cast<uint16_t>(pack2_bf16(p, 0.0f));
-        }
+    for (int j = 0; j < kN; ++j) {
+      const int64_t c = c0 + col + 16 * j;
+      h[i & 1][j] = v4h{};
+      l[i & 1][j] = 0;
+      if (r < Pp && c < Qp) {
+        h[i & 1][j] = *reinterpret_cast<const v4h *>(hi + r * Qp + c);
+        l[i & 1][j] = *reinterpret_cast<const uint32_t *>(lo + r * Qp + c);
       }
     }
-  });
+  };
+  v4f d_col[kTall ? kN : 1];
+  if constexpr (kTall)
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+      const int64_t c = c0 + col + 16 * j;
+      d_col[j] = c < Qp ? *reinterpret_cast<const v4f *>(d + c) : v4f{};
+    }
+  load(0);
+#pragma unroll
+  for (int i = 0; i < kM; ++i) {
+    const int64_t r = r0 + row + 16 * i;
+    v4f p[kLast ? kN : 1];
+    if constexpr (kLast)
+#pragma unroll
+      for (int j = 0; j < kN; ++j) p[j] = old_param(res, g, r, c0 + col + 16 * j);
+    if (i + 1 < kM) load(i + 1);
+    __builtin_amdgcn_sched_barrier(0);
+    const float dr = !kTall && r < Pp ? d[r] : 0.0f;
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+      const int64_t c = c0 + col + 16 * j;
+      if (r >= Pp || c >= Qp) continue;
+      const v4f old = join(h[i & 1][j], l[i & 1][j]);
+      const v4f by = kTall ? d_col[kTall ? j : 0] : v4f{dr, dr, dr, dr};
+      v4f v;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = __builtin_fmaf(by[k], old[k], t.acc[i][j][k] * (1.0f / kScale));
+      if constexpr (!kLast) {
+        uint32_t low;
+        *reinterpret_cast<v4h *>(next + r * Qp + c) = split(v, low);
+        *reinterpret_cast<uint32_t *>(lo + r * Qp + c) = low;
+      } else {
+        finish(res, g, r, c, v, p[kLast ? j : 0], keep, step);
+      }
+    }
+  }
 }
 
 // The workspace: sums of squares, X (hi twice, lo), A, C and their diagonals.
