@@ -147,14 +147,11 @@ __device__ __forceinline__ v4h split(v4f v, uint32_t &lo) {
   return hi;
 }
 
-__device__ __forceinline__ v4f join(v4h hi, uint32_t lo) {
+// lo at hi's scale.
+__device__ __forceinline__ v4f low_of(uint32_t lo) {
   const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(lo), false);
   const f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(lo), true);
-  const float rest[4] = {a.x, a.y, b.x, b.y};
-  v4f v;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) v[k] = __builtin_fmaf(rest[k], 1.0f / kLow, static_cast<float>(hi[k]));
-  return v;
+  return v4f{a.x, a.y, b.x, b.y} * (1.0f / kLow);
 }
 
 // Workgroup (x, y, z): 4 rows of 256 columns of matrix z, and every gridDim.y-th four after them.
@@ -578,10 +575,11 @@ __device__ __forceinline__ void lane_place(int &row, int &col) {
 
 // Writes a wave's kTile / 4 x kTile / 2 block of FP16 values (v: its fragments) to out[row][column] and, if `mirror`, to
 // out[column][row], 16 bytes per lane: through LDS, 16 bytes behind each row so that 16 of them use all
-// banks.  r0, c0: the tile's place in out [rows][cols], both multiples of 8, the block's bounds checked by 8.
+// banks.  r0, c0: the tile's place in out, whose sizes are multiples of 8.
 template <int kTile>
 __device__ __forceinline__ void store_block(const v4h (&v)[Tile<kTile>::kM][Tile<kTile>::kN], uint8_t *lds, _Float16 *out,
-                                            int64_t r0, int64_t c0, int64_t m, bool mirror) {
+                                            int64_t r0, int64_t c0, int64_t rows_end, int64_t cols_end, int64_t ld,
+                                            bool mirror) {
   constexpr int kM = Tile<kTile>::kM, kN = Tile<kTile>::kN, kHalf = (kM + 1) / 2;  // at most two parts of 32 rows
   constexpr int kRow = kN * 32 + 16;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -604,7 +602,8 @@ __device__ __forceinline__ void store_block(const v4h (&v)[Tile<kTile>::kM][Tile
     for (int n = lane; n < rows * kChunks; n += 64) {
       const int r = n / kChunks, c = n % kChunks * 8;
       const int64_t i = r0 + part * 16 + r, j = c0 + c;
-      if (i < m && j < m) *reinterpret_cast<uint4 *>(out + i * m + j) = *reinterpret_cast<const uint4 *>(mine + r * kRow + c * 2);
+      if (i < rows_end && j < cols_end)
+        *reinterpret_cast<uint4 *>(out + i * ld + j) = *reinterpret_cast<const uint4 *>(mine + r * kRow + c * 2);
     }
     if (mirror) {
       // 16 columns by 8 rows for each 16 lanes: lane l gets column l
@@ -615,8 +614,8 @@ __device__ __forceinline__ void store_block(const v4h (&v)[Tile<kTile>::kM][Tile
         const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((FP8Q_LDS v4s *)at);
         const v4s y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((FP8Q_LDS v4s *)(at + 4 * kRow));
         const int64_t i = r0 + part * 16 + 8 * rb, j = c0 + 16 * cb + l;
-        if (i < m && j < m)
-          *reinterpret_cast<uint4 *>(out + j * m + i) =
+        if (i < rows_end && j < cols_end)
+          *reinterpret_cast<uint4 *>(out + j * ld + i) =
               __builtin_bit_cast(uint4, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
       }
     }
@@ -643,14 +642,16 @@ struct Coefficients {
   float a, b, c;
 };
 
-// kSquare false: A = X X^T (or X^T X, kCols) and its diagonal; true: C = a I + b A + c A^2 from A and its diagonal.
-// Diagonals are unscaled and FP32, the matrices' own diagonals zero.  m: the size of A.
+// kSquare false: A = X X^T (or X^T X, kCols), its own diagonal zero, and the diagonal in FP32.  true: C = a I + b A +
+// c A^2 from these, its diagonal rounded to FP16 like the rest, and for each row the diagonal d in FP32
+// and its quotient by the rounded one, {d, d / rounded}.  m: the size of A.
 template <int kTile, bool kSquare, bool kCols>
 __global__ __launch_bounds__(kThreads, 2) void muon_symmetric_kernel(const _Float16 *__restrict__ from, int64_t ld,
                                                                      int64_t K, int64_t m, int G,
                                                                      const float *__restrict__ diagonal_in,
                                                                      Coefficients co, _Float16 *__restrict__ out,
-                                                                     float *__restrict__ diagonal) {
+                                                                     float *__restrict__ diagonal,
+                                                                     float2 *__restrict__ pairs) {
   const int tiles = static_cast<int>((m + kTile - 1) / kTile), per = tiles * (tiles + 1) / 2;
   const int64_t unit = unit_of(static_cast<int64_t>(per) * G);
   if (unit >= static_cast<int64_t>(per) * G) return;
@@ -663,7 +664,6 @@ __global__ __launch_bounds__(kThreads, 2) void muon_symmetric_kernel(const _Floa
   constexpr int kM = Tile<kTile>::kM, kN = Tile<kTile>::kN;
   Tile<kTile> t;
   multiply(t, Source<kCols>(x, r0, m, kTile, ld, K), Source<kCols>(x, c0, m, kTile, ld, K), lds);
-  float *const d = diagonal + g * m;
   const float *const d_in = kSquare ? diagonal_in + g * m : nullptr;
   int row, col;
   lane_place<kTile>(row, col);
@@ -695,8 +695,16 @@ __global__ __launch_bounds__(kThreads, 2) void muon_symmetric_kernel(const _Floa
         float s = t.acc[i][j][k] * (1.0f / kScale);
         if (r == c + k) {
           s *= 1.0f / kScale;
-          if (r < m) d[r] = kSquare ? __builtin_fmaf(co.c, __builtin_fmaf(di, di, s), __builtin_fmaf(co.b, di, co.a)) : s;
-          s = 0.0f;
+          if constexpr (kSquare) {
+            const float d = __builtin_fmaf(co.c, __builtin_fmaf(di, di, s), __builtin_fmaf(co.b, di, co.a));
+            s = d * kScale;
+            const float rounded = static_cast<float>(static_cast<_Float16>(s));
+            // below 2^-13 FP16 has fewer bits, and what they lose is nothing beside the other rows
+            if (r < m) pairs[g * m + r] = make_float2(d, fabsf(rounded) >= 0x1p-13f ? s / rounded : 1.0f);
+          } else {
+            if (r < m) diagonal[g * m + r] = s;
+            s = 0.0f;
+          }
         } else if constexpr (kSquare) {
           const float e = static_cast<float>(h[i][j][k]);
           s = __builtin_fmaf(co.c, __builtin_fmaf(di + dj[j][k], e, s), co.b * e);
@@ -706,7 +714,7 @@ __global__ __launch_bounds__(kThreads, 2) void muon_symmetric_kernel(const _Floa
     }
   }
   meet();  // every wave's copies are done, and its reads
-  store_block<kTile>(h, lds, out + g * m * m, r0, c0, m, ti != tj);
+  store_block<kTile>(h, lds, out + g * m * m, r0, c0, m, m, m, ti != tj);
 }
 
 struct Result {
@@ -766,10 +774,13 @@ __device__ __forceinline__ void raster(int u, int rows, int cols, int &i, int &j
   j = in / height;
 }
 
-// X = C X (kTall: the transposed matrix X = X C); kLast: the result, [P][Q], in its place.
+// X = C X (kTall: the transposed matrix X = X C) from the products with hi; kLast: the result, [P][Q], in its place.
+// With C's diagonal d rounded to dh in the product, row i (tall: column j) of it is multiplied by d / dh, which
+// makes dh hi exact and is within the rounding of what is off the diagonal, and d lo is added: hi is not
+// read again.
 template <int kTile, bool kLast, bool kTall>
 __global__ __launch_bounds__(kThreads, 2) void muon_apply_kernel(const _Float16 *__restrict__ c,
-                                                                 const float *__restrict__ diagonal, const Matrices x,
+                                                                 const float2 *__restrict__ pairs, const Matrices x,
                                                                  int G, const Result res) {
   const int64_t Pp = x.Pp, Qp = x.Qp, m = kTall ? Qp : Pp;
   const int rows = static_cast<int>((Pp + kTile - 1) / kTile), cols = static_cast<int>((Qp + kTile - 1) / kTile);
@@ -789,62 +800,78 @@ __global__ __launch_bounds__(kThreads, 2) void muon_apply_kernel(const _Float16 
     multiply(t, Source<false>(cg, r0, m, kTile, m, m), Source<true>(hi, c0, Qp, kTile, Qp, m), lds);
   uint8_t *const lo = x.lo + g * Pp * Qp;
   _Float16 *const next = x.next + g * Pp * Qp;
-  const float *const d = diagonal + g * m;
+  const float2 *const d = pairs + g * m;
   const float lr = kLast && res.param != nullptr ? (res.lr != nullptr ? *res.lr : res.lr_host) : 0.0f;
   const float keep = 1.0f - lr * res.decay, step = lr * res.scale;
   int row, col;
   lane_place<kTile>(row, col);
-  // The old X of a row of fragments is on its way while the row before it is worked on.
-  v4h h[2][kN];
-  uint32_t l[2][kN];
-  auto load = [&](int i) {
-    const int64_t r = r0 + row + 16 * i;
+  uint32_t low[kM][kN];
+#pragma unroll
+  for (int i = 0; i < kM; ++i)
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+      const int64_t r = r0 + row + 16 * i, c = c0 + col + 16 * j;
+      low[i][j] = r < Pp && c < Qp ? *reinterpret_cast<const uint32_t *>(lo + r * Qp + c) : 0u;
+    }
+  float2 d_row[kM];
+  if constexpr (!kTall)
+#pragma unroll
+    for (int i = 0; i < kM; ++i) d_row[i] = r0 + row + 16 * i < Pp ? d[r0 + row + 16 * i] : make_float2(0.0f, 0.0f);
+  __builtin_amdgcn_sched_barrier(0);
+  v4h h[kLast ? 1 : kM][kLast ? 1 : kN];
+  if constexpr (kTall) {  // columns' factors, four at a time for all rows
 #pragma unroll
     for (int j = 0; j < kN; ++j) {
       const int64_t c = c0 + col + 16 * j;
-      h[i & 1][j] = v4h{};
-      l[i & 1][j] = 0;
-      if (r < Pp && c < Qp) {
-        h[i & 1][j] = *reinterpret_cast<const v4h *>(hi + r * Qp + c);
-        l[i & 1][j] = *reinterpret_cast<const uint32_t *>(lo + r * Qp + c);
+      v4f d01 = {}, d23 = {};
+      if (c < Qp) {
+        d01 = *reinterpret_cast<const v4f *>(d + c);
+        d23 = *reinterpret_cast<const v4f *>(d + c + 2);
+      }
+      const v4f by = {d01[0], d01[2], d23[0], d23[2]}, turn = {d01[1], d01[3], d23[1], d23[3]};
+#pragma unroll
+      for (int i = 0; i < kM; ++i) {
+        const v4f rest = low_of(low[i][j]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          t.acc[i][j][k] = __builtin_fmaf(by[k], rest[k], t.acc[i][j][k] * (turn[k] * (1.0f / kScale)));
       }
     }
-  };
-  v4f d_col[kTall ? kN : 1];
-  if constexpr (kTall)
+  } else {
 #pragma unroll
-    for (int j = 0; j < kN; ++j) {
-      const int64_t c = c0 + col + 16 * j;
-      d_col[j] = c < Qp ? *reinterpret_cast<const v4f *>(d + c) : v4f{};
-    }
-  load(0);
+    for (int i = 0; i < kM; ++i)
+#pragma unroll
+      for (int j = 0; j < kN; ++j) {
+        const v4f rest = low_of(low[i][j]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          t.acc[i][j][k] = __builtin_fmaf(d_row[i].x, rest[k], t.acc[i][j][k] * (d_row[i].y * (1.0f / kScale)));
+      }
+  }
 #pragma unroll
   for (int i = 0; i < kM; ++i) {
     const int64_t r = r0 + row + 16 * i;
     v4f p[kLast ? kN : 1];
-    if constexpr (kLast)
+    if constexpr (kLast) {
 #pragma unroll
       for (int j = 0; j < kN; ++j) p[j] = old_param(res, g, r, c0 + col + 16 * j);
-    if (i + 1 < kM) load(i + 1);
-    __builtin_amdgcn_sched_barrier(0);
-    const float dr = !kTall && r < Pp ? d[r] : 0.0f;
+      __builtin_amdgcn_sched_barrier(0);
+    }
 #pragma unroll
     for (int j = 0; j < kN; ++j) {
       const int64_t c = c0 + col + 16 * j;
-      if (r >= Pp || c >= Qp) continue;
-      const v4f old = join(h[i & 1][j], l[i & 1][j]);
-      const v4f by = kTall ? d_col[kTall ? j : 0] : v4f{dr, dr, dr, dr};
-      v4f v;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = __builtin_fmaf(by[k], old[k], t.acc[i][j][k] * (1.0f / kScale));
       if constexpr (!kLast) {
-        uint32_t low;
-        *reinterpret_cast<v4h *>(next + r * Qp + c) = split(v, low);
-        *reinterpret_cast<uint32_t *>(lo + r * Qp + c) = low;
-      } else {
-        finish(res, g, r, c, v, p[kLast ? j : 0], keep, step);
+        uint32_t rest;
+        h[i][j] = split(t.acc[i][j], rest);
+        if (r < Pp && c < Qp) *reinterpret_cast<uint32_t *>(lo + r * Qp + c) = rest;
+      } else if (r < Pp && c < Qp) {
+        finish(res, g, r, c, t.acc[i][j], p[kLast ? j : 0], keep, step);
       }
     }
+  }
+  if constexpr (!kLast) {
+    meet();  // every wave's copies are done, and its reads
+    store_block<kTile>(h, lds, next, r0, c0, Pp, Qp, Qp, false);
   }
 }
 
@@ -870,7 +897,7 @@ struct Layout {
     a = take(2 * G * m * m);
     c = take(2 * G * m * m);
     da = take(4 * G * m);
-    dc = take(4 * G * m);
+    dc = take(8 * G * m);
     bytes = at;
   }
 };
@@ -941,20 +968,21 @@ hipError_t run(const Layout &w, const Update &u, bool f32, const Coefficients &c
     x.next = halves(w.hi[(s + 1) & 1]);
     with_tile(sym, [&](auto tile) {
       constexpr int kT = decltype(tile)::value;
-      auto go = [&](auto kernel, const _Float16 *from, int64_t ld, int64_t K, const float *d_in, _Float16 *to, float *d) {
+      auto go = [&](auto kernel, const _Float16 *from, int64_t ld, int64_t K, const float *d_in, _Float16 *to) {
         hipLaunchKernelGGL(kernel, grid_of(triangle_units(kT)), dim3(kThreads), 0, stream, from, ld, K, w.m, G, d_in, co, to,
-                           d);
+                           floats(w.da), reinterpret_cast<float2 *>(ws + w.dc));
       };
       if (tall)
-        go(muon_symmetric_kernel<kT, false, true>, x.hi, w.Qp, w.Pp, nullptr, halves(w.a), floats(w.da));
+        go(muon_symmetric_kernel<kT, false, true>, x.hi, w.Qp, w.Pp, nullptr, halves(w.a));
       else
-        go(muon_symmetric_kernel<kT, false, false>, x.hi, w.Qp, w.Qp, nullptr, halves(w.a), floats(w.da));
-      go(muon_symmetric_kernel<kT, true, false>, halves(w.a), w.m, w.m, floats(w.da), halves(w.c), floats(w.dc));
+        go(muon_symmetric_kernel<kT, false, false>, x.hi, w.Qp, w.Qp, nullptr, halves(w.a));
+      go(muon_symmetric_kernel<kT, true, false>, halves(w.a), w.m, w.m, floats(w.da), halves(w.c));
     });
     with_tile(app, [&](auto tile) {
       constexpr int kT = decltype(tile)::value;
       auto go = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, grid_of(apply_units(kT)), dim3(kThreads), 0, stream, halves(w.c), floats(w.dc), x, G, res);
+        hipLaunchKernelGGL(kernel, grid_of(apply_units(kT)), dim3(kThreads), 0, stream, halves(w.c),
+                           reinterpret_cast<const float2 *>(ws + w.dc), x, G, res);
       };
       if (s + 1 < steps)
         tall ? go(muon_apply_kernel<kT, false, true>) : go(muon_apply_kernel<kT, false, false>);

@@ -48,13 +48,15 @@ def by_products(x, steps=5, abc=ABC, rounded=False):
     r = half if rounded else (lambda t: t)
     for _ in range(steps):
         hi = r(x)
-        x = hi + low(x - hi) if rounded else x
+        lo = low(x - hi) if rounded else x - hi
         a = hi @ hi.transpose(-1, -2).contiguous()
         d = a * eye
         o = r(a - d)
         c = abc[0] * eye + abc[1] * (o + d) + abc[2] * ((o + d) @ (o + d))
-        dc = c * eye
-        x = dc @ x + r(c - dc) @ hi
+        dc = c.diagonal(dim1=-2, dim2=-1)[..., None]
+        dh = r(dc)
+        turn = torch.where(dh.abs() * 4096 >= 2.0 ** -13, dc / dh, 1.0)
+        x = turn * ((r(c - dc * eye) + dh * eye) @ hi) + dc * lo
     return x
 
 

@@ -65,8 +65,8 @@ def test_workspace():
     size = fq.load_library().fp8q_muon_workspace
     assert size(1, 0, 5) == 0
     assert size(1, 300, 1000) == size(1, 1000, 300)
-    # X in FP16 twice and its E4M3 rests, two square matrices, two diagonals and the sums, each rounded up to 256 bytes
-    assert size(3, 128, 256) == 3 * (5 * 128 * 256 + 4 * 128 * 128) + 2 * 3 * 4 * 128 + 256
+    # X in FP16 twice and its E4M3 rests, two square matrices, a diagonal, pairs and the sums, each rounded up to 256 bytes
+    assert size(3, 128, 256) == 3 * (5 * 128 * 256 + 4 * 128 * 128) + 3 * 12 * 128 + 256
 
 
 def test_binding_refuses_cpu_tensors():
