@@ -134,6 +134,12 @@ struct Matrices {
 
 constexpr float kLow = 256.0f;
 
+// lo lies as a product's lanes take it: in 64 columns of a row, the four neighbours 16 j + 4 g .. + 3 at 16 g + 4 j, so
+// that the 16 bytes at 16 g are those of one lane in four fragments.
+__device__ __forceinline__ int64_t low_place(int64_t c) {
+  return (c & ~int64_t(63)) + 16 * ((c >> 2) & 3) + 4 * ((c >> 4) & 3);
+}
+
 // Four values as hi and lo.
 __device__ __forceinline__ v4h split(v4f v, uint32_t &lo) {
   v4h hi;
@@ -193,9 +199,9 @@ __global__ __launch_bounds__(256) void muon_start_kernel(const Update u, const d
     }
     uint32_t lo;
     const v4h hi = split(v, lo);
-    const int64_t to = (blockIdx.z * x.Pp + r) * x.Qp + c;
-    *reinterpret_cast<v4h *>(x.next + to) = hi;
-    *reinterpret_cast<uint32_t *>(x.lo + to) = lo;
+    const int64_t to = (blockIdx.z * x.Pp + r) * x.Qp;
+    *reinterpret_cast<v4h *>(x.next + to + c) = hi;
+    *reinterpret_cast<uint32_t *>(x.lo + to + low_place(c)) = lo;
   }
 }
 
@@ -794,25 +800,30 @@ __global__ __launch_bounds__(kThreads, 2) void muon_apply_kernel(const _Float16 
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Tile<kTile>::kLds];
   constexpr int kM = Tile<kTile>::kM, kN = Tile<kTile>::kN;
   Tile<kTile> t;
+  uint8_t *const lo = x.lo + g * Pp * Qp;
+  _Float16 *const next = x.next + g * Pp * Qp;
+  const float2 *const d = pairs + g * m;
+  int row, col;
+  lane_place<kTile>(row, col);
+  // The lane's part of lo: kWide fragments of a row at a time.  Read before the products, which hide it.
+  constexpr int kWide = kN % 4 == 0 ? 4 : 2;
+  typedef uint32_t Low __attribute__((ext_vector_type(kWide)));
+  auto low_at = [&](int i, int j) {
+    return reinterpret_cast<Low *>(lo + (r0 + row + 16 * i) * Qp + low_place(c0 + col + 16 * j));
+  };
+  auto inside = [&](int i, int j) { return r0 + row + 16 * i < Pp && c0 + col + 16 * j < Qp; };
+  Low low[kM][kN / kWide];
+#pragma unroll
+  for (int i = 0; i < kM; ++i)
+#pragma unroll
+    for (int j = 0; j < kN; j += kWide) low[i][j / kWide] = inside(i, j) ? *low_at(i, j) : Low{};
+  in_order();
   if constexpr (kTall)
     multiply(t, Source<false>(hi, r0, Pp, kTile, Qp, m), Source<false>(cg, c0, m, kTile, m, m), lds);
   else
     multiply(t, Source<false>(cg, r0, m, kTile, m, m), Source<true>(hi, c0, Qp, kTile, Qp, m), lds);
-  uint8_t *const lo = x.lo + g * Pp * Qp;
-  _Float16 *const next = x.next + g * Pp * Qp;
-  const float2 *const d = pairs + g * m;
   const float lr = kLast && res.param != nullptr ? (res.lr != nullptr ? *res.lr : res.lr_host) : 0.0f;
   const float keep = 1.0f - lr * res.decay, step = lr * res.scale;
-  int row, col;
-  lane_place<kTile>(row, col);
-  uint32_t low[kM][kN];
-#pragma unroll
-  for (int i = 0; i < kM; ++i)
-#pragma unroll
-    for (int j = 0; j < kN; ++j) {
-      const int64_t r = r0 + row + 16 * i, c = c0 + col + 16 * j;
-      low[i][j] = r < Pp && c < Qp ? *reinterpret_cast<const uint32_t *>(lo + r * Qp + c) : 0u;
-    }
   float2 d_row[kM];
   if constexpr (!kTall)
 #pragma unroll
@@ -831,7 +842,7 @@ __global__ __launch_bounds__(kThreads, 2) void muon_apply_kernel(const _Float16 
       const v4f by = {d01[0], d01[2], d23[0], d23[2]}, turn = {d01[1], d01[3], d23[1], d23[3]};
 #pragma unroll
       for (int i = 0; i < kM; ++i) {
-        const v4f rest = low_of(low[i][j]);
+        const v4f rest = low_of(low[i][j / kWide][j % kWide]);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           t.acc[i][j][k] = __builtin_fmaf(by[k], rest[k], t.acc[i][j][k] * (turn[k] * (1.0f / kScale)));
@@ -842,7 +853,7 @@ __global__ __launch_bounds__(kThreads, 2) void muon_apply_kernel(const _Float16 
     for (int i = 0; i < kM; ++i)
 #pragma unroll
       for (int j = 0; j < kN; ++j) {
-        const v4f rest = low_of(low[i][j]);
+        const v4f rest = low_of(low[i][j / kWide][j % kWide]);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           t.acc[i][j][k] = __builtin_fmaf(d_row[i].x, rest[k], t.acc[i][j][k] * (d_row[i].y * (1.0f / kScale)));
@@ -850,22 +861,25 @@ __global__ __launch_bounds__(kThreads, 2) void muon_apply_kernel(const _Float16 
   }
 #pragma unroll
   for (int i = 0; i < kM; ++i) {
-    const int64_t r = r0 + row + 16 * i;
-    v4f p[kLast ? kN : 1];
     if constexpr (kLast) {
+      v4f p[kN];
 #pragma unroll
-      for (int j = 0; j < kN; ++j) p[j] = old_param(res, g, r, c0 + col + 16 * j);
+      for (int j = 0; j < kN; ++j) p[j] = old_param(res, g, r0 + row + 16 * i, c0 + col + 16 * j);
       __builtin_amdgcn_sched_barrier(0);
-    }
 #pragma unroll
-    for (int j = 0; j < kN; ++j) {
-      const int64_t c = c0 + col + 16 * j;
-      if constexpr (!kLast) {
-        uint32_t rest;
-        h[i][j] = split(t.acc[i][j], rest);
-        if (r < Pp && c < Qp) *reinterpret_cast<uint32_t *>(lo + r * Qp + c) = rest;
-      } else if (r < Pp && c < Qp) {
-        finish(res, g, r, c, t.acc[i][j], p[kLast ? j : 0], keep, step);
+      for (int j = 0; j < kN; ++j)
+        if (inside(i, j)) finish(res, g, r0 + row + 16 * i, c0 + col + 16 * j, t.acc[i][j], p[j], keep, step);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kN; j += kWide) {
+        Low rest;
+#pragma unroll
+        for (int k = 0; k < kWide; ++k) {
+          uint32_t one;
+          h[i][j + k] = split(t.acc[i][j + k], one);
+          rest[k] = one;
+        }
+        if (inside(i, j)) *low_at(i, j) = rest;
       }
     }
   }
