@@ -160,7 +160,7 @@ __device__ __forceinline__ v4f low_of(uint32_t lo) {
   return v4f{a.x, a.y, b.x, b.y} * (1.0f / kLow);
 }
 
-// Workgroup (x, y, z): 4 rows of 256 columns of matrix z, and every gridDim.y-th four after them.
+// Workgroup (x, y, z): 16 rows of 256 columns of matrix z, and every gridDim.y-th 16 after them.
 template <bool kF32, bool kVector>
 __global__ __launch_bounds__(256) void muon_start_kernel(const Update u, const double *__restrict__ sums, int count,
                                                          int64_t P, int64_t Q, const Matrices x) {
@@ -175,33 +175,41 @@ __global__ __launch_bounds__(256) void muon_start_kernel(const Update u, const d
 
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 256 + (threadIdx.x & 63) * 4;
   if (c >= x.Qp) return;
-  for (int64_t r = static_cast<int64_t>(blockIdx.y) * 4 + (threadIdx.x >> 6); r < x.Pp; r += gridDim.y * 4) {
-    v4f v = {};
-    if (r < P) {
-      const int64_t at = (blockIdx.z * P + r) * Q + c;
+  // Pp is a multiple of 16: every wave takes four rows at once
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.y) * 16 + (threadIdx.x >> 6) * 4; r0 < x.Pp; r0 += gridDim.y * 16) {
+    float g[4][4], m[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t at = (blockIdx.z * P + r0 + i) * Q + c;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) g[i][k] = m[i][k] = 0.0f;
+      if (r0 + i >= P) continue;
       if (kVector) {  // Q % 4 == 0
         if (c < Q) {
-          float g[4], m[4];
-          load4<kF32>(u.grad, at, g);
-          if (u.momentum != nullptr) load4<true>(u.momentum, at, m);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            v[k] = static_cast<float>((u.momentum != nullptr ? update_of(u, g[k], m[k]) : g[k]) * by);
+          load4<kF32>(u.grad, at, g[i]);
+          if (u.momentum != nullptr) load4<true>(u.momentum, at, m[i]);
         }
       } else {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           if (c + k >= Q) break;
-          const float g = value_at<kF32>(u.grad, at + k);
-          v[k] = static_cast<float>((u.momentum != nullptr ? update_of(u, g, u.momentum[at + k]) : g) * by);
+          g[i][k] = value_at<kF32>(u.grad, at + k);
+          if (u.momentum != nullptr) m[i][k] = u.momentum[at + k];
         }
       }
     }
-    uint32_t lo;
-    const v4h hi = split(v, lo);
-    const int64_t to = (blockIdx.z * x.Pp + r) * x.Qp;
-    *reinterpret_cast<v4h *>(x.next + to + c) = hi;
-    *reinterpret_cast<uint32_t *>(x.lo + to + low_place(c)) = lo;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v4f v;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        v[k] = static_cast<float>((u.momentum != nullptr ? update_of(u, g[i][k], m[i][k]) : g[i][k]) * by);
+      uint32_t lo;
+      const v4h hi = split(v, lo);
+      const int64_t to = (blockIdx.z * x.Pp + r0 + i) * x.Qp;
+      *reinterpret_cast<v4h *>(x.next + to + c) = hi;
+      *reinterpret_cast<uint32_t *>(x.lo + to + low_place(c)) = lo;
+    }
   }
 }
 
@@ -234,11 +242,13 @@ struct Source {
   int64_t bytes;   // by rows: of the tile's rows; by columns: of a stage
   int voff, stages;
 
-  // By rows: rows [at, at + most) of `rows`; by columns: columns from `at` on, K rows.
-  __device__ __forceinline__ Source(const _Float16 *from, int64_t at, int64_t rows, int most, int64_t ld, int64_t K) {
+  // By rows: rows [at, at + most) of `rows`; by columns: columns from `at` on, K rows.  Of the K / 64 stages all, or
+  // `count` from `first` on.
+  __device__ __forceinline__ Source(const _Float16 *from, int64_t at, int64_t rows, int most, int64_t ld, int64_t K,
+                                    int first = 0, int count = 0) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     stride = ld * 2;
-    stages = static_cast<int>(K / 64);
+    stages = count > 0 ? count : static_cast<int>(K / 64);
     const int line = 4 * (wave & 1) + (lane >> 4), row = 16 * (wave >> 1) + line + 8 * ((lane >> 3) & 1);
     const int chunk = (lane & 7) ^ (kCols ? 2 * (line & 3) : line);
     voff = row * static_cast<int>(stride) + chunk * 16;
@@ -247,8 +257,9 @@ struct Source {
       bytes = 64 * stride - at * 2;  // columns past the last are others' or zeros, and their output is not used
     } else {
       p = reinterpret_cast<const uint8_t *>(from + at * ld);
-      bytes = (rows - at < most ? rows - at : most) * stride;  // rows past the last are zeros
+      bytes = (rows - at < most ? rows - at : most) * stride - first * 128;  // rows past the last are zeros
     }
+    p += kCols ? first * 64 * stride : first * 128;
   }
   // The wave's 1 KB of panel i of stage s; past the last stage zeros without traffic, so that every wave
   // always has the same number of copies in flight.
@@ -657,10 +668,14 @@ __global__ __launch_bounds__(kThreads, 2) void muon_symmetric_kernel(const _Floa
                                                                      const float *__restrict__ diagonal_in,
                                                                      Coefficients co, _Float16 *__restrict__ out,
                                                                      float *__restrict__ diagonal,
-                                                                     float2 *__restrict__ pairs) {
+                                                                     float2 *__restrict__ pairs, int splits,
+                                                                     float *__restrict__ parts) {
   const int tiles = static_cast<int>((m + kTile - 1) / kTile), per = tiles * (tiles + 1) / 2;
-  const int64_t unit = unit_of(static_cast<int64_t>(per) * G);
-  if (unit >= static_cast<int64_t>(per) * G) return;
+  const int64_t all = static_cast<int64_t>(per) * G * splits;
+  int64_t unit = unit_of(all);
+  if (unit >= all) return;
+  const int part = static_cast<int>(unit % splits);
+  unit /= splits;
   const int g = static_cast<int>(unit / per);
   int ti, tj;
   triangle(static_cast<int>(unit % per), ti, tj);
@@ -669,7 +684,24 @@ __global__ __launch_bounds__(kThreads, 2) void muon_symmetric_kernel(const _Floa
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Tile<kTile>::kLds];
   constexpr int kM = Tile<kTile>::kM, kN = Tile<kTile>::kN;
   Tile<kTile> t;
-  multiply(t, Source<kCols>(x, r0, m, kTile, ld, K), Source<kCols>(x, c0, m, kTile, ld, K), lds);
+  if constexpr (kTile == 128 && !kSquare) {
+    const int stages = static_cast<int>(K / 64), first = stages * part / splits;
+    const int count = stages * (part + 1) / splits - first;
+    multiply(t, Source<kCols>(x, r0, m, kTile, ld, K, first, count), Source<kCols>(x, c0, m, kTile, ld, K, first, count),
+             lds);
+    if (splits > 1) {  // muon_sum_kernel adds the parts up
+      int row, col;
+      lane_place<kTile>(row, col);
+      float *const to = parts + (unit * splits + part) * (kTile * kTile) + row * kTile + col;
+#pragma unroll
+      for (int i = 0; i < Tile<kTile>::kM; ++i)
+#pragma unroll
+        for (int j = 0; j < Tile<kTile>::kN; ++j) *reinterpret_cast<v4f *>(to + i * 16 * kTile + j * 16) = t.acc[i][j];
+      return;
+    }
+  } else {
+    multiply(t, Source<kCols>(x, r0, m, kTile, ld, K), Source<kCols>(x, c0, m, kTile, ld, K), lds);
+  }
   const float *const d_in = kSquare ? diagonal_in + g * m : nullptr;
   int row, col;
   lane_place<kTile>(row, col);
@@ -721,6 +753,33 @@ __global__ __launch_bounds__(kThreads, 2) void muon_symmetric_kernel(const _Floa
   }
   meet();  // every wave's copies are done, and its reads
   store_block<kTile>(h, lds, out + g * m * m, r0, c0, m, m, m, ti != tj);
+}
+
+// A and its diagonal from the parts of its tiles of 128: workgroup (x, y) takes 8 rows of tile y of all.
+__global__ __launch_bounds__(256) void muon_sum_kernel(const float *__restrict__ parts, int splits, int64_t m, int tiles,
+                                                       _Float16 *__restrict__ out, float *__restrict__ diagonal) {
+  const int per = tiles * (tiles + 1) / 2, g = blockIdx.y / per;
+  int ti, tj;
+  triangle(blockIdx.y % per, ti, tj);
+  const int row = blockIdx.x * 8 + (threadIdx.x >> 5), col = (threadIdx.x & 31) * 4;
+  const float *from = parts + static_cast<int64_t>(blockIdx.y) * splits * (128 * 128) + row * 128 + col;
+  v4f sum = {};
+#pragma unroll 8
+  for (int s = 0; s < splits; ++s) sum += *reinterpret_cast<const v4f *>(from + s * (128 * 128));
+  const int64_t i = ti * 128 + row, j = tj * 128 + col;
+  _Float16 *const o = out + g * m * m;
+  v4h h;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    float v = sum[k] * (1.0f / kScale);
+    if (i == j + k) {
+      diagonal[g * m + i] = v * (1.0f / kScale);
+      v = 0.0f;
+    }
+    h[k] = static_cast<_Float16>(v);
+    if (ti != tj) o[(j + k) * m + i] = h[k];
+  }
+  *reinterpret_cast<v4h *>(o + i * m + j) = h;
 }
 
 struct Result {
@@ -890,9 +949,12 @@ __global__ __launch_bounds__(kThreads, 2) void muon_apply_kernel(const _Float16 
 }
 
 // The workspace: sums of squares, X (hi twice, lo), A, C and their diagonals.
+constexpr int64_t kFewTiles = 128;  // tiles and their parts that do not fill half of the CUs
+
 struct Layout {
   int64_t G, P, Q, Pp, Qp, m, count;  // count: workgroups that sum a matrix's squares
-  int64_t sums, hi[2], lo, a, c, da, dc, bytes;
+  int64_t tiles, splits;              // of a matrix's A in tiles of 128, and parts of each
+  int64_t sums, hi[2], lo, a, c, da, dc, parts, bytes;
   Layout(int64_t G, int64_t P, int64_t Q) : G(G), P(P), Q(Q) {
     Pp = padded(P);
     Qp = padded(Q);
@@ -912,6 +974,12 @@ struct Layout {
     c = take(2 * G * m * m);
     da = take(4 * G * m);
     dc = take(8 * G * m);
+    // A long sum of few tiles is split, at least 8 stages each.  256 x 7168 (3 tiles, 112 stages): 51 -> 14 us.
+    tiles = (m / 128) * (m / 128 + 1) / 2;
+    const int64_t stages = (Pp < Qp ? Qp : Pp) / 64, room = kFewTiles / (tiles * G);
+    splits = stages / 8 < room ? stages / 8 : room;
+    splits = splits < 4 ? 1 : (splits > 16 ? 16 : splits);
+    parts = take(splits > 1 ? 4 * 128 * 128 * G * tiles * splits : 0);
     bytes = at;
   }
 };
@@ -960,9 +1028,11 @@ hipError_t run(const Layout &w, const Update &u, bool f32, const Coefficients &c
       vector ? go(muon_momentum_kernel<true, true>) : go(muon_momentum_kernel<true, false>);
     else
       vector ? go(muon_momentum_kernel<false, true>) : go(muon_momentum_kernel<false, false>);
-    // about 16 rows for each thread: every workgroup adds up the sums first
-    const int64_t bands = (w.Pp + 63) / 64;
-    const dim3 tiles(static_cast<uint32_t>((w.Qp + 255) / 256), static_cast<uint32_t>(bands < 65535 ? bands : 65535),
+    // Every workgroup adds up the sums first: of many, a thread takes 16 rows instead of 4.
+    const int64_t columns = (w.Qp + 255) / 256;
+    int64_t bands = w.Pp / 16;
+    if (columns * bands * w.G > 16 * cus) bands = (bands + 3) / 4;
+    const dim3 tiles(static_cast<uint32_t>(columns), static_cast<uint32_t>(bands < 65535 ? bands : 65535),
                      static_cast<uint32_t>(G));
     auto start = [&](auto kernel) {
       hipLaunchKernelGGL(kernel, tiles, block, 0, stream, u, sums, static_cast<int>(w.count), w.P, w.Q, x);
@@ -975,22 +1045,26 @@ hipError_t run(const Layout &w, const Update &u, bool f32, const Coefficients &c
   auto tiles = [](int64_t size, int tile) { return (size + tile - 1) / tile; };
   auto triangle_units = [&](int tile) { return w.G * tiles(w.m, tile) * (tiles(w.m, tile) + 1) / 2; };
   auto apply_units = [&](int tile) { return w.G * tiles(w.Pp, tile) * tiles(w.Qp, tile); };
-  const int sym = tile_for(triangle_units, cus), app = tile_for(apply_units, cus);
+  const int sym = w.splits > 1 ? 128 : tile_for(triangle_units, cus), app = tile_for(apply_units, cus);
   auto grid_of = [](int64_t units) { return dim3(static_cast<uint32_t>((units + 7) / 8 * 8)); };
   for (int64_t s = 0; s < steps; ++s) {
     x.hi = halves(w.hi[s & 1]);
     x.next = halves(w.hi[(s + 1) & 1]);
     with_tile(sym, [&](auto tile) {
       constexpr int kT = decltype(tile)::value;
-      auto go = [&](auto kernel, const _Float16 *from, int64_t ld, int64_t K, const float *d_in, _Float16 *to) {
-        hipLaunchKernelGGL(kernel, grid_of(triangle_units(kT)), dim3(kThreads), 0, stream, from, ld, K, w.m, G, d_in, co, to,
-                           floats(w.da), reinterpret_cast<float2 *>(ws + w.dc));
+      auto go = [&](auto kernel, const _Float16 *from, int64_t ld, int64_t K, const float *d_in, _Float16 *to, int64_t splits) {
+        hipLaunchKernelGGL(kernel, grid_of(triangle_units(kT) * splits), dim3(kThreads), 0, stream, from, ld, K, w.m, G, d_in, co, to,
+                           floats(w.da), reinterpret_cast<float2 *>(ws + w.dc), static_cast<int>(splits), floats(w.parts));
       };
       if (tall)
-        go(muon_symmetric_kernel<kT, false, true>, x.hi, w.Qp, w.Pp, nullptr, halves(w.a));
+        go(muon_symmetric_kernel<kT, false, true>, x.hi, w.Qp, w.Pp, nullptr, halves(w.a), w.splits);
       else
-        go(muon_symmetric_kernel<kT, false, false>, x.hi, w.Qp, w.Qp, nullptr, halves(w.a));
-      go(muon_symmetric_kernel<kT, true, false>, halves(w.a), w.m, w.m, floats(w.da), halves(w.c));
+        go(muon_symmetric_kernel<kT, false, false>, x.hi, w.Qp, w.Qp, nullptr, halves(w.a), w.splits);
+      if (w.splits > 1)
+        hipLaunchKernelGGL(muon_sum_kernel, dim3(16, static_cast<uint32_t>(w.G * w.tiles)), dim3(256), 0, stream,
+                           floats(w.parts), static_cast<int>(w.splits), w.m, static_cast<int>(w.m / 128), halves(w.a),
+                           floats(w.da));
+      go(muon_symmetric_kernel<kT, true, false>, halves(w.a), w.m, w.m, floats(w.da), halves(w.c), 1);
     });
     with_tile(app, [&](auto tile) {
       constexpr int kT = decltype(tile)::value;

@@ -79,7 +79,8 @@ def matrices(shape, kind, dtype=F32, seed=0):
 
 
 SHAPES = [(1, 1), (1, 7), (7, 1), (5, 3), (8, 8), (64, 64), (65, 63), (100, 130), (128, 128), (129, 257), (300, 1000),
-          (1000, 300), (513, 512), (3, 77, 200), (4, 200, 77), (2, 256, 640)]
+          (1000, 300), (513, 512), (3, 77, 200), (4, 200, 77), (2, 256, 640),
+          (128, 7168), (7168, 200), (2, 70, 3000)]
 
 
 @pytest.mark.parametrize("kind", ["normal", "strong"])
