@@ -41,7 +41,8 @@ typedef short v4s __attribute__((ext_vector_type(4)));
 constexpr float kScale = 4096.0f;  // of X, A and C as stored
 constexpr int64_t kPad = 128;      // sizes of the stored matrices
 constexpr int kThreads = 512;
-constexpr int kPerSum = 8192;  // elements of a workgroup that sums squares
+constexpr int kPerSum = 8192;  // elements that a workgroup sums the squares of at a time
+constexpr int64_t kSums = 16384;  // the most of these workgroups, for several matrices together
 
 int64_t padded(int64_t v) { return (v + kPad - 1) / kPad * kPad; }
 
@@ -76,44 +77,48 @@ __device__ __forceinline__ float update_of(const Update &u, float g, float m) {
   return u.nesterov ? __builtin_fmaf(u.beta, m, g * u.grad_scale) : m;
 }
 
-// Workgroup (x, y): kPerSum elements of matrix y: the new momentum and the sum of the update's squares.
+// Workgroup (x, y): kPerSum elements of matrix y, and every gridDim.x-th so many after them: the new momentum and
+// the sum of the update's squares.
 // In 64 bits, which hold the squares of every FP32 number.
 template <bool kF32, bool kVector>
 __global__ __launch_bounds__(256) void muon_momentum_kernel(const Update u, int64_t size, double *__restrict__ sums) {
   __shared__ double waves[4];
   double sum = 0.0;
-  const int64_t base = blockIdx.y * size, end = base + size;
+  const int64_t end = (blockIdx.y + int64_t(1)) * size;
+  int64_t first = blockIdx.y * size + static_cast<int64_t>(blockIdx.x) * kPerSum;
+  for (; first < end; first += static_cast<int64_t>(gridDim.x) * kPerSum) {
 #pragma unroll
-  for (int k = 0; k < kPerSum / 2048; ++k) {
-    const int64_t at = base + static_cast<int64_t>(blockIdx.x) * kPerSum + k * 2048 + threadIdx.x * 8;
-    if (at >= end) break;
-    const int n = end - at < 8 ? static_cast<int>(end - at) : 8;
-    float g[8], m[8];
-    if (kVector) {
-      load8<kF32>(u.grad, at, g);
-      if (u.momentum != nullptr) load8<true>(u.momentum, at, m);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        g[i] = i < n ? value_at<kF32>(u.grad, at + i) : 0.0f;
-        m[i] = i < n && u.momentum != nullptr ? u.momentum[at + i] : 0.0f;
-      }
-    }
-    if (u.momentum != nullptr) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) m[i] = __builtin_fmaf(u.beta, m[i], g[i] * u.grad_scale);
+    for (int k = 0; k < kPerSum / 2048; ++k) {
+      const int64_t at = first + k * 2048 + threadIdx.x * 8;
+      if (at >= end) break;
+      const int n = end - at < 8 ? static_cast<int>(end - at) : 8;
+      float g[8], m[8];
       if (kVector) {
-        store8<true>(u.momentum, at, m);
+        load8<kF32>(u.grad, at, g);
+        if (u.momentum != nullptr) load8<true>(u.momentum, at, m);
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (i < n) u.momentum[at + i] = m[i];
+        for (int i = 0; i < 8; ++i) {
+          g[i] = i < n ? value_at<kF32>(u.grad, at + i) : 0.0f;
+          m[i] = i < n && u.momentum != nullptr ? u.momentum[at + i] : 0.0f;
+        }
       }
-    }
+      if (u.momentum != nullptr) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const double v = u.momentum != nullptr ? update_of(u, g[i], m[i]) : g[i];
-      sum += v * v;
+        for (int i = 0; i < 8; ++i) m[i] = __builtin_fmaf(u.beta, m[i], g[i] * u.grad_scale);
+        if (kVector) {
+          store8<true>(u.momentum, at, m);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (i < n) u.momentum[at + i] = m[i];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const double v = u.momentum != nullptr ? update_of(u, g[i], m[i]) : g[i];
+        sum += v * v;
+      }
     }
   }
   for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
@@ -145,10 +150,12 @@ __device__ __forceinline__ v4h split(v4f v, uint32_t &lo) {
   v4h hi;
   v4f rest;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    hi[k] = static_cast<_Float16>(v[k]);
-    rest[k] = (v[k] - static_cast<float>(hi[k])) * kLow;
-  }
+  for (int k = 0; k < 4; ++k) hi[k] = static_cast<_Float16>(v[k]);
+  // One rounding for both: the compiler may round a product or sum twice for one of two conversions and once
+  // for the other, and where these differ lo would belong to another hi.
+  asm volatile("" : "+v"(hi));
+#pragma unroll
+  for (int k = 0; k < 4; ++k) rest[k] = (v[k] - static_cast<float>(hi[k])) * kLow;
   lo = pack4_e4m3(rest[0], rest[1], rest[2], rest[3]);
   return hi;
 }
@@ -166,12 +173,16 @@ __global__ __launch_bounds__(256) void muon_start_kernel(const Update u, const d
                                                          int64_t P, int64_t Q, const Matrices x) {
   __shared__ double waves[4];
   double sum = 0.0;
+#pragma unroll 8
   for (int i = threadIdx.x; i < count; i += 256) sum += sums[static_cast<int64_t>(blockIdx.z) * count + i];
   for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
   if ((threadIdx.x & 63) == 0) waves[threadIdx.x >> 6] = sum;
   __syncthreads();
   sum = (waves[0] + waves[1]) + (waves[2] + waves[3]);
-  const double by = sum > 0.0 ? static_cast<double>(kScale) / sqrt(sum) : 0.0;
+  // kScale / |U| as a power of two, which may lie outside FP32, and a factor of 1/2 to 1: FP64 products cost twice
+  // the time of the copy.
+  int power = 0;
+  const float factor = sum > 0.0 ? static_cast<float>(frexp(static_cast<double>(kScale) / sqrt(sum), &power)) : 0.0f;
 
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 256 + (threadIdx.x & 63) * 4;
   if (c >= x.Qp) return;
@@ -203,7 +214,7 @@ __global__ __launch_bounds__(256) void muon_start_kernel(const Update u, const d
       v4f v;
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        v[k] = static_cast<float>((u.momentum != nullptr ? update_of(u, g[i][k], m[i][k]) : g[i][k]) * by);
+        v[k] = ldexpf(u.momentum != nullptr ? update_of(u, g[i][k], m[i][k]) : g[i][k], power) * factor;
       uint32_t lo;
       const v4h hi = split(v, lo);
       const int64_t to = (blockIdx.z * x.Pp + r0 + i) * x.Qp;
@@ -683,31 +694,12 @@ __global__ __launch_bounds__(kThreads, 2) void muon_symmetric_kernel(const _Floa
   const _Float16 *x = from + g * m * K;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Tile<kTile>::kLds];
   constexpr int kM = Tile<kTile>::kM, kN = Tile<kTile>::kN;
-  Tile<kTile> t;
-  if constexpr (kTile == 128 && !kSquare) {
-    const int stages = static_cast<int>(K / 64), first = stages * part / splits;
-    const int count = stages * (part + 1) / splits - first;
-    multiply(t, Source<kCols>(x, r0, m, kTile, ld, K, first, count), Source<kCols>(x, c0, m, kTile, ld, K, first, count),
-             lds);
-    if (splits > 1) {  // muon_sum_kernel adds the parts up
-      int row, col;
-      lane_place<kTile>(row, col);
-      float *const to = parts + (unit * splits + part) * (kTile * kTile) + row * kTile + col;
-#pragma unroll
-      for (int i = 0; i < Tile<kTile>::kM; ++i)
-#pragma unroll
-        for (int j = 0; j < Tile<kTile>::kN; ++j) *reinterpret_cast<v4f *>(to + i * 16 * kTile + j * 16) = t.acc[i][j];
-      return;
-    }
-  } else {
-    multiply(t, Source<kCols>(x, r0, m, kTile, ld, K), Source<kCols>(x, c0, m, kTile, ld, K), lds);
-  }
   const float *const d_in = kSquare ? diagonal_in + g * m : nullptr;
   int row, col;
   lane_place<kTile>(row, col);
   v4h h[kM][kN];
   v4f dj[kSquare ? kN : 1];
-  if constexpr (kSquare) {  // A's own tile, all of it on its way at once
+  auto read_own = [&]() {  // A's own tile, all of it on its way at once
 #pragma unroll
     for (int j = 0; j < kN; ++j) {
       const int64_t c = c0 + col + 16 * j;
@@ -720,7 +712,28 @@ __global__ __launch_bounds__(kThreads, 2) void muon_symmetric_kernel(const _Floa
         const int64_t r = r0 + row + 16 * i, c = c0 + col + 16 * j;
         h[i][j] = r < m && c < m ? *reinterpret_cast<const v4h *>(x + r * m + c) : v4h{};
       }
+  };
+  // before the products where there are registers for it
+  if constexpr (kSquare && kTile != 256) read_own();
+  in_order();
+  Tile<kTile> t;
+  if constexpr (kTile == 128 && !kSquare) {
+    const int stages = static_cast<int>(K / 64), first = stages * part / splits;
+    const int count = stages * (part + 1) / splits - first;
+    multiply(t, Source<kCols>(x, r0, m, kTile, ld, K, first, count), Source<kCols>(x, c0, m, kTile, ld, K, first, count),
+             lds);
+    if (splits > 1) {  // muon_sum_kernel adds the parts up
+      float *const to = parts + (unit * splits + part) * (kTile * kTile) + row * kTile + col;
+#pragma unroll
+      for (int i = 0; i < Tile<kTile>::kM; ++i)
+#pragma unroll
+        for (int j = 0; j < Tile<kTile>::kN; ++j) *reinterpret_cast<v4f *>(to + i * 16 * kTile + j * 16) = t.acc[i][j];
+      return;
+    }
+  } else {
+    multiply(t, Source<kCols>(x, r0, m, kTile, ld, K), Source<kCols>(x, c0, m, kTile, ld, K), lds);
   }
+  if constexpr (kSquare && kTile == 256) read_own();
 #pragma unroll
   for (int i = 0; i < kM; ++i) {
     const int64_t r = r0 + row + 16 * i;
@@ -736,7 +749,7 @@ __global__ __launch_bounds__(kThreads, 2) void muon_symmetric_kernel(const _Floa
           if constexpr (kSquare) {
             const float d = __builtin_fmaf(co.c, __builtin_fmaf(di, di, s), __builtin_fmaf(co.b, di, co.a));
             s = d * kScale;
-            const float rounded = static_cast<float>(static_cast<_Float16>(s));
+            const float rounded = static_cast<float>(static_cast<_Float16>(s));  // s is exact, and rounded alike below
             // below 2^-13 FP16 has fewer bits, and what they lose is nothing beside the other rows
             if (r < m) pairs[g * m + r] = make_float2(d, fabsf(rounded) >= 0x1p-13f ? s / rounded : 1.0f);
           } else {
@@ -960,6 +973,8 @@ struct Layout {
     Qp = padded(Q);
     m = Pp < Qp ? Pp : Qp;
     count = (P * Q + kPerSum - 1) / kPerSum;
+    const int64_t most = G < kSums ? kSums / G : 1;
+    count = count < most ? count : most;
     int64_t at = 0;
     auto take = [&](int64_t size) {
       const int64_t here = at;
