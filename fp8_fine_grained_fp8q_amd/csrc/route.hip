@@ -122,9 +122,25 @@ __device__ __forceinline__ float load_logit(const void *p, int64_t at) {
   return kF32 ? static_cast<const float *>(p)[at] : bf16_lo(static_cast<const uint16_t *>(p)[at]);
 }
 
+// e^x for x <= 0, to 2^-22 of itself (0 below FP32's normal range): the hardware's 2^y at y = x log2 e rounded,
+// times 1 + ln 2 of what y lost.  7 instructions instead of 20.
+__device__ __forceinline__ float exp_of(float x) {
+  x = fmaxf(x, -1000.0f);  // also -inf, whose loss would be NaN
+  const float y = x * 1.44269502f;
+  const float rest = __builtin_fmaf(x, 1.92596303e-8f, __builtin_fmaf(x, 1.44269502f, -y));
+  const float e = __builtin_amdgcn_exp2f(y);
+  return __builtin_fmaf(e, rest * 0.693147182f, e);
+}
+
+// 1 / x for x in [1, 2], to one unit of the last place.
+__device__ __forceinline__ float reciprocal(float x) {
+  const float r = __builtin_amdgcn_rcpf(x);
+  return __builtin_fmaf(r, __builtin_fmaf(-x, r, 1.0f), r);
+}
+
 // 1 / (1 + e^-z) and 1 minus it, from e^-|z|: no overflow, no cancellation.  -inf gives 0 and 1.
 __device__ __forceinline__ float sigmoid(float z, float &rest) {
-  const float t = expf(-fabsf(z)), r = 1.0f / (1.0f + t);
+  const float t = exp_of(-fabsf(z)), r = reciprocal(1.0f + t);
   rest = (z >= 0.0f ? t : 1.0f) * r;
   return (z >= 0.0f ? 1.0f : t) * r;
 }
@@ -140,7 +156,7 @@ __device__ __forceinline__ void scores(const float (&z)[kV], float (&s)[kV], flo
 #pragma unroll
   for (int v = 0; v < kV; ++v) {
     float rest;
-    s[v] = kSoftmax ? expf(z[v] - top) : sigmoid(z[v], rest);
+    s[v] = kSoftmax ? exp_of(z[v] - top) : sigmoid(z[v], rest);
     sum += s[v];
   }
   sum = across<kLanes>(sum, Add{});
@@ -153,16 +169,50 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// Top-k of `key` (consumed): chosen expert j goes to ids[j] (LDS, one writer per token), -1 where
-// no key above -inf is left.  Returns whether two keys that follow each other, the (k+1)-th among
-// them, differ by less than `near` times (their size + floor).
-template <int kLanes, int kV, class Key>
-__device__ __forceinline__ bool select(Key (&key)[kV], int k, int l, int32_t *ids, float near, float floor) {
+// Keys of the top-k with their expert, as one number that sorts by the key and then by the lower index: an FP32
+// number as FP64 has 29 zero bits at its end, and FP64 maxima are as fast as FP32 ones.  Keys of -inf (and NaN)
+// lie below kNone and are never chosen.
+constexpr double kNone = -0x1p200, kLowest = -0x1p210;
+
+__device__ __forceinline__ double pack(float key, int expert) {
+  const double d = key > -INFINITY ? static_cast<double>(key + 0.0f) : kLowest;  // -0 as 0
+  const int64_t bits = __builtin_bit_cast(int64_t, d);
+  return __builtin_bit_cast(double, bits | static_cast<int64_t>(bits < 0 ? expert : 1023 - expert));
+}
+
+__device__ __forceinline__ int expert_in(double packed) {
+  const int low = static_cast<int>(__builtin_bit_cast(int64_t, packed)) & 1023;
+  return packed < 0.0 ? low : 1023 - low;
+}
+
+// Top-k of packed keys (consumed): chosen expert j goes to ids[j] (LDS, one writer per token), -1 where no key
+// is left.  Returns whether two keys that follow each other, the (k+1)-th among them, differ by less
+// than `near` times (their size + floor).
+template <int kLanes, int kV>
+__device__ __forceinline__ bool select(double (&key)[kV], int k, int l, int32_t *ids, float near, float floor) {
   bool close = false;
-  Key last = 0;
+  double last = 0.0;
   const int steps = near > 0.0f ? k + 1 : k;
   for (int j = 0; j < steps; ++j) {
-    Key best = key[0];
+    double top = key[0];
+#pragma unroll
+    for (int v = 1; v < kV; ++v) top = fmax(top, key[v]);
+    top = across<kLanes>(top, Max{});
+    const bool some = top > kNone;
+    if (j < k && l == 0) ids[j] = some ? expert_in(top) : -1;
+#pragma unroll
+    for (int v = 0; v < kV; ++v) key[v] = key[v] == top ? kLowest : key[v];
+    if (near > 0.0f && j > 0) close |= some && last - top <= static_cast<double>(near) * (fabs(last) + static_cast<double>(floor));
+    last = top;
+  }
+  return close;
+}
+
+// The same for keys that need all of FP64's bits.
+template <int kLanes, int kV>
+__device__ __forceinline__ void select_exact(double (&key)[kV], int k, int l, int32_t *ids) {
+  for (int j = 0; j < k; ++j) {
+    double best = key[0];
     int at = expert_of<kLanes>(l, 0);
 #pragma unroll
     for (int v = 1; v < kV; ++v) {
@@ -170,19 +220,15 @@ __device__ __forceinline__ bool select(Key (&key)[kV], int k, int l, int32_t *id
       best = more ? key[v] : best;
       at = more ? expert_of<kLanes>(l, v) : at;
     }
-    const Key top = across<kLanes>(best, Max{});
-    const bool some = top > static_cast<Key>(-INFINITY);
+    const double top = across<kLanes>(best, Max{});
+    const bool some = top > -INFINITY;
     int won = best == top && some ? at : kNoExpert;
     won = across<kLanes>(won, Min{});
 #pragma unroll
     for (int v = 0; v < kV; ++v)
-      if (won == expert_of<kLanes>(l, v)) key[v] = static_cast<Key>(-INFINITY);
-    if (j < k && l == 0) ids[j] = won == kNoExpert ? -1 : won;
-    if (near > 0.0f && j > 0)
-      close |= some && last - top <= static_cast<Key>(near) * (fabs(last) + static_cast<Key>(floor));
-    last = top;
+      if (won == expert_of<kLanes>(l, v)) key[v] = -INFINITY;
+    if (l == 0) ids[j] = won == kNoExpert ? -1 : won;
   }
-  return close;
 }
 
 // What a workgroup leaves in the workspace: FP32 sums of p [E], counts [E], its tokens and its routed
@@ -260,13 +306,16 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(const RouteArg
     here = here && top > -INFINITY;
     const float r = 1.0f / sum;
     {
-      float key[kV];
+      double key[kV];
 #pragma unroll
       for (int v = 0; v < kV; ++v)
-        key[v] = a.bias == nullptr || z[v] == -INFINITY ? z[v] : (kSoftmax ? s[v] * r : s[v]) + bias[v];
-      // An FP32 score is off by 2^-24 (4 + |z - top|) of itself and its sum with the bias by 2^-24:
-      // 2^-17 covers two of them down to scores of e^-60, the floor the smaller ones.
-      const bool close = select<kLanes, kV>(key, k, l, ids, a.bias == nullptr ? 0.0f : 0x1p-17f, 2.0f * far + 1e-20f);
+        key[v] = pack(a.bias == nullptr || z[v] == -INFINITY ? z[v] : (kSoftmax ? s[v] * r : s[v]) + bias[v],
+                      expert_of<kLanes>(l, v));
+      // A sigmoid in FP32 is off by less than 2^-21.5 of itself, a softmax by 2^-24 (12 + |z - top|), their sums with
+      // the bias by 2^-24: 2^-19 and 2^-17 cover two of them, the latter down to scores of e^-50, and the
+      // floor covers the smaller ones.
+      const float near = a.bias == nullptr ? 0.0f : (kSoftmax ? 0x1p-17f : 0x1p-19f);
+      const bool close = select<kLanes, kV>(key, k, l, ids, near, 2.0f * far + 1e-16f);
       if (__any(close)) {
         double rank[kV], total = 0.0;
 #pragma unroll
@@ -281,7 +330,7 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(const RouteArg
           rank[v] = (kSoftmax ? rank[v] / total : rank[v]) + static_cast<double>(bias[v]);
           if (z[v] == -INFINITY) rank[v] = -INFINITY;
         }
-        select<kLanes, kV>(rank, k, l, ids, 0.0f, 0.0f);
+        select_exact<kLanes, kV>(rank, k, l, ids);
       }
     }
     wave_sync();
@@ -297,6 +346,8 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(const RouteArg
 #pragma unroll
     for (int i = 0; i < kSlots; ++i) {
       const int j = l + i * kLanes;
+      id[i] = -1;
+      if (i * kLanes >= k) break;
       id[i] = j < k && here ? ids[j] : -1;
       x[i] = id[i] >= 0 ? load_logit<kF32>(a.logits, row * E + id[i]) : -INFINITY;
       m = fmaxf(m, x[i]);
@@ -307,11 +358,12 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(const RouteArg
     }
 #pragma unroll
     for (int i = 0; i < kSlots; ++i) {
+      if (i * kLanes >= k) break;
       float rest;
       if (a.normalize)
-        x[i] = kSoftmax ? expf(x[i] - m) : expf(fminf(x[i], 0.0f) - m) / (1.0f + expf(-fabsf(x[i])));
+        x[i] = kSoftmax ? exp_of(x[i] - m) : exp_of(fminf(x[i], 0.0f) - m) * reciprocal(1.0f + exp_of(-fabsf(x[i])));
       else
-        x[i] = kSoftmax ? expf(x[i] - top) * r : sigmoid(x[i], rest);
+        x[i] = kSoftmax ? exp_of(x[i] - top) * r : sigmoid(x[i], rest);
       total += id[i] >= 0 ? x[i] : 0.0f;
     }
     if (a.normalize) total = across<kLanes>(total, Add{});
@@ -424,7 +476,10 @@ __global__ __launch_bounds__(1024) void moe_route_sum_kernel(const RouteArgs a, 
   const uint32_t blocks = gridDim.x * gridDim.y;
   if (lane == 0) {
     __hip_atomic_store(&a.losses[blockIdx.y * gridDim.x + blockIdx.x], mine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    const uint32_t arrived = __hip_atomic_fetch_add(a.counter, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+    // the part of the loss has arrived; as an atomic of the device's scope it needs no fence, which would write
+    // back the XCD's L2
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    const uint32_t arrived = __hip_atomic_fetch_add(a.counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     last = arrived + 1 == blocks;
   }
   wave_sync();
@@ -479,6 +534,8 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_backward_kernel(const
 #pragma unroll
     for (int i = 0; i < kSlots; ++i) {
       const int j = l + i * kLanes;
+      id[i] = -1;
+      if (i * kLanes >= k) break;
       id[i] = here && j < k ? a.ids[row * k + j] : -1;
       if (id[i] >= E) id[i] = -1;
       w[i] = dw[i] = 0.0f;
