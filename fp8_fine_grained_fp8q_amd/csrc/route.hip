@@ -16,8 +16,8 @@
 //   sigmoid:  dz_e = (1 - s_e) (p_e (g_e - sum p g) + [e chosen] d_j).
 //
 // The ranks are those of scores computed in 64 bits.  Scores in FP32 give the same ones unless two
-// that follow each other are nearer than their errors; a wave that sees such a pair ranks its tokens
-// again with 64-bit scores (about one token in 100).
+// that follow each other are nearer than their errors; then the chosen ones and those beside the last of them are
+// ranked by their 64-bit scores (about one token in 500 with sigmoid scores).
 //
 // A group of 16 lanes takes a token of up to 256 experts, 64 lanes one of up to 1024, 4 to 16
 // logits per lane in registers: the maxima of a top-k step are 4 DPP steps inside a row of lanes, and
@@ -185,50 +185,60 @@ __device__ __forceinline__ int expert_in(double packed) {
   return packed < 0.0 ? low : 1023 - low;
 }
 
-// Top-k of packed keys (consumed): chosen expert j goes to ids[j] (LDS, one writer per token), -1 where no key
-// is left.  Returns whether two keys that follow each other, the (k+1)-th among them, differ by less
-// than `near` times (their size + floor).
+constexpr int kCandidates = 128;  // of a token whose order FP32 leaves open
+
+// The largest packed key of a token, which is taken out.
 template <int kLanes, int kV>
-__device__ __forceinline__ bool select(double (&key)[kV], int k, int l, int32_t *ids, float near, float floor) {
+__device__ __forceinline__ double take_top(double (&key)[kV]) {
+  double top = key[0];
+#pragma unroll
+  for (int v = 1; v < kV; ++v) top = fmax(top, key[v]);
+  top = across<kLanes>(top, Max{});
+#pragma unroll
+  for (int v = 0; v < kV; ++v) key[v] = key[v] == top ? kLowest : key[v];
+  return top;
+}
+
+// Top-k of packed keys (consumed): chosen expert j goes to ids[j] (LDS, one writer per token), -1 where no key
+// is left.  With near > 0 also: every expert behind the k-th whose key differs from its by less than `near` times
+// (its size + floor) follows there, `found` counts all of them, up to kCandidates + 1, and the answer
+// is whether two keys that follow each other are as near.
+template <int kLanes, int kV>
+__device__ __forceinline__ bool select(double (&key)[kV], int k, int l, int32_t *ids, float near, float floor, int &found) {
   bool close = false;
   double last = 0.0;
-  const int steps = near > 0.0f ? k + 1 : k;
-  for (int j = 0; j < steps; ++j) {
-    double top = key[0];
-#pragma unroll
-    for (int v = 1; v < kV; ++v) top = fmax(top, key[v]);
-    top = across<kLanes>(top, Max{});
+  auto within = [&](double top) {
+    return last - top <= static_cast<double>(near) * (fabs(last) + static_cast<double>(floor));
+  };
+  found = 0;
+  for (int j = 0; j < k; ++j) {
+    const double top = take_top<kLanes>(key);
     const bool some = top > kNone;
-    if (j < k && l == 0) ids[j] = some ? expert_in(top) : -1;
-#pragma unroll
-    for (int v = 0; v < kV; ++v) key[v] = key[v] == top ? kLowest : key[v];
-    if (near > 0.0f && j > 0) close |= some && last - top <= static_cast<double>(near) * (fabs(last) + static_cast<double>(floor));
+    if (l == 0) ids[j] = some ? expert_in(top) : -1;
+    close |= near > 0.0f && j > 0 && some && within(top);
+    found += some ? 1 : 0;
     last = top;
+  }
+  if (near > 0.0f) {
+    bool more = found == k;
+    while (true) {
+      const double top = take_top<kLanes>(key);
+      more = more && top > kNone && within(top) && found <= kCandidates;
+      if (!__any(more)) break;
+      if (more) {
+        close = true;
+        if (l == 0 && found < kCandidates) ids[found] = expert_in(top);
+        ++found;
+      }
+    }
   }
   return close;
 }
 
-// The same for keys that need all of FP64's bits.
-template <int kLanes, int kV>
-__device__ __forceinline__ void select_exact(double (&key)[kV], int k, int l, int32_t *ids) {
-  for (int j = 0; j < k; ++j) {
-    double best = key[0];
-    int at = expert_of<kLanes>(l, 0);
-#pragma unroll
-    for (int v = 1; v < kV; ++v) {
-      const bool more = key[v] > best;
-      best = more ? key[v] : best;
-      at = more ? expert_of<kLanes>(l, v) : at;
-    }
-    const double top = across<kLanes>(best, Max{});
-    const bool some = top > -INFINITY;
-    int won = best == top && some ? at : kNoExpert;
-    won = across<kLanes>(won, Min{});
-#pragma unroll
-    for (int v = 0; v < kV; ++v)
-      if (won == expert_of<kLanes>(l, v)) key[v] = -INFINITY;
-    if (l == 0) ids[j] = won == kNoExpert ? -1 : won;
-  }
+// A token's score + bias in 64 bits.
+template <bool kSoftmax>
+__device__ __forceinline__ double exact_score(double z, double top, double total, double bias) {
+  return (kSoftmax ? exp(z - top) / total : 1.0 / (1.0 + exp(-z))) + bias;
 }
 
 // What a workgroup leaves in the workspace: FP32 sums of p [E], counts [E], its tokens and its routed
@@ -269,7 +279,8 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(const RouteArg
   constexpr int kSlots = kMaxTopK / kLanes;        // of a lane
   __shared__ float sums[kRouteThreads / 64][kMost];
   __shared__ int32_t hist[kMost];
-  __shared__ int32_t chosen[kRouteThreads / kLanes][kMaxTopK];
+  __shared__ int32_t chosen[kRouteThreads / kLanes][kCandidates];
+  __shared__ double exact[kRouteThreads / kLanes][kCandidates];
   __shared__ int32_t totals[2];
   __shared__ double loss[kRouteThreads / 64];
   const int l = threadIdx.x % kLanes, group = threadIdx.x / kLanes, groups = blockDim.x / kLanes;
@@ -315,22 +326,74 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(const RouteArg
       // the bias by 2^-24: 2^-19 and 2^-17 cover two of them, the latter down to scores of e^-50, and the
       // floor covers the smaller ones.
       const float near = a.bias == nullptr ? 0.0f : (kSoftmax ? 0x1p-17f : 0x1p-19f);
-      const bool close = select<kLanes, kV>(key, k, l, ids, near, 2.0f * far + 1e-16f);
+      int found;
+      const bool close = select<kLanes, kV>(key, k, l, ids, near, 2.0f * far + 1e-16f, found);
       if (__any(close)) {
-        double rank[kV], total = 0.0;
-#pragma unroll
-        for (int v = 0; v < kV; ++v) {
-          const double x = z[v];
-          rank[v] = kSoftmax ? exp(x - static_cast<double>(top)) : 1.0 / (1.0 + exp(-x));
-          total += rank[v];
+        wave_sync();
+        double total = 1.0;
+        const double high = top;
+        if (kSoftmax) {
+          total = 0.0;
+#pragma unroll 1
+          for (int v = 0; v < kV; ++v) {
+            const int e = expert_of<kLanes>(l, v);
+            if (here && e < E) total += exp(static_cast<double>(load_logit<kF32>(a.logits, row * E + e)) - high);
+          }
+          total = across<kLanes>(total, Add{});
         }
-        if (kSoftmax) total = across<kLanes>(total, Add{});
+        auto score_of = [&](int e) {
+          return exact_score<kSoftmax>(load_logit<kF32>(a.logits, row * E + e), high, total, a.bias[e]);
+        };
+        if (close && found <= kCandidates) {
+          // every candidate's place among them: those with a higher score, or as high and a lower index
+          double *const score = exact[group];
+#pragma unroll 1
+          for (int c = l; c < found; c += kLanes) score[c] = score_of(ids[c]);
+          wave_sync();
+          int place[kCandidates / kLanes], id[kCandidates / kLanes];
 #pragma unroll
-        for (int v = 0; v < kV; ++v) {
-          rank[v] = (kSoftmax ? rank[v] / total : rank[v]) + static_cast<double>(bias[v]);
-          if (z[v] == -INFINITY) rank[v] = -INFINITY;
+          for (int i = 0; i < kCandidates / kLanes; ++i) {
+            place[i] = k;
+            id[i] = -1;
+          }
+#pragma unroll
+          for (int i = 0; i < kCandidates / kLanes; ++i) {
+            const int c = l + i * kLanes;
+            if (c >= found) break;
+            id[i] = ids[c];
+            const double mine = score[c];
+            int before = 0;
+            for (int o = 0; o < found; ++o) before += score[o] > mine || (score[o] == mine && ids[o] < id[i]) ? 1 : 0;
+            place[i] = before;
+          }
+          wave_sync();
+#pragma unroll
+          for (int i = 0; i < kCandidates / kLanes; ++i)
+            if (place[i] < k) ids[place[i]] = id[i];
+        } else if (close) {
+          // more than that lie together (equal logits and biases): each rank by all scores
+          uint32_t taken = 0;
+#pragma unroll 1
+          for (int j = 0; j < k; ++j) {
+            double best = -INFINITY;
+            int at = kNoExpert, v_at = 0;
+#pragma unroll 1
+            for (int v = 0; v < kV; ++v) {
+              const int e = expert_of<kLanes>(l, v);
+              if (e >= E || (taken >> v & 1u) != 0 || load_logit<kF32>(a.logits, row * E + e) == -INFINITY) continue;
+              const double one = score_of(e);
+              if (one > best) {
+                best = one;
+                at = e;
+                v_at = v;
+              }
+            }
+            const double most = across<kLanes>(best, Max{});
+            const int won = across<kLanes>(best == most ? at : kNoExpert, Min{});
+            if (won == at && at != kNoExpert) taken |= 1u << v_at;
+            if (l == 0) ids[j] = won == kNoExpert ? -1 : won;
+          }
         }
-        select_exact<kLanes, kV>(rank, k, l, ids);
       }
     }
     wave_sync();

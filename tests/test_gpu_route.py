@@ -117,6 +117,24 @@ def test_near_ties_are_ranked_in_64_bits():
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k", [(64, 8), (250, 60), (256, 8), (1024, 64)])
+def test_many_equal_scores(score, E, k):
+    """All experts alike but for a few: more experts than FP32 tells apart, up to all of them, beside tokens
+    without ties in the same wave."""
+    g = torch.Generator(device="cuda").manual_seed(E)
+    z = torch.randn((2, 37, E), device="cuda", generator=g)
+    z[:, ::3] = 0.25
+    z[:, ::6, ::50] = 0.5
+    z[0, 9] = -torch.inf
+    z[0, 9, 3::7] = -1.0
+    z[1, 4, : E // 2] = 1.0 + 1e-7 * torch.randint(0, 3, (E // 2,), device="cuda", generator=g)
+    b = torch.zeros(E, device="cuda")
+    check_forward(z, k, b, None, score, True)
+    b[5:40] = 3e-8 * torch.randint(0, 4, (35,), device="cuda", generator=g)
+    check_forward(z, k, b, None, score, False)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_masked_experts_tokens_and_sequences(score):
     """-inf experts, rows without any, padded rows of NaN and of inf, a sequence without a token."""
     z, b, v = make(4, 21, 48, F32, 3, True, True)
