@@ -308,7 +308,15 @@ struct Places {
   __device__ __forceinline__ void read(v8h (&x)[2][kN], uint32_t base, int first) const {
     if constexpr (kCols) {
       v4s r[2][kN][2];
-      if constexpr (kN == 2) {
+      if constexpr (kN == 1) {
+        asm volatile(
+            "ds_read_b64_tr_b16 %0, %4 offset:0\n\tds_read_b64_tr_b16 %1, %4 offset:1024\n\t"
+            "ds_read_b64_tr_b16 %2, %4 offset:4096\n\tds_read_b64_tr_b16 %3, %4 offset:5120\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(r[0][0][0]), "=&v"(r[0][0][1]), "=&v"(r[1][0][0]), "=&v"(r[1][0][1])
+            : "v"(base + at[first + 0])
+            : "memory");
+      } else if constexpr (kN == 2) {
         asm volatile(
             "ds_read_b64_tr_b16 %0, %8 offset:0\n\tds_read_b64_tr_b16 %1, %8 offset:1024\n\t"
             "ds_read_b64_tr_b16 %2, %9 offset:0\n\tds_read_b64_tr_b16 %3, %9 offset:1024\n\t"
@@ -359,7 +367,14 @@ struct Places {
           x[h][f] = __builtin_bit_cast(v8h, __builtin_shufflevector(r[h][f][0], r[h][f][1], 0, 1, 2, 3, 4, 5, 6, 7));
     } else {
       base += first * 2048;
-      if constexpr (kN == 2) {
+      if constexpr (kN == 1) {
+        asm volatile(
+            "ds_read_b128 %0, %2 offset:0\n\tds_read_b128 %1, %3 offset:0\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(x[0][0]), "=&v"(x[1][0])
+            : "v"(base + at[0]), "v"(base + at[1])
+            : "memory");
+      } else if constexpr (kN == 2) {
         asm volatile(
             "ds_read_b128 %0, %4 offset:0\n\tds_read_b128 %1, %4 offset:2048\n\t"
             "ds_read_b128 %2, %5 offset:0\n\tds_read_b128 %3, %5 offset:2048\n\t"
@@ -421,7 +436,7 @@ __device__ __forceinline__ void in_order() { asm volatile("" ::: "memory"); }
 template <int kTile>
 struct Tile {
   static constexpr int kM = kTile / 64, kN = kTile / 32;  // fragments of a wave
-  static constexpr int kLds = kTile == 192 ? 18 * kPanel : 16 * kPanel;
+  static constexpr int kLds = kTile == 192 ? 18 * kPanel : kTile == 64 ? 10 * kPanel : 16 * kPanel;
   v4f acc[kM][kN];
   __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -552,45 +567,50 @@ __device__ __forceinline__ void multiply(Tile<192> &t, const Source<kPCols> &p, 
   wait_copies<0>();
 }
 
-// Tiles of 128, for few of them: four buffers, every wave in step, so that three stages are in flight.
-template <bool kPCols, bool kQCols>
-__device__ __forceinline__ void multiply(Tile<128> &t, const Source<kPCols> &p, const Source<kQCols> &q, uint8_t *lds) {
-  uint8_t *const b_0 = lds, *const b_1 = lds + 4 * kPanel, *const b_2 = lds + 8 * kPanel, *const b_3 = lds + 12 * kPanel;
+// Tiles of 128 and of 64, for few of them: what counts is the time until a stage arrives.  Four buffers for whole
+// stages (128 KB) or five (80 KB, two workgroups per CU), every wave in step, all but one stage in flight.  With
+// eight buffers and one workgroup tiles of 64 took 11.0 instead of 8.6 us (C X of 256 x 7168).
+template <int kTile, bool kPCols, bool kQCols>
+__device__ __forceinline__ void multiply_ring(Tile<kTile> &t, const Source<kPCols> &p, const Source<kQCols> &q, uint8_t *lds) {
+  constexpr int kPanels = kTile / 64, kStage = 2 * kPanels * kPanel, kRing = Tile<kTile>::kLds / kStage;
+  constexpr int kM = Tile<kTile>::kM, kN = Tile<kTile>::kN;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const Places<kPCols, 2> at_p((wave >> 1) * 2);
-  const Places<kQCols, 4> at_q((wave & 1) * 4);
+  const Places<kPCols, kM> at_p((wave >> 1) * kM);
+  const Places<kQCols, kN> at_q((wave & 1) * kN);
   auto copy = [&](int s, uint8_t *to) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) p.copy(s, i, to + i * kPanel);
+    for (int i = 0; i < kPanels; ++i) p.copy(s, i, to + i * kPanel);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) q.copy(s, i, to + (2 + i) * kPanel);
+    for (int i = 0; i < kPanels; ++i) q.copy(s, i, to + (kPanels + i) * kPanel);
   };
   t.clear();
-  copy(0, b_0);
-  in_order();
-  copy(1, b_1);
-  in_order();
-  copy(2, b_2);
-  auto stage = [&](int s, uint8_t *cur, uint8_t *free) {
-    wait_copies<8>();
+#pragma unroll
+  for (int s = 0; s + 1 < kRing; ++s) {
+    copy(s, lds + s * kStage);
+    in_order();
+  }
+  int cur = 0, free = (kRing - 1) * kStage;
+  for (int s = 0; s < p.stages; ++s) {
+    wait_copies<(kRing - 2) * 2 * kPanels>();
     meet();  // the stage has landed, and every wave has read the one before it
-    copy(s + 3, free);
-    v8h a[2][2], b[2][4];
-    at_p.read(a, lds_address(cur), 0);
-    at_q.read(b, lds_address(cur + 2 * kPanel), 0);
-    t.add<4>(a, b, 0);
-  };
-  for (int s = 0;;) {
-    stage(s, b_0, b_3);
-    if (++s == p.stages) break;
-    stage(s, b_1, b_0);
-    if (++s == p.stages) break;
-    stage(s, b_2, b_1);
-    if (++s == p.stages) break;
-    stage(s, b_3, b_2);
-    if (++s == p.stages) break;
+    copy(s + kRing - 1, lds + free);
+    v8h a[2][kM], b[2][kN];
+    at_p.read(a, lds_address(lds) + cur, 0);
+    at_q.read(b, lds_address(lds) + cur + kPanels * kPanel, 0);
+    t.template add<kN>(a, b, 0);
+    free = cur;
+    cur = cur == (kRing - 1) * kStage ? 0 : cur + kStage;
   }
   wait_copies<0>();
+}
+
+template <bool kPCols, bool kQCols>
+__device__ __forceinline__ void multiply(Tile<128> &t, const Source<kPCols> &p, const Source<kQCols> &q, uint8_t *lds) {
+  multiply_ring(t, p, q, lds);
+}
+template <bool kPCols, bool kQCols>
+__device__ __forceinline__ void multiply(Tile<64> &t, const Source<kPCols> &p, const Source<kQCols> &q, uint8_t *lds) {
+  multiply_ring(t, p, q, lds);
 }
 
 // The lane's first row and column in the tile; fragment (i, j) is 16 i rows and 16 j columns further.
@@ -999,14 +1019,23 @@ struct Layout {
   }
 };
 
-// Tile size with the least time by rounds over the CUs.
+// The tile size with the least time, by rounds over the CUs: smaller tiles fill them better and need more of the
+// operands' bytes per product.  Whole calls (5 steps), in us, with all products in tiles of one size and by this rule:
+//                  256    192    128     64   rule
+//   300 x 1000     349    288    162     98     98
+//   1400 x 1400    569    465    266    181    181
+//   2000 x 2000    736    583    354    434    358
+//   16 x 512 x 512 367    296    176    199    175
+//   2304 x 5000   1035   1037    804   1017    673
+//   4096 x 7168   2206   2495   3086   4161   2148
+// (A of the last: 253 tiles of 192 in 132 us, 136 of 256 in 156.)
 template <class Units>
 int tile_for(Units units, int64_t cus) {
   int best = 256;
   double least = 0;
-  for (int tile : {256, 192, 128}) {
+  for (int tile : {256, 192, 128, 64}) {
     const double rounds = static_cast<double>((units(tile) + cus - 1) / cus);
-    const double time = rounds * tile * tile * (tile == 256 ? 1.0 : tile == 192 ? 1.1 : 1.4);
+    const double time = rounds * tile * tile * (tile == 256 ? 1.0 : tile == 192 ? 1.1 : tile == 128 ? 1.4 : 2.5);
     if (least == 0 || time < least) {
       least = time;
       best = tile;
@@ -1021,8 +1050,10 @@ void with_tile(int tile, F f) {
     f(std::integral_constant<int, 256>{});
   else if (tile == 192)
     f(std::integral_constant<int, 192>{});
-  else
+  else if (tile == 128)
     f(std::integral_constant<int, 128>{});
+  else
+    f(std::integral_constant<int, 64>{});
 }
 
 hipError_t run(const Layout &w, const Update &u, bool f32, const Coefficients &co, int64_t steps, const Result &res,
@@ -1060,26 +1091,31 @@ hipError_t run(const Layout &w, const Update &u, bool f32, const Coefficients &c
   auto tiles = [](int64_t size, int tile) { return (size + tile - 1) / tile; };
   auto triangle_units = [&](int tile) { return w.G * tiles(w.m, tile) * (tiles(w.m, tile) + 1) / 2; };
   auto apply_units = [&](int tile) { return w.G * tiles(w.Pp, tile) * tiles(w.Qp, tile); };
-  const int sym = w.splits > 1 ? 128 : tile_for(triangle_units, cus), app = tile_for(apply_units, cus);
+  const int square = tile_for(triangle_units, cus), sym = w.splits > 1 ? 128 : square, app = tile_for(apply_units, cus);
   auto grid_of = [](int64_t units) { return dim3(static_cast<uint32_t>((units + 7) / 8 * 8)); };
   for (int64_t s = 0; s < steps; ++s) {
     x.hi = halves(w.hi[s & 1]);
     x.next = halves(w.hi[(s + 1) & 1]);
+    auto symmetric = [&](auto kernel, int tile, const _Float16 *from, int64_t ld, int64_t K, const float *d_in, _Float16 *to,
+                         int64_t splits) {
+      hipLaunchKernelGGL(kernel, grid_of(triangle_units(tile) * splits), dim3(kThreads), 0, stream, from, ld, K, w.m, G, d_in,
+                         co, to, floats(w.da), reinterpret_cast<float2 *>(ws + w.dc), static_cast<int>(splits),
+                         floats(w.parts));
+    };
     with_tile(sym, [&](auto tile) {
       constexpr int kT = decltype(tile)::value;
-      auto go = [&](auto kernel, const _Float16 *from, int64_t ld, int64_t K, const float *d_in, _Float16 *to, int64_t splits) {
-        hipLaunchKernelGGL(kernel, grid_of(triangle_units(kT) * splits), dim3(kThreads), 0, stream, from, ld, K, w.m, G, d_in, co, to,
-                           floats(w.da), reinterpret_cast<float2 *>(ws + w.dc), static_cast<int>(splits), floats(w.parts));
-      };
       if (tall)
-        go(muon_symmetric_kernel<kT, false, true>, x.hi, w.Qp, w.Pp, nullptr, halves(w.a), w.splits);
+        symmetric(muon_symmetric_kernel<kT, false, true>, kT, x.hi, w.Qp, w.Pp, nullptr, halves(w.a), w.splits);
       else
-        go(muon_symmetric_kernel<kT, false, false>, x.hi, w.Qp, w.Qp, nullptr, halves(w.a), w.splits);
-      if (w.splits > 1)
-        hipLaunchKernelGGL(muon_sum_kernel, dim3(16, static_cast<uint32_t>(w.G * w.tiles)), dim3(256), 0, stream,
-                           floats(w.parts), static_cast<int>(w.splits), w.m, static_cast<int>(w.m / 128), halves(w.a),
-                           floats(w.da));
-      go(muon_symmetric_kernel<kT, true, false>, halves(w.a), w.m, w.m, floats(w.da), halves(w.c), 1);
+        symmetric(muon_symmetric_kernel<kT, false, false>, kT, x.hi, w.Qp, w.Qp, nullptr, halves(w.a), w.splits);
+    });
+    if (w.splits > 1)
+      hipLaunchKernelGGL(muon_sum_kernel, dim3(16, static_cast<uint32_t>(w.G * w.tiles)), dim3(256), 0, stream,
+                         floats(w.parts), static_cast<int>(w.splits), w.m, static_cast<int>(w.m / 128), halves(w.a),
+                         floats(w.da));
+    with_tile(square, [&](auto tile) {
+      constexpr int kT = decltype(tile)::value;
+      symmetric(muon_symmetric_kernel<kT, true, false>, kT, halves(w.a), w.m, w.m, floats(w.da), halves(w.c), 1);
     });
     with_tile(app, [&](auto tile) {
       constexpr int kT = decltype(tile)::value;
@@ -1104,7 +1140,7 @@ int64_t muon_workspace(int64_t G, int64_t P, int64_t Q) { return Layout(G, P, Q)
 
 bool muon_grids_fit(int64_t G, int64_t P, int64_t Q) {
   const Layout w(G, P, Q);
-  const int64_t units = (w.Pp / 128) * (w.Qp / 128);  // the smallest tiles, of which a triangle has fewer
+  const int64_t units = (w.Pp / 64) * (w.Qp / 64);  // the smallest tiles, of which a triangle has fewer
   return G <= 65535 && grid_fits(w.count, 256) && units < (int64_t(1) << 31) / kThreads &&
          grid_fits(G * units + 8, kThreads);
 }

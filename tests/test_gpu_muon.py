@@ -107,6 +107,15 @@ def test_larger_tiles(shape):
     assert (off <= torch.sqrt(inside ** 2 + (norm * 0.6 * 2.0 ** -8) ** 2)).all()
 
 
+@pytest.mark.parametrize("shape", [(16, 512, 512), (16, 600, 512), (12, 600, 500), (32, 1000, 500), (85, 600, 512)])
+def test_tiles_of_128_and_tall_ones_of_256(shape):
+    """Batches of a few hundred tiles of 128, and tall matrices' tiles of 256."""
+    x = matrices(shape, "strong", BF16, 4)
+    e, norm, inside = allowed(x)
+    off = (fq.fp8q_orthogonalize(x).double() - e).flatten(-2).norm(dim=-1)
+    assert (off <= torch.sqrt(inside ** 2 + (norm * 0.6 * 2.0 ** -8) ** 2)).all()
+
+
 @pytest.mark.parametrize("steps,abc", [(1, ABC), (2, ABC), (8, ABC), (12, (1.875, -1.25, 0.375)), (3, (1.5, -0.5, 0.0))])
 def test_steps_and_coefficients(steps, abc):
     for shape in ((90, 150), (150, 90)):
