@@ -6,18 +6,27 @@
 //   p = p (1 - lr weight_decay) - lr scale X.
 // X has the smaller of the two sizes, m, as its rows (n columns): tall matrices are worked on transposed.
 //
-// Three matrix products per step, all as P Q^T of operands with contiguous rows, on the FP16 matrix
-// instructions: A (lower triangle of tiles, mirrored), C = a I + b A + c A^2 (likewise), C X with X^T kept
-// beside X.  5 steps of 4096 x 7168: 2 (m^2 n / 2 + m^3 / 2 + m^2 n) flops each = 2.1e12 in all.
+// Three matrix products per step on the FP16 matrix instructions: A and C = a I + b A + c A^2, of which only the
+// lower triangle of tiles is computed and mirrored, and C X (tall: X C).  5 steps of 4096 x 7168:
+// 2 (m^2 n / 2 + m^3 / 2 + m^2 n) flops each = 2.1e12 in all.  X stays in the orientation of the matrix, once: the
+// product that contracts over its columns reads it by rows, the other by columns (LDS's transposing reads).
 //
 // Numerics.  FP16 has 11 significant bits, three more than BF16, and its range is no matter: |X|_2 stays
 // below 1.3 and operands are scaled by 2^12.  Rounding X itself to 11 bits would drown the small singular
 // values beside strong directions (a rank-1 matrix with a floor of noise: 1e-2 of the result's norm), as
-// would rounding a + b A_ii + ..., where the terms cancel.  So X is kept in 22 bits, as two FP16 numbers;
-// the diagonals of A and C are kept in FP32 apart from the matrices, whose diagonals are zero; and the
-// diagonal's part of C X is formed from the 22 bits in FP32.  Products see 11 bits of what is off
-// the diagonal.  Result: 1e-4 to 9e-4 of its norm off (normal, rank-1 and rank-16 matrices with noise),
-// less than the rounding to BF16 (1.7e-3).
+// would rounding a + b A_ii + ..., where the terms cancel.  So X is kept in 15 bits, hi in FP16 and the rest lo in
+// E4M3 (behind those the products' own 11 bits lose more, and FP16 would be another byte per element to read and
+// write each step), the diagonal of A in FP32 apart from A, whose own is zero, and that of C in FP32 beside its rounded one.
+// The products see hi and 11 bits of what is off the diagonal; lo and the diagonal's rest come in with FP32
+// factors afterwards (muon_apply_kernel).  Result: 1e-4 to 9e-4 of its norm off (normal, rank-1 and rank-16
+// matrices with noise), less than the rounding to BF16 (1.7e-3).
+//
+// What bounds it.  Large: the matrix cores at the clock that the power limit leaves.  32 x 4096 x 7168 in 18.0 ms:
+// C X 1.83 ms (1.05 PFLOP/s), of which the sums alone take 1.35 (1.41, what a large library product reaches) and
+// lo, the factors and the stores the rest; A 0.88, C 0.34, momentum and norm 0.91 (HBM), first X 0.80, the last
+// C X with the parameters 2.74.  Reading lo after the products (1.89), storing hi without LDS (1.89), starting the
+// CUs apart (1.83) and reading the parameters two rows ahead (3.24) did not help.  Small: the launches, each 4 to
+// 9 us and none able to start before the one before it has ended.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>

@@ -12,6 +12,9 @@
 // one; the weights stay in registers too.  All sums are FP32, in an order that depends on the sizes
 // only, with one rounding of each result.
 //
+// 16384 x 7168 from FP32 to BF16: 133 us, 5.3 TB/s (a copy kernel of this card's best 6.16 TB/s: 114).  Gradient of
+// 8192 x 7168 in BF16: 61 us, 5.7 TB/s (with one row on its way and cached loads 80), and 5 us for the sums.
+//
 // dw and db: every workgroup of the backward kernel keeps its rows' sums in registers and leaves
 // them in the workspace, 4 H bytes each; a second kernel adds up at most kNormGroups of them.
 #include <hip/hip_runtime.h>

@@ -21,8 +21,12 @@
 //
 // A group of 16 lanes takes a token of up to 256 experts, 64 lanes one of up to 1024, 4 to 16
 // logits per lane in registers: the maxima of a top-k step are 4 DPP steps inside a row of lanes, and
-// one instruction works for 4 tokens.  Logits are read once (8 MB for 8192 tokens x 256 experts,
-// under 2 us of HBM time), so the top-k's instructions bound the call.
+// one instruction works for 4 tokens.  Logits are read once (16 MB for 16384 tokens x 256 experts,
+// 3 us of HBM time), so the top-k's instructions bound the call: 32 us there with sigmoid scores and a bias, of
+// which the 64 tokens of a small batch take 14.6.  With all 256 experts ranked in 64 bits for the tokens that
+// FP32 leaves open it took 41.  Counts and sums of p stay in a workgroup's LDS and registers; a second launch
+// (4 to 7 us) adds them up to slope and loss.
+// The gradient reads and writes 33 MB in 14 us.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>

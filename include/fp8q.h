@@ -562,12 +562,14 @@ fp8q_status fp8q_moe_route_backward(const void *logits, int32_t dtype, int64_t B
  *   X = U / |U|_F;  A = X X^T,  X = (a I + b A + c A^2) X.
  * (This library's reading of a training step's optimizer; the pages name none for matrices.)
  * X, A and C = a I + b A + c A^2 are multiplied as FP16 with FP32 sums (11 significant bits of what is off the
- * diagonals; the diagonals in FP32, X itself kept in 22 bits): the result is off by 1e-4 to 1e-3 of its norm.  |U|_F is
- * summed in 64 bits.  Coefficients must keep every singular value below 15 in between (those here keep
- * them below 1.3), or the result is not finite.  U is finite; a matrix of zeros gives zeros.
+ * diagonals; the diagonals in FP32, X itself kept in 15 bits): the result is off by 1e-4 to 1e-3 of its norm, up to 4e-3
+ * where singular values lie a factor of 500 and more below the norm.  |U|_F is summed in 64 bits.  Coefficients must
+ * keep every singular value below 15 in between (those here keep them below 1.3), or the result is not finite.
+ * U is finite; a matrix of zeros gives zeros.
  *   ns : HOST struct, read during the call only; 1 <= steps <= 100; usual: {3.4445, -4.7750, 2.0315, 5}
- *   workspace : fp8q_muon_workspace(G, P, Q) bytes: about 8 per element of the matrices (their sizes rounded up to
- *               128) and 4 per element of the G square matrices of the smaller size; written
+ *   workspace : fp8q_muon_workspace(G, P, Q) bytes: about 5 per element of the matrices (their sizes rounded up to
+ *               128) and 4 per element of the G square matrices of the smaller size (few long ones: and up to 8 MB
+ *               for the parts of A); written
  */
 typedef struct {
   double a, b, c;
@@ -578,8 +580,8 @@ typedef struct {
  * out = the matrices x made orthogonal.
  *   x : [G][P][Q] BF16 or FP32 per dtype;  out_bf16 : [G][P][Q] (out)
  * Requires G >= 1, 0 <= P, Q <= 2^20 (and G P Q such that the grids fit).  P == 0 or Q == 0 is a no-op.
- * 2 + 3 steps launches.  Errors: FP8Q_ERR_DTYPE, FP8Q_ERR_SHAPE, FP8Q_ERR_VALUE, FP8Q_ERR_NULL, FP8Q_ERR_ALIGN,
- * FP8Q_ERR_DEVICE, FP8Q_ERR_LAUNCH.
+ * 2 + 3 steps launches (2 + 4 steps for few long matrices).  Errors: FP8Q_ERR_DTYPE, FP8Q_ERR_SHAPE, FP8Q_ERR_VALUE,
+ * FP8Q_ERR_NULL, FP8Q_ERR_ALIGN, FP8Q_ERR_DEVICE, FP8Q_ERR_LAUNCH.
  */
 fp8q_status fp8q_orthogonalize(const void *x, int32_t dtype, int64_t G, int64_t P, int64_t Q,
                                const fp8q_newton_schulz *ns, uint16_t *out_bf16, void *workspace, void *stream);
