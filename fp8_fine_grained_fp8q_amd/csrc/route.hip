@@ -328,10 +328,10 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(const RouteArg
                       expert_of<kLanes>(l, v));
       // A sigmoid in FP32 is off by less than 2^-21.5 of itself, a softmax by 2^-24 (12 + |z - top|), their sums with
       // the bias by 2^-24: 2^-19 and 2^-17 cover two of them, the latter down to scores of e^-50, and the
-      // floor covers the smaller ones.
+      // floor covers the smaller ones.  Scores end at 1, so a far larger bias (an expert's mask) adds nothing to it.
       const float near = a.bias == nullptr ? 0.0f : (kSoftmax ? 0x1p-17f : 0x1p-19f);
       int found;
-      const bool close = select<kLanes, kV>(key, k, l, ids, near, 2.0f * far + 1e-16f, found);
+      const bool close = select<kLanes, kV>(key, k, l, ids, near, fminf(2.0f * far + 1e-16f, 2.0f), found);
       if (__any(close)) {
         wave_sync();
         double total = 1.0;

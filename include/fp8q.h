@@ -523,7 +523,7 @@ enum { FP8Q_SCORE_SOFTMAX = 0, FP8Q_SCORE_SIGMOID = 1 };
  *   logits : [B][S][E] BF16 or FP32 per dtype, finite or -inf (otherwise the token's weights, the
  *            sequence's slope and the loss are unspecified; ids stay below E); an expert with logit -inf
  *            is not chosen, slots left over get id -1 and weight 0
- *   bias : [E] FP32 or NULL;  valid : [B][S] bytes, 0 for a token that does not count, or NULL
+ *   bias : [E] FP32, finite or -inf (such an expert is not chosen), or NULL;  valid : [B][S] bytes, 0 for a token that does not count, or NULL
  *          A token that does not count, or whose logits are all -inf, gets ids -1 and weights 0 and
  *          enters neither counts nor loss; its logits are not used (they may be NaN).
  *   topk_ids int32, topk_weights FP32 : [B][S][k] (out);  counts int32, slope FP32 : [B][E] (out);  loss : FP32 (out)

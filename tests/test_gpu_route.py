@@ -156,6 +156,25 @@ def test_masked_experts_tokens_and_sequences(score):
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("mask", [-torch.inf, torch.finfo(F32).min, -1e9, -30.0])
+def test_experts_masked_by_their_bias(score, mask):
+    """Half of the experts with a bias that keeps them from being chosen, and more slots than the others fill."""
+    z, b, v = make(2, 70, 200, F32, 11, True, True)
+    b[1::2] = mask
+    ids, w, *_ = check_forward(z, 8, b, v, score, True)
+    assert not (ids[v] & 1).any()
+    b[4:] = mask
+    if mask > -torch.inf:  # those are taken in their order all the same
+        check_forward(z, 8, b, v, score, True)
+        return
+    b[1] = 0.0
+    ids, w, counts, loss, slope = fq.fp8q_moe_route(z, 8, b, v, score=score, balance=0.01)
+    assert (ids[v][:, 3:] == -1).all() and not w[v][:, 3:].any() and (ids[~v] == -1).all()
+    assert (ids[v][:, :3].sort(-1).values == torch.tensor([0, 1, 2], device="cuda")).all()
+    assert torch.isfinite(w).all() and torch.isfinite(loss).all() and (counts[:, :3] == v.sum(1, keepdim=True)).all()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_far_logits(score):
     """Normalized weights of chosen experts whose scores vanish together in FP32 stay finite."""
     z = -200.0 - torch.arange(24.0, device="cuda").repeat(1, 5, 1)
