@@ -21,7 +21,7 @@
 // factors afterwards (muon_apply_kernel).  Result: 1e-4 to 9e-4 of its norm off (normal, rank-1 and rank-16
 // matrices with noise), less than the rounding to BF16 (1.7e-3).
 //
-// What bounds it.  Large: the matrix cores at the clock that the power limit leaves.  32 x 4096 x 7168 in 18.0 ms:
+// What bounds it.  Large: the matrix cores at the clock that the power limit leaves.  32 x 7168 x 2048 in 18.0 ms:
 // C X 1.83 ms (1.05 PFLOP/s), of which the sums alone take 1.35 (1.41, what a large library product reaches) and
 // lo, the factors and the stores the rest; A 0.88, C 0.34, momentum and norm 0.91 (HBM), first X 0.80, the last
 // C X with the parameters 2.74.  Reading lo after the products (1.89), storing hi without LDS (1.89), starting the
