@@ -154,26 +154,26 @@ __device__ __forceinline__ int64_t low_place(int64_t c) {
   return (c & ~int64_t(63)) + 16 * ((c >> 2) & 3) + 4 * ((c >> 4) & 3);
 }
 
-// Four values as hi and lo.
+// Four values at lo's scale (kLow times hi's) as hi and lo.
 __device__ __forceinline__ v4h split(v4f v, uint32_t &lo) {
   v4h hi;
   v4f rest;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) hi[k] = static_cast<_Float16>(v[k]);
+  for (int k = 0; k < 4; ++k) hi[k] = static_cast<_Float16>(v[k] * (1.0f / kLow));
   // One rounding for both: the compiler may round a product or sum twice for one of two conversions and once
   // for the other, and where these differ lo would belong to another hi.
   asm volatile("" : "+v"(hi));
 #pragma unroll
-  for (int k = 0; k < 4; ++k) rest[k] = (v[k] - static_cast<float>(hi[k])) * kLow;
+  for (int k = 0; k < 4; ++k) rest[k] = __builtin_fmaf(static_cast<float>(hi[k]), -kLow, v[k]);
   lo = pack4_e4m3(rest[0], rest[1], rest[2], rest[3]);
   return hi;
 }
 
-// lo at hi's scale.
+// lo at its scale.
 __device__ __forceinline__ v4f low_of(uint32_t lo) {
   const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(lo), false);
   const f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(lo), true);
-  return v4f{a.x, a.y, b.x, b.y} * (1.0f / kLow);
+  return v4f{a.x, a.y, b.x, b.y};
 }
 
 // Workgroup (x, y, z): 16 rows of 256 columns of matrix z, and every gridDim.y-th 16 after them.
@@ -188,10 +188,10 @@ __global__ __launch_bounds__(256) void muon_start_kernel(const Update u, const d
   if ((threadIdx.x & 63) == 0) waves[threadIdx.x >> 6] = sum;
   __syncthreads();
   sum = (waves[0] + waves[1]) + (waves[2] + waves[3]);
-  // kScale / |U| as a power of two, which may lie outside FP32, and a factor of 1/2 to 1: FP64 products cost twice
+  // kLow kScale / |U| as a power of two, which may lie outside FP32, and a factor of 1/2 to 1: FP64 products cost twice
   // the time of the copy.
   int power = 0;
-  const float factor = sum > 0.0 ? static_cast<float>(frexp(static_cast<double>(kScale) / sqrt(sum), &power)) : 0.0f;
+  const float factor = sum > 0.0 ? static_cast<float>(frexp(static_cast<double>(kLow * kScale) / sqrt(sum), &power)) : 0.0f;
 
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 256 + (threadIdx.x & 63) * 4;
   if (c >= x.Qp) return;
@@ -839,13 +839,13 @@ __device__ __forceinline__ v4f old_param(const Result &res, int64_t g, int64_t i
   return *reinterpret_cast<const v4f *>(res.param + (g * res.P + i) * res.Q + j);
 }
 
-// The result there, from kScale X and old_param's.
+// The result there, from kLow kScale X and old_param's.
 __device__ __forceinline__ void finish(const Result &res, int64_t g, int64_t i, int64_t j, v4f v, v4f p, float keep,
                                        float step) {
   if (i >= res.P) return;
   const int64_t at = (g * res.P + i) * res.Q + j;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) v[k] *= 1.0f / kScale;
+  for (int k = 0; k < 4; ++k) v[k] *= 1.0f / (kLow * kScale);
   if ((res.Q & 3) == 0) {
     if (j >= res.Q) return;
     if (res.param == nullptr) {
@@ -946,7 +946,7 @@ __global__ __launch_bounds__(kThreads, 2) void muon_apply_kernel(const _Float16 
         const v4f rest = low_of(low[i][j / kWide][j % kWide]);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          t.acc[i][j][k] = __builtin_fmaf(by[k], rest[k], t.acc[i][j][k] * (turn[k] * (1.0f / kScale)));
+          t.acc[i][j][k] = __builtin_fmaf(by[k], rest[k], t.acc[i][j][k] * (turn[k] * (kLow / kScale)));
       }
     }
   } else {
@@ -957,7 +957,7 @@ __global__ __launch_bounds__(kThreads, 2) void muon_apply_kernel(const _Float16 
         const v4f rest = low_of(low[i][j / kWide][j % kWide]);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          t.acc[i][j][k] = __builtin_fmaf(d_row[i].x, rest[k], t.acc[i][j][k] * (d_row[i].y * (1.0f / kScale)));
+          t.acc[i][j][k] = __builtin_fmaf(d_row[i].x, rest[k], t.acc[i][j][k] * (d_row[i].y * (kLow / kScale)));
       }
   }
 #pragma unroll
