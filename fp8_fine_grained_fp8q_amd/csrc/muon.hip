@@ -22,10 +22,10 @@
 // matrices with noise), less than the rounding to BF16 (1.7e-3).
 //
 // What bounds it.  Large: the matrix cores at the clock that the power limit leaves.  32 x 7168 x 2048 in 18.0 ms:
-// C X 1.83 ms (1.05 PFLOP/s), of which the sums alone take 1.35 (1.41, what a large library product reaches) and
+// C X 1.78 ms (1.08 PFLOP/s), of which the sums alone take 1.35 (1.41, what a large library product reaches) and
 // lo, the factors and the stores the rest; A 0.88, C 0.34, momentum and norm 0.91 (HBM), first X 0.80, the last
 // C X with the parameters 2.74.  Reading lo after the products (1.89), storing hi without LDS (1.89), starting the
-// CUs apart (1.83) and reading the parameters two rows ahead (3.24) did not help.  Small: the launches, each 4 to
+// CUs apart (no gain) and reading the parameters two rows ahead (3.24) did not help.  Small: the launches, each 4 to
 // 9 us and none able to start before the one before it has ended.
 #include <hip/hip_runtime.h>
 #include <math.h>
@@ -746,7 +746,7 @@ __global__ __launch_bounds__(kThreads, 2) void muon_symmetric_kernel(const _Floa
   if constexpr (kSquare && kTile != 256) read_own();
   in_order();
   Tile<kTile> t;
-  if constexpr (kTile == 128 && !kSquare) {
+  if constexpr (kTile == 64 && !kSquare) {
     const int stages = static_cast<int>(K / 64), first = stages * part / splits;
     const int count = stages * (part + 1) / splits - first;
     multiply(t, Source<kCols>(x, r0, m, kTile, ld, K, first, count), Source<kCols>(x, c0, m, kTile, ld, K, first, count),
@@ -797,18 +797,18 @@ __global__ __launch_bounds__(kThreads, 2) void muon_symmetric_kernel(const _Floa
   store_block<kTile>(h, lds, out + g * m * m, r0, c0, m, m, m, ti != tj);
 }
 
-// A and its diagonal from the parts of its tiles of 128: workgroup (x, y) takes 8 rows of tile y of all.
+// A and its diagonal from the parts of its tiles of 64: workgroup (x, y) takes 16 rows of tile y of all.
 __global__ __launch_bounds__(256) void muon_sum_kernel(const float *__restrict__ parts, int splits, int64_t m, int tiles,
                                                        _Float16 *__restrict__ out, float *__restrict__ diagonal) {
   const int per = tiles * (tiles + 1) / 2, g = blockIdx.y / per;
   int ti, tj;
   triangle(blockIdx.y % per, ti, tj);
-  const int row = blockIdx.x * 8 + (threadIdx.x >> 5), col = (threadIdx.x & 31) * 4;
-  const float *from = parts + static_cast<int64_t>(blockIdx.y) * splits * (128 * 128) + row * 128 + col;
+  const int row = blockIdx.x * 16 + (threadIdx.x >> 4), col = (threadIdx.x & 15) * 4;
+  const float *from = parts + static_cast<int64_t>(blockIdx.y) * splits * (64 * 64) + row * 64 + col;
   v4f sum = {};
 #pragma unroll 8
-  for (int s = 0; s < splits; ++s) sum += *reinterpret_cast<const v4f *>(from + s * (128 * 128));
-  const int64_t i = ti * 128 + row, j = tj * 128 + col;
+  for (int s = 0; s < splits; ++s) sum += *reinterpret_cast<const v4f *>(from + s * (64 * 64));
+  const int64_t i = ti * 64 + row, j = tj * 64 + col;
   _Float16 *const o = out + g * m * m;
   v4h h;
 #pragma unroll
@@ -991,11 +991,11 @@ __global__ __launch_bounds__(kThreads, 2) void muon_apply_kernel(const _Float16 
 }
 
 // The workspace: sums of squares, X (hi twice, lo), A, C and their diagonals.
-constexpr int64_t kFewTiles = 128;  // tiles and their parts that do not fill half of the CUs
+constexpr int64_t kFewTiles = 256;  // tiles of 64 and their parts, one for each CU
 
 struct Layout {
   int64_t G, P, Q, Pp, Qp, m, count;  // count: workgroups that sum a matrix's squares
-  int64_t tiles, splits;              // of a matrix's A in tiles of 128, and parts of each
+  int64_t tiles, splits;              // of a matrix's A in tiles of 64, and parts of each
   int64_t sums, hi[2], lo, a, c, da, dc, parts, bytes;
   Layout(int64_t G, int64_t P, int64_t Q) : G(G), P(P), Q(Q) {
     Pp = padded(P);
@@ -1018,12 +1018,14 @@ struct Layout {
     c = take(2 * G * m * m);
     da = take(4 * G * m);
     dc = take(8 * G * m);
-    // A long sum of few tiles is split, at least 8 stages each.  256 x 7168 (3 tiles, 112 stages): 51 -> 14 us.
-    tiles = (m / 128) * (m / 128 + 1) / 2;
+    // A long sum of few tiles is split, at least 4 stages each.  Whole calls: 256 x 7168 (10 tiles, 112 stages) 122 us (in
+    // tiles of 128 144), 896 x 7168 (105 tiles in 2 parts) 276 (in one 308); two parts for each CU 384 x 7168 143 -> 147.
+    // Sums of less than 32 stages are over before muon_sum_kernel's launch would pay.
+    tiles = (m / 64) * (m / 64 + 1) / 2;
     const int64_t stages = (Pp < Qp ? Qp : Pp) / 64, room = kFewTiles / (tiles * G);
-    splits = stages / 8 < room ? stages / 8 : room;
-    splits = splits < 4 ? 1 : (splits > 16 ? 16 : splits);
-    parts = take(splits > 1 ? 4 * 128 * 128 * G * tiles * splits : 0);
+    splits = stages / 4 < room ? stages / 4 : room;
+    splits = stages < 32 || splits < 2 ? 1 : (splits > 16 ? 16 : splits);
+    parts = take(splits > 1 ? 4 * 64 * 64 * G * tiles * splits : 0);
     bytes = at;
   }
 };
@@ -1100,7 +1102,7 @@ hipError_t run(const Layout &w, const Update &u, bool f32, const Coefficients &c
   auto tiles = [](int64_t size, int tile) { return (size + tile - 1) / tile; };
   auto triangle_units = [&](int tile) { return w.G * tiles(w.m, tile) * (tiles(w.m, tile) + 1) / 2; };
   auto apply_units = [&](int tile) { return w.G * tiles(w.Pp, tile) * tiles(w.Qp, tile); };
-  const int square = tile_for(triangle_units, cus), sym = w.splits > 1 ? 128 : square, app = tile_for(apply_units, cus);
+  const int square = tile_for(triangle_units, cus), sym = w.splits > 1 ? 64 : square, app = tile_for(apply_units, cus);
   auto grid_of = [](int64_t units) { return dim3(static_cast<uint32_t>((units + 7) / 8 * 8)); };
   for (int64_t s = 0; s < steps; ++s) {
     x.hi = halves(w.hi[s & 1]);
@@ -1119,8 +1121,8 @@ hipError_t run(const Layout &w, const Update &u, bool f32, const Coefficients &c
         symmetric(muon_symmetric_kernel<kT, false, false>, kT, x.hi, w.Qp, w.Qp, nullptr, halves(w.a), w.splits);
     });
     if (w.splits > 1)
-      hipLaunchKernelGGL(muon_sum_kernel, dim3(16, static_cast<uint32_t>(w.G * w.tiles)), dim3(256), 0, stream,
-                         floats(w.parts), static_cast<int>(w.splits), w.m, static_cast<int>(w.m / 128), halves(w.a),
+      hipLaunchKernelGGL(muon_sum_kernel, dim3(4, static_cast<uint32_t>(w.G * w.tiles)), dim3(256), 0, stream,
+                         floats(w.parts), static_cast<int>(w.splits), w.m, static_cast<int>(w.m / 64), halves(w.a),
                          floats(w.da));
     with_tile(square, [&](auto tile) {
       constexpr int kT = decltype(tile)::value;

@@ -568,7 +568,7 @@ fp8q_status fp8q_moe_route_backward(const void *logits, int32_t dtype, int64_t B
  * U is finite; a matrix of zeros gives zeros.
  *   ns : HOST struct, read during the call only; 1 <= steps <= 100; usual: {3.4445, -4.7750, 2.0315, 5}
  *   workspace : fp8q_muon_workspace(G, P, Q) bytes: about 5 per element of the matrices (their sizes rounded up to
- *               128) and 4 per element of the G square matrices of the smaller size (few long ones: and up to 8 MB
+ *               128) and 4 per element of the G square matrices of the smaller size (few long ones: and up to 4 MB
  *               for the parts of A); written
  */
 typedef struct {
