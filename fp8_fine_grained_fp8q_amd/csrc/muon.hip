@@ -21,10 +21,10 @@
 // factors afterwards (muon_apply_kernel).  Result: 1e-4 to 9e-4 of its norm off (normal, rank-1 and rank-16
 // matrices with noise), less than the rounding to BF16 (1.7e-3).
 //
-// What bounds it.  Large: the matrix cores at the clock that the power limit leaves.  32 x 7168 x 2048 in 18.0 ms:
+// What bounds it.  Large: the matrix cores at the clock that the power limit leaves.  32 x 7168 x 2048 in 17.6 ms:
 // C X 1.78 ms (1.08 PFLOP/s), of which the sums alone take 1.35 (1.41, what a large library product reaches) and
 // lo, the factors and the stores the rest; A 0.88, C 0.34, momentum and norm 0.91 (HBM), first X 0.80, the last
-// C X with the parameters 2.74.  Reading lo after the products (1.89), storing hi without LDS (1.89), starting the
+// C X with the parameters 2.39.  Reading lo after the products (1.89), storing hi without LDS (1.89), starting the
 // CUs apart (no gain) and reading the parameters two rows ahead (3.24) did not help.  Small: the launches, each 4 to
 // 9 us and none able to start before the one before it has ended.
 #include <hip/hip_runtime.h>
@@ -46,6 +46,8 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 typedef _Float16 v4h __attribute__((ext_vector_type(4)));
 typedef short v4s __attribute__((ext_vector_type(4)));
+typedef int v2i __attribute__((ext_vector_type(2)));
+typedef int v4i __attribute__((ext_vector_type(4)));
 
 constexpr float kScale = 4096.0f;  // of X, A and C as stored
 constexpr int64_t kPad = 128;      // sizes of the stored matrices
@@ -622,6 +624,11 @@ __device__ __forceinline__ void multiply(Tile<64> &t, const Source<kPCols> &p, c
   multiply_ring(t, p, q, lds);
 }
 
+// Memory from p on, beyond whose end loads give zeros and stores write nothing.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void *p, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), static_cast<short>(0), static_cast<int>(bytes), 0x00020000);
+}
+
 // The lane's first row and column in the tile; fragment (i, j) is 16 i rows and 16 j columns further.
 template <int kTile>
 __device__ __forceinline__ void lane_place(int &row, int &col) {
@@ -872,6 +879,42 @@ __device__ __forceinline__ void finish(const Result &res, int64_t g, int64_t i, 
   }
 }
 
+// finish for a tile whose columns all lie inside the aligned parameters: rows past the last are beyond the buffers'
+// ends, and an address is a register (with 64-bit addresses and a branch for each fragment the last product of
+// 32 x 7168 x 2048 took 2.74 instead of 2.40 ms).  Two rows of fragments at a time were no faster.
+template <int kTile>
+__device__ __forceinline__ void step_rows(const Result &res, int64_t g, int64_t r0, int64_t c0, const Tile<kTile> &t,
+                                          float keep, float step) {
+  constexpr int kM = Tile<kTile>::kM, kN = Tile<kTile>::kN;
+  if (r0 >= res.P) return;
+  const int64_t first = (g * res.P + r0) * res.Q + c0, rows = res.P - r0 < kTile ? res.P - r0 : kTile;
+  const int size = static_cast<int>((rows * res.Q - c0) * 4), line = static_cast<int>(res.Q) * 4;
+  const __amdgpu_buffer_rsrc_t param = buffer(res.param + first, size);
+  const __amdgpu_buffer_rsrc_t copy = buffer(res.copy + first, res.copy != nullptr ? size / 2 : 0);
+  int row, col;
+  lane_place<kTile>(row, col);
+  const int at = row * line + col * 4;
+  step *= 1.0f / (kLow * kScale);
+#pragma unroll
+  for (int i = 0; i < kM; ++i) {
+    const int to = at + i * 16 * line;
+    v4i old[kN];
+#pragma unroll
+    for (int j = 0; j < kN; ++j) old[j] = __builtin_amdgcn_raw_buffer_load_b128(param, to, j * 64, 0);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+      v4f v = __builtin_bit_cast(v4f, old[j]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = v[k] * keep - step * t.acc[i][j][k];
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i, v), param, to, j * 64, 0);
+      const v2i half = {static_cast<int>(pack2_bf16(v[0], v[1])), static_cast<int>(pack2_bf16(v[2], v[3]))};
+      if (res.copy != nullptr) __builtin_amdgcn_raw_buffer_store_b64(half, copy, to >> 1, j * 32, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
 // Tiles of C X.  Raster: 8 tiles of rows at a time, so that an XCD's run reads few panels.
 __device__ __forceinline__ void raster(int u, int rows, int cols, int &i, int &j) {
   const int band = 8 * cols, first = u / band * 8;
@@ -959,6 +1002,12 @@ __global__ __launch_bounds__(kThreads, 2) void muon_apply_kernel(const _Float16 
         for (int k = 0; k < 4; ++k)
           t.acc[i][j][k] = __builtin_fmaf(d_row[i].x, rest[k], t.acc[i][j][k] * (d_row[i].y * (kLow / kScale)));
       }
+  }
+  if constexpr (kLast) {
+    if (res.param != nullptr && (res.Q & 3) == 0 && c0 + kTile <= res.Q) {
+      step_rows<kTile>(res, g, r0, c0, t, keep, step);
+      return;
+    }
   }
 #pragma unroll
   for (int i = 0; i < kM; ++i) {
