@@ -25,7 +25,7 @@
 // C X 1.78 ms (1.08 PFLOP/s), of which the sums alone take 1.35 (1.41, what a large library product reaches) and
 // lo, the factors and the stores the rest; A 0.88, C 0.34, momentum and norm 0.91 (HBM), first X 0.80, the last
 // C X with the parameters 2.39.  Reading lo after the products (1.89), storing hi without LDS (1.89), starting the
-// CUs apart (no gain) and reading the parameters two rows ahead (3.24) did not help.  Small: the launches, each 4 to
+// CUs apart (no gain) and lo and hi by buffer addresses (1.80) did not help.  Small: the launches, each 4 to
 // 9 us and none able to start before the one before it has ended.
 #include <hip/hip_runtime.h>
 #include <math.h>

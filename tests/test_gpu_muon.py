@@ -173,6 +173,29 @@ def test_muon(shape, nesterov):
             assert torch.equal(c, p.bfloat16())
 
 
+@pytest.mark.parametrize("shape", [(2, 70, 320), (3, 321, 128), (70, 3000), (200, 260), (260, 200), (16, 512, 512), (16, 600, 512),
+                                   (12, 600, 500), (32, 1000, 512), (32, 1000, 500), (40, 500, 900), (85, 512, 512)])
+def test_muon_over_tiles(shape):
+    """Tiles of every size, whole and cut by the matrix's right and lower edge, beside the next matrix's rows."""
+    lr, beta, decay, scale = 0.02, 0.9, 0.1, 1.5
+    n = math.prod(shape)
+    p, m = matrices(shape, "normal", F32, 1), 0.5 * matrices(shape, "strong", F32, 2)
+    g = matrices(shape, "strong", BF16, 3)
+    rp, _, e, inside = step(p, g, m, lr, beta, True, decay, scale, 1.0)
+    raws = [torch.full((n + 128,), 7.0, device="cuda", dtype=dtype) for dtype in (F32, BF16)]
+    q, c = (raw[64:64 + n].view(shape) for raw in raws)
+    q.copy_(p)
+    fq.fp8q_muon(q, g, m, lr=lr, beta=beta, weight_decay=decay, scale=scale, copy=c)
+    off = (q.double() - rp).flatten(-2).norm(dim=-1)
+    size = 2.0 ** -24 * (4 * rp.flatten(-2).norm(dim=-1) + 8 * lr * scale * e.flatten(-2).norm(dim=-1))
+    assert (off <= lr * scale * inside + size).all()
+    # an element's error is a part of its matrix's
+    assert ((q.double() - rp).abs().flatten(-2).amax(dim=-1) <= lr * scale * inside + size).all()
+    assert torch.equal(c, q.bfloat16())
+    for raw in raws:
+        assert (raw[:64] == 7).all() and (raw[64 + n:] == 7).all()
+
+
 def test_muon_default_scale_and_device_lr():
     shape = (40, 100)
     p0, m0, g = matrices(shape, "normal", F32, 1), matrices(shape, "normal", F32, 2), matrices(shape, "normal", F32, 3)
