@@ -679,7 +679,8 @@ void for_experts(int64_t E, F f) {
     f(integral_constant<int, 64>{}, integral_constant<int, 16>{});
 }
 
-// Threads of a workgroup and workgroups per sequence of S tokens.
+// Threads of a workgroup and workgroups per sequence of S tokens: one at the least, which writes the counts, the slope and the
+// sums of a sequence without tokens too.
 void route_grid(int64_t S, int64_t E, int &threads, int64_t &groups) {
   const int lanes = E <= 256 ? 16 : 64;
   const int64_t needed = (S * lanes + 63) / 64 * 64;
@@ -688,6 +689,7 @@ void route_grid(int64_t S, int64_t E, int &threads, int64_t &groups) {
   const int64_t at_once = threads / lanes;
   groups = (S + at_once - 1) / at_once;
   if (groups > kRouteGroups) groups = kRouteGroups;
+  if (groups == 0) groups = 1;
 }
 
 }  // namespace
@@ -710,7 +712,7 @@ hipError_t launch_moe_route(const void *logits, bool f32, int64_t B, int64_t S, 
   RouteArgs a = {logits, bias,  valid, ids, w, counts, loss, slope, reinterpret_cast<uint32_t *>(ws),
                  reinterpret_cast<double *>(ws + kHead), reinterpret_cast<float *>(ws + kHead + 8 * B * columns),
                  B, S, static_cast<int>(E), static_cast<int>(k), normalize, scale, balance};
-  const dim3 grid(static_cast<uint32_t>(groups > 0 ? groups : 1), static_cast<uint32_t>(B)), block(threads);
+  const dim3 grid(static_cast<uint32_t>(groups), static_cast<uint32_t>(B)), block(threads);
   for_experts(E, [&](auto lanes, auto values) {
     auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, a); };
     constexpr int kL = decltype(lanes)::value, kV = decltype(values)::value;
