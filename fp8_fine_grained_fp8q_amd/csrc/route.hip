@@ -19,6 +19,9 @@
 // that follow each other are nearer than their errors; then the chosen ones and those beside the last of them are
 // ranked by their 64-bit scores (about one token in 500 with sigmoid scores).
 //
+// Sigmoid scores of a token may all lie below FP32's range.  Normalized weights and shares p are therefore formed
+// from scores times e^-m, with m the largest logit, of the chosen ones or of all, and at most 0.
+//
 // A group of 16 lanes takes a token of up to 256 experts, 64 lanes one of up to 1024, 4 to 16
 // logits per lane in registers: the maxima of a top-k step are 4 DPP steps inside a row of lanes, and
 // one instruction works for 4 tokens.  Logits are read once (16 MB for 16384 tokens x 256 experts,
@@ -161,6 +164,21 @@ __device__ __forceinline__ void scores(const float (&z)[kV], float (&s)[kV], flo
   for (int v = 0; v < kV; ++v) {
     float rest;
     s[v] = kSoftmax ? exp_of(z[v] - top) : sigmoid(z[v], rest);
+    sum += s[v];
+  }
+  sum = across<kLanes>(sum, Add{});
+}
+
+// Sigmoid scores and their sum times e^-min(top, 0) in place of those of `scores`: tokens whose scores are all below FP32's
+// range keep their shares p = s / sum s.  The same bits where top >= 0, and called only where a token of the wave has
+// another one: a second exponential per logit.
+template <int kLanes, int kV>
+__device__ __forceinline__ void raise_scores(const float (&z)[kV], float top, float (&s)[kV], float &sum) {
+  const float m = fminf(top, 0.0f);
+  sum = 0.0f;
+#pragma unroll
+  for (int v = 0; v < kV; ++v) {
+    s[v] = exp_of(fminf(z[v], 0.0f) - m) * reciprocal(1.0f + exp_of(-fabsf(z[v])));
     sum += s[v];
   }
   sum = across<kLanes>(sum, Add{});
@@ -319,13 +337,18 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(const RouteArg
     if (here) load_logits<kLanes, kV, kF32>(a.logits, row, E, l, z);
     scores<kLanes, kV, kSoftmax>(z, s, sum, top);
     here = here && top > -INFINITY;
-    const float r = 1.0f / sum;
+    float r = 1.0f / sum;
     {
       double key[kV];
 #pragma unroll
       for (int v = 0; v < kV; ++v)
         key[v] = pack(a.bias == nullptr || z[v] == -INFINITY ? z[v] : (kSoftmax ? s[v] * r : s[v]) + bias[v],
                       expert_of<kLanes>(l, v));
+      if constexpr (!kSoftmax)  // the keys are packed: from here on s is for the shares
+        if (__any(here && top < 0.0f)) {
+          raise_scores<kLanes, kV>(z, top, s, sum);
+          r = 1.0f / sum;
+        }
       // A sigmoid in FP32 is off by less than 2^-21.5 of itself, a softmax by 2^-24 (12 + |z - top|), their sums with
       // the bias by 2^-24: 2^-19 and 2^-17 cover two of them, the latter down to scores of e^-50, and the
       // floor covers the smaller ones.  Scores end at 1, so a far larger bias (an expert's mask) adds nothing to it.
@@ -594,6 +617,8 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_backward_kernel(const
     for (int v = 0; v < kV; ++v) z[v] = -INFINITY;
     if (here) load_logits<kLanes, kV, kF32>(a.logits, row, E, l, z);
     scores<kLanes, kV, kSoftmax>(z, s, sum, top);
+    if constexpr (!kSoftmax)
+      if (__any(here && top < 0.0f)) raise_scores<kLanes, kV>(z, top, s, sum);
     const float r = 1.0f / sum;
 
     float w[kSlots], dw[kSlots], dot = 0.0f;

@@ -519,7 +519,9 @@ enum { FP8Q_SCORE_SOFTMAX = 0, FP8Q_SCORE_SIGMOID = 1 };
  *   counts[b][e] : tokens of sequence b with expert e among their k
  *   slope[b][e] = balance / B * E counts[b][e] / (n_b sum_e counts[b][e]), n_b the sequence's tokens
  *   loss = sum over b, e of slope[b][e] * (sum over the tokens of p_e),  p = s / sum_e s_e
- * so that slope is the loss's derivative by each p_e, with the counts held fixed.
+ * so that slope is the loss's derivative by each p_e, with the counts held fixed.  Normalized weights and shares p are
+ * formed relative to the token's largest score, so they hold where all of its scores lie below FP32's range; single
+ * weights, and shares, below FP32's normal range (1.2e-38) are 0.
  *   logits : [B][S][E] BF16 or FP32 per dtype, finite or -inf (otherwise the token's weights, the
  *            sequence's slope and the loss are unspecified; ids stay below E); an expert with logit -inf
  *            is not chosen, slots left over get id -1 and weight 0
