@@ -18,8 +18,11 @@
 // E4M3 (behind those the products' own 11 bits lose more, and FP16 would be another byte per element to read and
 // write each step), the diagonal of A in FP32 apart from A, whose own is zero, and that of C in FP32 beside its rounded one.
 // The products see hi and 11 bits of what is off the diagonal; lo and the diagonal's rest come in with FP32
-// factors afterwards (muon_apply_kernel).  Result: 1e-4 to 9e-4 of its norm off (normal, rank-1 and rank-16
-// matrices with noise), less than the rounding to BF16 (1.7e-3).
+// factors afterwards (muon_apply_kernel).  Result, off by, of its norm (a model of these roundings in 64 bits): smaller side
+// 128 and more, 1e-4 to 9e-4 (normal, a few strong directions over noise, down to singular values of 1/500 of the norm),
+// less than the rounding to BF16 (1.7e-3), and up to 6e-3 with a floor of 1/10000.  What is off the diagonals of A and C
+// averages out over fewer elements below that: 64, 3e-3; 16, 2e-2; 8, 3e-2 at worst (one direction over a floor of 1/500;
+// normal ones 1e-3, 2e-3 and 4e-3), against 1e-6 to 5e-5 with FP32 throughout.
 //
 // What bounds it.  Large: the matrix cores at the clock that the power limit leaves.  32 x 7168 x 2048 in 17.6 ms:
 // C X 1.78 ms (1.08 PFLOP/s), of which the sums alone take 1.35 (1.41, what a large library product reaches) and

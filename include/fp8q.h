@@ -564,9 +564,12 @@ fp8q_status fp8q_moe_route_backward(const void *logits, int32_t dtype, int64_t B
  *   X = U / |U|_F;  A = X X^T,  X = (a I + b A + c A^2) X.
  * (This library's reading of a training step's optimizer; the pages name none for matrices.)
  * X, A and C = a I + b A + c A^2 are multiplied as FP16 with FP32 sums (11 significant bits of what is off the
- * diagonals; the diagonals in FP32, X itself kept in 15 bits): the result is off by 1e-4 to 1e-3 of its norm, up to 4e-3
- * where singular values lie a factor of 500 and more below the norm.  |U|_F is summed in 64 bits.  Coefficients must
- * keep every singular value below 15 in between (those here keep them below 1.3), or the result is not finite.
+ * diagonals; the diagonals in FP32, X itself kept in 15 bits).  These roundings average out over the smaller side,
+ * m = min(P, Q).  With the usual coefficients and 5 steps the result is off by
+ *   m >= 128 : up to 1e-3 of its norm, 7e-3 where singular values lie more than a factor of 500 below |U|_F;
+ *   m < 128  : up to max(1e-3, 0.3 / m) of its norm (8: 4e-2, 64: 5e-3; matrices of noise, or of a few strong directions over
+ *              it, a tenth to a quarter of that), with singular values as far below up to max(7e-3, min(0.1, 1 / m)).
+ * |U|_F is summed in 64 bits.  Coefficients must keep every singular value below 15 in between (those here keep them below 1.3), or the result is not finite.
  * U is finite; a matrix of zeros gives zeros.
  *   ns : HOST struct, read during the call only; 1 <= steps <= 100; usual: {3.4445, -4.7750, 2.0315, 5}
  *   workspace : fp8q_muon_workspace(G, P, Q) bytes: about 5 per element of the matrices (their sizes rounded up to
