@@ -59,6 +59,7 @@ bool bad_route(int64_t B, int64_t S, int64_t E, int64_t k) {
 // Shared checks of Muon's matrices [G][P][Q] and of its Newton-Schulz products.
 constexpr int64_t kMaxMuonSize = int64_t(1) << 20;
 constexpr int64_t kMaxMuonSteps = 100;
+constexpr double kMaxMuonA = 15.99;  // a is C's diagonal where a matrix has nothing (its padding too), FP16 at a scale of 4096
 
 bool bad_matrices(int64_t G, int64_t P, int64_t Q) {
   return G < 1 || bad_dim(G) || P < 0 || P > kMaxMuonSize || Q < 0 || Q > kMaxMuonSize || too_many(G * 64, P * Q) ||
@@ -66,7 +67,7 @@ bool bad_matrices(int64_t G, int64_t P, int64_t Q) {
 }
 
 bool bad_newton_schulz(const fp8q_newton_schulz &ns) {
-  return !f32_number(ns.a) || !f32_number(ns.b) || !f32_number(ns.c) || ns.steps < 1 || ns.steps > kMaxMuonSteps;
+  return !f32_number(ns.a) || fabs(ns.a) > kMaxMuonA || !f32_number(ns.b) || !f32_number(ns.c) || ns.steps < 1 || ns.steps > kMaxMuonSteps;
 }
 
 // Shared checks of the two GEMM entry points (everything except the grouped extras).
@@ -520,7 +521,7 @@ const char *fp8q_status_string(fp8q_status status) {
     case FP8Q_ERR_DEVICE: return "no usable HIP device";
     case FP8Q_ERR_LAUNCH: return "kernel launch failed";
     case FP8Q_ERR_OFFSETS: return "grouped GEMM offsets invalid (offsets[0] != 0, decreasing, or offsets[G] != M_tot)";
-    case FP8Q_ERR_VALUE: return "hyperparameter out of range (not a finite FP32 number, beta outside [0, 1), eps < 0, a step count out of range, a router's scale <= 0, or lr / (1 - beta1^step) or lr * weight_decay past FP32)";
+    case FP8Q_ERR_VALUE: return "hyperparameter out of range (not a finite FP32 number, beta outside [0, 1), eps < 0, a step count out of range, a router's scale <= 0, |a| of Newton-Schulz products above 15.99, or lr / (1 - beta1^step) or lr * weight_decay past FP32)";
     default: return "unknown status";
   }
 }

@@ -11,8 +11,8 @@
 // 2 (m^2 n / 2 + m^3 / 2 + m^2 n) flops each = 2.1e12 in all.  X stays in the orientation of the matrix, once: the
 // product that contracts over its columns reads it by rows, the other by columns (LDS's transposing reads).
 //
-// Numerics.  FP16 has 11 significant bits, three more than BF16, and its range is no matter: |X|_2 stays
-// below 1.3 and operands are scaled by 2^12.  Rounding X itself to 11 bits would drown the small singular
+// Numerics.  FP16 has 11 significant bits, three more than BF16, and its range is no matter with the usual coefficients:
+// |X|_2 stays below 1.3 and operands are scaled by 2^12 (others: |X|_2 below 5.65, |C|_2 below 15.99).  Rounding X itself to 11 bits would drown the small singular
 // values beside strong directions (a rank-1 matrix with a floor of noise: 1e-2 of the result's norm), as
 // would rounding a + b A_ii + ..., where the terms cancel.  So X is kept in 15 bits, hi in FP16 and the rest lo in
 // E4M3 (behind those the products' own 11 bits lose more, and FP16 would be another byte per element to read and

@@ -569,9 +569,12 @@ fp8q_status fp8q_moe_route_backward(const void *logits, int32_t dtype, int64_t B
  *   m >= 128 : up to 1e-3 of its norm, 7e-3 where singular values lie more than a factor of 500 below |U|_F;
  *   m < 128  : up to max(1e-3, 0.3 / m) of its norm (8: 4e-2, 64: 5e-3; matrices of noise, or of a few strong directions over
  *              it, a tenth to a quarter of that), with singular values as far below up to max(7e-3, min(0.1, 1 / m)).
- * |U|_F is summed in 64 bits.  Coefficients must keep every singular value below 15 in between (those here keep them below 1.3), or the result is not finite.
+ * |U|_F is summed in 64 bits.  FP16 holds A and C off their diagonals, and C on it, up to 15.99: coefficients must keep the
+ * singular values s of every X that enters a step below 5.65 (A_ij reaches s^2 / 2) and |a + b s^2 + c s^4| below 15.99 from
+ * s = 0 to the largest (|a| is checked), or the result is not finite.  Those here keep s below 1.3.  X has its 15 bits while its
+ * elements are below 1, and 12 at the least beyond.
  * U is finite; a matrix of zeros gives zeros.
- *   ns : HOST struct, read during the call only; 1 <= steps <= 100; usual: {3.4445, -4.7750, 2.0315, 5}
+ *   ns : HOST struct, read during the call only; 1 <= steps <= 100, |a| <= 15.99; usual: {3.4445, -4.7750, 2.0315, 5}
  *   workspace : fp8q_muon_workspace(G, P, Q) bytes: about 5 per element of the matrices (their sizes rounded up to
  *               128) and 4 per element of the G square matrices of the smaller size (few long ones: and up to 4 MB
  *               for the parts of A); written
