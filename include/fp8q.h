@@ -479,8 +479,10 @@ fp8q_status fp8q_adamw(const fp8q_adamw_tensor *tensors, int64_t count, int32_t 
  *   x : [T][H] in x_dtype;  weight : [H] FP32;  bias : [H] FP32 or NULL
  *   y : [T][H] in out_dtype (out);  rstd : [T] FP32 (out);  mean : [T] FP32 (out; center == 0: not written,
  *       may be NULL)
- * Requires H % 8 == 0, 8 <= H <= 16384, eps >= 0.  T == 0 is a no-op.  Values whose squares FP32 does not hold
- * (above about 1e19) give y = 0.
+ * Requires H % 8 == 0, 8 <= H <= 16384, eps >= 0.  T == 0 is a no-op.  A row whose sum of squares FP32 does not hold
+ * (values above about 1e19 / sqrt(H)) has rstd = 0 and y = bias, or 0 without one; where the sum of its values is too large
+ * too (center), mean is infinite and y NaN.  With eps == 0 rows whose squares all vanish in FP32 (values, or their distances
+ * from the mean, below about 1e-23) have rstd infinite and y not finite.
  * Errors: FP8Q_ERR_DTYPE, FP8Q_ERR_SHAPE, FP8Q_ERR_VALUE, FP8Q_ERR_NULL, FP8Q_ERR_ALIGN (mean and rstd 4-byte),
  * FP8Q_ERR_DEVICE, FP8Q_ERR_LAUNCH.
  */
@@ -492,7 +494,8 @@ fp8q_status fp8q_layer_norm(const void *x, int32_t x_dtype, const float *weight,
  * Gradients of fp8q_layer_norm, with h = (x - mean) rstd and g = dy weight:
  *   dx = rstd (g - sum g / H - h sum g h / H)   (RMS norm: without sum g / H),
  *   dweight = sum over rows of dy h,  dbias = sum over rows of dy.
- * Sums in FP32 in an order that only the sizes decide (the same inputs give the same bits).
+ * Sums in FP32 in an order that only the sizes decide (the same inputs give the same bits); those of dweight and dbias add
+ * up T / 256 rows one after the other, then 256 such sums.
  *   dy, x : [T][H] in dy_dtype, x_dtype;  mean, rstd : [T] as written by fp8q_layer_norm (mean NULL: RMS norm)
  *   dx : [T][H] in out_dtype (out);  dweight : [H] FP32 (out);  dbias : [H] FP32 (out) or NULL
  *   workspace : fp8q_layer_norm_backward_workspace(T, H) bytes (8 H per 4 rows, at most 2048 H), written
