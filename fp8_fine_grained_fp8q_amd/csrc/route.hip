@@ -8,7 +8,7 @@
 // s + bias (of z without a bias: both scores rise with z), ties to the lower index; an expert with
 // logit -inf is never chosen.  Weights w_j = scale s_j (softmax, sigmoid), or normalized over the
 // chosen ones, w_j = scale s_j / sum_i s_i.  With p = s / sum_e s_e, a sequence's counts c_e and its
-// n tokens (valid ones with a finite logit), and B sequences,
+// n tokens (valid ones with an expert), and B sequences,
 //   slope_e = balance / B * E c_e / (n sum_e c_e),  loss = sum over sequences and e of slope_e sum_t p_te,
 // so slope is the loss's derivative by every p_te of the sequence.  Backward, with g = dloss slope
 // and d_j = dw_j w_j (normalized: w_j (dw_j - sum_i w_i dw_i / scale), a softmax over the chosen):
@@ -424,6 +424,7 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(const RouteArg
       }
     }
     wave_sync();
+    here = here && ids[0] >= 0;  // without an expert (the bias masks those that the logits leave) a token counts for nothing
     if (here) {
       if (l == 0) ++tokens;
 #pragma unroll

@@ -529,8 +529,8 @@ enum { FP8Q_SCORE_SOFTMAX = 0, FP8Q_SCORE_SIGMOID = 1 };
  *            sequence's slope and the loss are unspecified; ids stay below E); an expert with logit -inf
  *            is not chosen, slots left over get id -1 and weight 0
  *   bias : [E] FP32, finite or -inf (such an expert is not chosen), or NULL;  valid : [B][S] bytes, 0 for a token that does not count, or NULL
- *          A token that does not count, or whose logits are all -inf, gets ids -1 and weights 0 and
- *          enters neither counts nor loss; its logits are not used (they may be NaN).
+ *          A token that does not count, or that has no expert (each has logit or bias -inf), gets ids -1 and weights 0
+ *          and enters neither counts, n_b nor loss; the logits of one that does not count are not used (they may be NaN).
  *   topk_ids int32, topk_weights FP32 : [B][S][k] (out);  counts int32, slope FP32 : [B][E] (out);  loss : FP32 (out)
  *   workspace : fp8q_moe_route_workspace(B, S, E) bytes, written
  * Requires 1 <= E <= 1024, 1 <= k <= min(E, 64), 1 <= B <= 65535, B S k < 2^31, scale > 0 (it and its reciprocal
