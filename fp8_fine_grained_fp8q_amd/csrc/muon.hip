@@ -24,12 +24,14 @@
 // averages out over fewer elements below that: 64, 3e-3; 16, 2e-2; 8, 3e-2 at worst (one direction over a floor of 1/500;
 // normal ones 1e-3, 2e-3 and 4e-3), against 1e-6 to 5e-5 with FP32 throughout.
 //
-// What bounds it.  Large: the matrix cores at the clock that the power limit leaves.  32 x 7168 x 2048 in 17.6 ms:
+// What bounds it.  Large: the matrix cores at the clock that the power limit leaves, and CUs that the last round of
+// tiles leaves idle (C X of 4096 x 7168: 448 tiles on 256 CUs).  32 x 7168 x 2048 in 17.4 to 17.9 ms:
 // C X 1.78 ms (1.08 PFLOP/s), of which the sums alone take 1.35 (1.41, what a large library product reaches) and
-// lo, the factors and the stores the rest; A 0.88, C 0.34, momentum and norm 0.91 (HBM), first X 0.80, the last
-// C X with the parameters 2.39.  Reading lo after the products (1.89), storing hi without LDS (1.89), starting the
-// CUs apart (no gain) and lo and hi by buffer addresses (1.80) did not help.  Small: the launches, each 4 to
-// 9 us and none able to start before the one before it has ended.
+// lo, the factors and the stores the rest (its instance for wide matrices spills 20 bytes per thread); A 0.93, C 0.34,
+// momentum and norm 0.95 (HBM), first X 0.79, which reads gradient and momentum again, the last C X with the parameters
+// 2.41.  Reading lo after the products (1.89), storing hi without LDS (1.89), starting the CUs apart (no gain) and lo and
+// hi by buffer addresses (1.80) did not help.  Small: the launches, each 4 to 9 us and none able to start before the one
+// before it has ended.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>

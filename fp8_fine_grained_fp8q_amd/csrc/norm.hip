@@ -6,14 +6,19 @@
 //   g = dy w,  dx = rstd (g - sum g / H - h sum g h / H)  (RMS norm: without sum g),
 //   dw = sum over rows of dy h,  db = sum over rows of dy.
 //
-// Bound by HBM: x in and y out, or x and dy in and dx out.  A row stays in the registers of one
-// workgroup (8 columns per thread, or 16 of more than 8192), so x is read once and the squares are those
+// Bound by HBM from about 4096 columns on: x in and y out, or x and dy in and dx out.  A row stays in the registers of
+// one workgroup (8 columns per thread, or 16 of more than 8192), so x is read once and the squares are those
 // of x - mean.  Workgroups take every gridDim.x-th row and load the next one before they sum this
 // one; the weights stay in registers too.  All sums are FP32, in an order that depends on the sizes
 // only, with one rounding of each result.
 //
 // 16384 x 7168 from FP32 to BF16: 133 us, 5.3 TB/s (a copy kernel of this card's best 6.16 TB/s: 114).  Gradient of
 // 8192 x 7168 in BF16: 61 us, 5.7 TB/s (with one row on its way and cached loads 80), and 5 us for the sums.
+// Narrow rows are bound by the steps of a workgroup's rows, one row at a time (whole calls, BF16, copy's floor in
+// brackets): 8192 x 1024 12 us (5) and gradient 28 us (8), 8192 x 256 11 (1.4) and 20 (2), 2^20 x 128 293 (87) and 1860
+// (131): the gradient has kNormGroups workgroups whatever their size, of one wave each up to 512 columns.  Rows above 8192
+// cost the gradient registers: 16 columns per thread of x, dy, their next rows, weights and sums spill 56 to 268 bytes of
+// scratch per thread; 4096 x 16384 105 us in BF16 (65), 402 in FP32 (131).
 //
 // dw and db: every workgroup of the backward kernel keeps its rows' sums in registers and leaves
 // them in the workspace, 4 H bytes each; a second kernel adds up at most kNormGroups of them.

@@ -25,8 +25,11 @@
 // A group of 16 lanes takes a token of up to 256 experts, 64 lanes one of up to 1024, 4 to 16
 // logits per lane in registers: the maxima of a top-k step are 4 DPP steps inside a row of lanes, and
 // one instruction works for 4 tokens.  Logits are read once (16 MB for 16384 tokens x 256 experts,
-// 3 us of HBM time), so the top-k's instructions bound the call: 32 us there with sigmoid scores and a bias, of
-// which the 64 tokens of a small batch take 14.6.  With all 256 experts ranked in 64 bits for the tokens that
+// 3 us of HBM time).  What bounds the call is the time of one token: k maxima that follow each other over FP64 keys, the
+// exponentials and the ways through LDS, 14.7 us for 64 tokens with sigmoid scores and a bias.  The
+// instance for 256 experts takes 184 registers and 58 KB of LDS, one workgroup of 512 threads per CU, so that 16384 tokens in
+// four sequences are 512 workgroups in two rounds of it: 31 us (fewer registers by launch bounds were slower).  512 and 1024
+// experts, 16384 tokens: 90 and 94 us for the whole call.  With all 256 experts ranked in 64 bits for the tokens that
 // FP32 leaves open it took 41.  Counts and sums of p stay in a workgroup's LDS and registers; a second launch
 // (4 to 7 us) adds them up to slope and loss.
 // The gradient reads and writes 33 MB in 14 us.
@@ -192,8 +195,8 @@ __device__ __forceinline__ void wave_sync() {
 }
 
 // Keys of the top-k with their expert, as one number that sorts by the key and then by the lower index: an FP32
-// number as FP64 has 29 zero bits at its end, and FP64 maxima are as fast as FP32 ones.  Keys of -inf (and NaN)
-// lie below kNone and are never chosen.
+// number as FP64 has 29 zero bits at its end, so that one maximum finds both.  Keys of -inf (and NaN) lie below kNone
+// and are never chosen.
 constexpr double kNone = -0x1p200, kLowest = -0x1p210;
 
 __device__ __forceinline__ double pack(float key, int expert) {
