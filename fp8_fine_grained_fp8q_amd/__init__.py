@@ -829,7 +829,8 @@ def fp8q_moe_route(logits: torch.Tensor, k: int, bias: torch.Tensor | None = Non
     [.., S, k], topk_weights float32 [.., S, k], counts int32 [.., E], loss float32 [1], slope float32
     [.., E]).  Chosen by score + bias (float32 [E]); weights scale * score, normalized over the chosen ones;
     loss = balance * the mean over the sequences of E sum_e (share of the slots)_e (mean of p_e), slope its
-    derivative by each p.  Tokens with valid (bool [.., S]) False get ids -1 and weights 0 and do not count."""
+    derivative by each p.  Tokens with valid (bool [.., S]) False, or whose experts all have logit or bias -inf, get ids -1
+    and weights 0 and do not count."""
     if stream is not None:
         with _on(stream):
             return fp8q_moe_route(logits, k, bias, valid, score, normalize, scale, balance)
